@@ -463,6 +463,163 @@ lora_status mlp_backward(const mlp_shape* shape, const uint16_t* dy, const uint1
                          float* ddown_pack, int accumulate, uint16_t* trace, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* ---- RMS norm with the residual's addition --------------------------- */
+
+/* The norm in front of a projection, with the residual stream's addition:
+ *   h_t = bf16(x_t + residual_t)          (residual NULL: h_t = x_t)
+ *   rstd_t = 1 / sqrt(mean_j h_tj^2 + eps)
+ *   y_tj = bf16(h_tj rstd_t weight_j)     (fp32 throughout, rounded once)
+ *   x, residual bf16 [n][hidden]; weight bf16 [hidden]
+ *   h     bf16 [n][hidden] out  the new residual stream, kept for the backward;
+ *                               NULL exactly when residual is NULL (the
+ *                               backward then takes x).  h may be x or residual.
+ *   y     bf16 [n][hidden] out  may be x
+ *   rstd  fp32 [n] out, nullable; kept for the backward
+ * A row's result depends on that row alone, not on n.  The sum of squares is
+ * fp32: a row whose squares overflow it (|h| beyond ~1e19) gives zeros, and
+ * non-finite h propagates per IEEE 754.  0 <= n < 2^30, 1 <= hidden <= 32768
+ * (multiples of 8 run on 16-byte accesses); x, residual, weight, h and y
+ * 16-byte aligned. */
+lora_status rmsnorm_forward(int64_t n, int64_t hidden, const uint16_t* x, const uint16_t* residual,
+                            const uint16_t* weight, float eps, uint16_t* h, uint16_t* y,
+                            float* rstd, void* stream);
+
+/* The same norm with its output in 8 bits, each 32 columns with one scale:
+ *   v_tj = h_tj rstd_t weight_j (fp32, not rounded to bf16 first);
+ *   per block b of 32 columns, 2^e with e the least integer for which
+ *   max |v| <= 448 2^e over the block's finite v (e >= -126): no value saturates;
+ *   q_tj = e4m3(v_tj 2^-e), rounded to nearest even; NaN and +-Inf give the
+ *   NaN code.
+ *   q        uint8 [n][hidden] out     OCP e4m3 codes
+ *   q_scales uint8 [n][hidden/32] out  e + 127 (E8M0)
+ * This is the x that w4_linear and lora_forward_w4 take with x_scales.
+ * hidden a multiple of 32; the rest as rmsnorm_forward. */
+lora_status rmsnorm_forward_q8(int64_t n, int64_t hidden, const uint16_t* x,
+                               const uint16_t* residual, const uint16_t* weight, float eps,
+                               uint16_t* h, uint8_t* q, uint8_t* q_scales, float* rstd,
+                               void* stream);
+
+/* Backward for dy = dL/dy and, through the residual stream, dh = dL/dh
+ * (nullable).  With xh = h rstd and g = dy weight:
+ *   dx = bf16(dh + rstd (g - xh mean_j(g xh)))
+ * is the gradient of x and of residual alike, and
+ *   dweight_j = sum_t dy_tj xh_tj  (fp32 [hidden], nullable: a frozen weight;
+ *   accumulate != 0 adds into it, 0 overwrites it, with zeros for n = 0).
+ *   dy, dh, h bf16 [n][hidden]; rstd fp32 [n] from the forward
+ *   dx bf16 [n][hidden] out, may be dy or dh
+ * dweight is summed in a fixed order: results are bitwise repeatable.
+ * Workspace: needed only with dweight (else ws may be NULL). */
+size_t rmsnorm_backward_workspace_bytes(int64_t n, int64_t hidden);
+lora_status rmsnorm_backward(int64_t n, int64_t hidden, const uint16_t* dy, const uint16_t* dh,
+                             const uint16_t* h, const uint16_t* weight, const float* rstd,
+                             uint16_t* dx, float* dweight, int accumulate, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* ---- few-token products with 4-bit weights ---------------------------- */
+
+/* The frozen weight in 4 bits with one scale per 32 input columns:
+ *   W_ik = e2m1(code_ik) 2^(scale_{i, k/32} - 127)
+ *   codes  uint8 [d_out][d_in/2]   k even in the low nibble, k odd in the high;
+ *                                  a code is sign, 2 exponent bits, 1 fraction
+ *                                  bit: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}
+ *   scales uint8 [d_out][d_in/32]  E8M0 (255 is NaN)
+ * w4_quantize lays a bf16 W [d_out][d_in] out so, once per frozen matrix: per
+ * 32 weights the least power of two (2^-126 or more) with max |w| <= 6 scale,
+ * codes to nearest, ties to the even code.  W must be finite (NaN becomes 0 and
+ * +-Inf +-6 scale).  d_in, d_out multiples of 64, <= 2^20; W, codes 16-byte
+ * aligned. */
+lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t* codes,
+                        uint8_t* scales, void* stream);
+
+#define LORA_W4_MAX_TOKENS 256   /* decoding batches; larger ones run lora_forward */
+
+/* y_t = bf16(W x_t) for 0 <= n <= LORA_W4_MAX_TOKENS tokens, summed in fp32 and
+ * rounded once: projections without adapters, and the lm_head's logits of a
+ * decoding step.
+ *   x  bf16 [n][d_in] with x_scales NULL; or e4m3 codes uint8 [n][d_in] with
+ *      x_scales uint8 [n][d_in/32] (E8M0), as rmsnorm_forward_q8 writes them
+ *   y  bf16 [n][d_out] out
+ * d_in, d_out multiples of 64, <= 2^20; x, codes, y 16-byte aligned. */
+lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
+                      const uint8_t* x_scales, const uint8_t* codes, const uint8_t* scales,
+                      uint16_t* y, void* stream);
+
+/* lora_forward for decoding batches on a 4-bit base:
+ *   y_t = bf16(W x_t + s_a B_a (A_a x_t)),   a = adapter_ids[t],
+ * the base product, s_a A_a x_t and the delta in fp32, rounded once.  Shape,
+ * packs, descriptors, ids (sorted or not), their device checks and flags as for
+ * lora_forward: a token with an invalid id or an inactive adapter gets the base
+ * output.  x and x_scales, codes and scales as for w4_linear;
+ * n_tokens <= LORA_W4_MAX_TOKENS.  Workspace:
+ * lora_forward_w4_workspace_bytes(shape); word 0 is the status word. */
+size_t lora_forward_w4_workspace_bytes(const lora_shape* shape);
+lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_t* x_scales,
+                            const uint8_t* codes, const uint8_t* scales, const uint16_t* A_pack,
+                            const uint16_t* B_pack, const lora_adapter_desc* desc,
+                            const int32_t* adapter_ids, uint16_t* y, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* ---- gradient norms, clipping ----------------------------------------- */
+
+/* An adapter's gradient lies in many tensors (A and B of every projection and
+ * layer) of one flat fp32 buffer.  A table built once says which belong to
+ * which group (adapter):
+ *   device array of n_tensors entries, sorted by group; tensors must not
+ *   overlap; first_chunk_0 = 0 and first_chunk_{i+1} = first_chunk_i +
+ *   ceil(count_i / LORA_GRAD_CHUNK); n_chunks is the sum over all entries.
+ * Elements outside every tensor are never touched.  An entry that breaks these
+ * rules is never used as an address beyond n_elems: its chunks are left out and
+ * LORA_FLAG_BAD_DESC is set (what the groups of such a table give is undefined). */
+#define LORA_GRAD_CHUNK 8192
+typedef struct {
+  int64_t offset;       /* first element in the flat buffer */
+  int64_t count;        /* elements, >= 0 */
+  int32_t group;        /* 0 .. n_groups - 1 */
+  int32_t first_chunk;
+} grad_tensor;
+
+typedef struct {        /* host struct */
+  int64_t n_elems;      /* elements of the flat buffers, <= 2^42 */
+  int32_t n_chunks;     /* 0 .. 2^24 - 1 */
+  int32_t n_tensors;    /* 0 .. 2^24 */
+  int32_t n_groups;     /* 1 .. 16384 */
+  int32_t reserved;     /* must be 0 */
+} grad_shape;
+
+/* Workspace of the three calls below; word 0 is the status word.  0 on an
+ * invalid shape. */
+size_t grad_workspace_bytes(const grad_shape* shape);
+
+/* norms[a] = sqrt(sum of g^2 over group a's tensors), fp32 [n_groups] out,
+ * summed in 64 bits in a fixed order (bitwise repeatable).  A group whose
+ * gradient holds NaN or +-Inf has a NaN or infinite norm and sets
+ * LORA_FLAG_NONFINITE_GRAD; a group without tensors has norm 0. */
+lora_status grad_norm(const grad_shape* shape, const grad_tensor* table, const float* g,
+                      float* norms, void* ws, size_t ws_bytes, void* stream);
+
+/* g_out = g min(1, max_norm / (norm + 1e-6)), each group by its own norm
+ * (max_norm >= 0, +Inf: no clipping).  g_out may be g.  A group with a
+ * non-finite gradient is copied as it is and LORA_FLAG_NONFINITE_GRAD set, so
+ * that adam_step_multi skips it.  norms (nullable): the norms before clipping. */
+lora_status grad_clip(const grad_shape* shape, const grad_tensor* table, const float* g,
+                      float max_norm, float* g_out, float* norms, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* grad_clip and one AdamW step per group in one call, without writing the
+ * clipped gradient: each element as in adam_step on min(1, max_norm / (norm +
+ * 1e-6)) g, the constants taken from the 64-bit lr, betas, eps and decay.  steps: DEVICE int64 [n_groups], the steps each group has made; the
+ * call makes step steps[a] + 1 and stores it, so a captured graph counts on with
+ * every replay.  A group with a non-finite gradient keeps p, m, v, its bf16 copy
+ * and its counter, and LORA_FLAG_NONFINITE_GRAD is set.  p, m, v updated in
+ * place, g read only, p_bf16 (nullable) receives bf16(p); norms (nullable) as
+ * for grad_clip. */
+lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table, int64_t* steps,
+                              float* p, const float* g, float* m, float* v, float max_norm,
+                              double lr, double beta1, double beta2, double eps,
+                              double weight_decay,
+                              uint16_t* p_bf16, float* norms, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* ---- forward without allocation ------------------------------------- */
 
 /* For callers that cannot allocate device memory or hand in a workspace: code

@@ -20,6 +20,9 @@ Modules
   loss      -- cross_entropy / importance_sampling / ppo / custom dLoss/dlogprob
   adam      -- per-adapter AdamW step
   mlp       -- dense SwiGLU MLP with LoRA on gate, up and down
+  norm      -- RMS norm with the residual's addition, its 8-bit output, its backward
+  w4        -- 4-bit weights with a scale per 32: rounding, values, the product
+  clip      -- per-adapter gradient norms over many tensors, clipping, AdamW on top
   moe       -- top-k routed expert layer with per-(expert, adapter) LoRA
 """
-from . import adam, logprob, lora, loss, mlp, moe, segments  # noqa: F401
+from . import adam, clip, logprob, lora, loss, mlp, moe, norm, segments, w4  # noqa: F401

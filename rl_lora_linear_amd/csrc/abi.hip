@@ -1100,6 +1100,217 @@ lora_status bf16_add(int64_t n, const uint16_t* a, const uint16_t* b, uint16_t* 
   return launch_add_bf16(n, a, b, out, S(stream));
 }
 
+// ------------------------------------------------------------------ RMS norm
+static lora_status norm_checks(int64_t n, int64_t hidden, const char* what) {
+  LORA_ARG_CHECK(n >= 0 && n <= INT32_MAX / 2, "%s: n %lld outside [0, 2^30)", what, (long long)n);
+  LORA_ARG_CHECK(hidden > 0, "%s: hidden must be positive", what);
+  if (hidden > 32768) {
+    set_error("%s: hidden %lld must be <= 32768", what, (long long)hidden);
+    return LORA_E_UNSUPPORTED;
+  }
+  return LORA_OK;
+}
+
+static lora_status norm_forward_checks(int64_t n, int64_t hidden, const uint16_t* x,
+                                       const uint16_t* residual, const uint16_t* weight, float eps,
+                                       uint16_t* h, const char* what) {
+  TRY(norm_checks(n, hidden, what));
+  LORA_ARG_CHECK(eps >= 0.f && std::isfinite(eps), "%s: eps must be finite and >= 0", what);
+  LORA_ARG_CHECK(weight && aligned16(weight), "%s: weight NULL or not 16-byte aligned", what);
+  LORA_ARG_CHECK((residual != nullptr) == (h != nullptr), "%s: residual and h go together", what);
+  LORA_ARG_CHECK(n == 0 || (x && aligned16(x)), "%s: x NULL or not 16-byte aligned", what);
+  LORA_ARG_CHECK(aligned16(residual) && aligned16(h), "%s: residual and h must be 16-byte aligned",
+                 what);
+  return LORA_OK;
+}
+
+lora_status rmsnorm_forward(int64_t n, int64_t hidden, const uint16_t* x, const uint16_t* residual,
+                            const uint16_t* weight, float eps, uint16_t* h, uint16_t* y,
+                            float* rstd, void* stream) {
+  TRY(norm_forward_checks(n, hidden, x, residual, weight, eps, h, "rmsnorm_forward"));
+  LORA_ARG_CHECK(n == 0 || (y && aligned16(y)), "rmsnorm_forward: y NULL or not 16-byte aligned");
+  if (n == 0) return LORA_OK;
+  return launch_rmsnorm_fwd(n, hidden, x, residual, weight, eps, h, y, nullptr, nullptr, rstd,
+                            S(stream));
+}
+
+lora_status rmsnorm_forward_q8(int64_t n, int64_t hidden, const uint16_t* x,
+                               const uint16_t* residual, const uint16_t* weight, float eps,
+                               uint16_t* h, uint8_t* q, uint8_t* q_scales, float* rstd,
+                               void* stream) {
+  TRY(norm_forward_checks(n, hidden, x, residual, weight, eps, h, "rmsnorm_forward_q8"));
+  LORA_ARG_CHECK(n == 0 || (q && q_scales && aligned16(q)),
+                 "rmsnorm_forward_q8: q or q_scales NULL, or q not 16-byte aligned");
+  if (hidden % 32) {
+    set_error("rmsnorm_forward_q8: hidden %lld must be a multiple of 32", (long long)hidden);
+    return LORA_E_UNSUPPORTED;
+  }
+  if (n == 0) return LORA_OK;
+  return launch_rmsnorm_fwd(n, hidden, x, residual, weight, eps, h, nullptr, q, q_scales, rstd,
+                            S(stream));
+}
+
+size_t rmsnorm_backward_workspace_bytes(int64_t n, int64_t hidden) {
+  if (norm_checks(n, hidden, "rmsnorm_backward") != LORA_OK) return 0;
+  return 256 + (size_t)rmsnorm_bwd_blocks(n, hidden) * hidden * sizeof(float);
+}
+
+lora_status rmsnorm_backward(int64_t n, int64_t hidden, const uint16_t* dy, const uint16_t* dh,
+                             const uint16_t* h, const uint16_t* weight, const float* rstd,
+                             uint16_t* dx, float* dweight, int accumulate, void* ws,
+                             size_t ws_bytes, void* stream) {
+  TRY(norm_checks(n, hidden, "rmsnorm_backward"));
+  LORA_ARG_CHECK(weight && aligned16(weight), "rmsnorm_backward: weight NULL or not 16-byte aligned");
+  LORA_ARG_CHECK(n == 0 || (dy && h && rstd && dx), "rmsnorm_backward: dy, h, rstd and dx must be non-NULL");
+  LORA_ARG_CHECK(aligned16(dy) && aligned16(dh) && aligned16(h) && aligned16(dx),
+                 "rmsnorm_backward: dy, dh, h and dx must be 16-byte aligned");
+  if (dweight && (!ws || ws_bytes < rmsnorm_backward_workspace_bytes(n, hidden))) {
+    set_error("rmsnorm_backward: workspace too small (need rmsnorm_backward_workspace_bytes(%lld, %lld))",
+              (long long)n, (long long)hidden);
+    return LORA_E_WORKSPACE;
+  }
+  if (n == 0 && !dweight) return LORA_OK;
+  return launch_rmsnorm_bwd(n, hidden, dy, dh, h, weight, rstd, dx, dweight, accumulate,
+                            dweight ? (float*)((char*)ws + 256) : nullptr, S(stream));
+}
+
+// ------------------------------------------------------------------ 4-bit weights
+static lora_status w4_dims(int64_t d_in, int64_t d_out, const char* what) {
+  LORA_ARG_CHECK(d_in > 0 && d_out > 0, "%s: d_in and d_out must be positive", what);
+  if (d_in % 64 || d_out % 64 || d_in > (1 << 20) || d_out > (1 << 20)) {
+    set_error("%s: d_in %lld and d_out %lld must be multiples of 64 and <= 2^20", what,
+              (long long)d_in, (long long)d_out);
+    return LORA_E_UNSUPPORTED;
+  }
+  return LORA_OK;
+}
+
+static lora_status w4_tokens(int64_t n, const char* what) {
+  LORA_ARG_CHECK(n >= 0, "%s: n must be >= 0", what);
+  if (n > LORA_W4_MAX_TOKENS) {
+    set_error("%s: %lld tokens, at most %d", what, (long long)n, LORA_W4_MAX_TOKENS);
+    return LORA_E_UNSUPPORTED;
+  }
+  return LORA_OK;
+}
+
+lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t* codes,
+                        uint8_t* scales, void* stream) {
+  TRY(w4_dims(d_in, d_out, "w4_quantize"));
+  LORA_ARG_CHECK(W && codes && scales, "w4_quantize: W, codes and scales must be non-NULL");
+  LORA_ARG_CHECK(aligned16(W) && aligned16(codes), "w4_quantize: W and codes must be 16-byte aligned");
+  return launch_w4_quantize(W, d_out, d_in, codes, scales, S(stream));
+}
+
+lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
+                      const uint8_t* x_scales, const uint8_t* codes, const uint8_t* scales,
+                      uint16_t* y, void* stream) {
+  TRY(w4_dims(d_in, d_out, "w4_linear"));
+  TRY(w4_tokens(n, "w4_linear"));
+  LORA_ARG_CHECK(codes && scales && aligned16(codes), "w4_linear: codes or scales NULL, or codes not 16-byte aligned");
+  LORA_ARG_CHECK(n == 0 || (x && y && aligned16(x) && aligned16(y)),
+                 "w4_linear: x or y NULL or not 16-byte aligned");
+  if (n == 0) return LORA_OK;
+  return launch_w4_linear(n, d_in, d_out, x, x_scales, codes, scales, y, S(stream));
+}
+
+size_t lora_forward_w4_workspace_bytes(const lora_shape* shape) {
+  if (check_shape(shape) != LORA_OK || w4_tokens(shape->n_tokens, "lora_forward_w4") != LORA_OK)
+    return 0;
+  return w4_ws_bytes(shape->n_tokens, shape->max_rank);
+}
+
+lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_t* x_scales,
+                            const uint8_t* codes, const uint8_t* scales, const uint16_t* A_pack,
+                            const uint16_t* B_pack, const lora_adapter_desc* desc,
+                            const int32_t* adapter_ids, uint16_t* y, void* ws, size_t ws_bytes,
+                            void* stream) {
+  TRY(check_shape(shape));
+  const lora_shape& sh = *shape;
+  TRY(w4_tokens(sh.n_tokens, "lora_forward_w4"));
+  LORA_ARG_CHECK(codes && scales && A_pack && B_pack && desc,
+                 "codes, scales, A_pack, B_pack and desc must be non-NULL");
+  LORA_ARG_CHECK(aligned16(codes) && aligned16(A_pack) && aligned16(B_pack),
+                 "codes and the packs must be 16-byte aligned");
+  LORA_ARG_CHECK(sh.n_tokens == 0 || (x && adapter_ids && y), "x, adapter_ids and y must be non-NULL");
+  LORA_ARG_CHECK(sh.n_tokens == 0 || (aligned16(x) && aligned16(y)), "x and y must be 16-byte aligned");
+  if (!ws || ws_bytes < w4_ws_bytes(sh.n_tokens, sh.max_rank)) {
+    set_error("lora_forward_w4: workspace %zu bytes < %zu needed", ws_bytes,
+              w4_ws_bytes(sh.n_tokens, sh.max_rank));
+    return LORA_E_WORKSPACE;
+  }
+  if (sh.n_tokens == 0) return LORA_OK;
+  return launch_lora_w4(sh, x, x_scales, codes, scales, A_pack, B_pack, desc, adapter_ids, y, ws,
+                        S(stream));
+}
+
+// ------------------------------------------------------------------ gradient norms
+static lora_status check_grad_shape(const grad_shape* sh) {
+  LORA_ARG_CHECK(sh != nullptr, "grad shape is NULL");
+  LORA_ARG_CHECK(sh->n_elems >= 0 && sh->n_elems <= (int64_t)1 << 42, "n_elems %lld outside [0, 2^42]",
+                 (long long)sh->n_elems);
+  LORA_ARG_CHECK(sh->n_groups >= 1 && sh->n_groups <= 16384, "n_groups %d outside [1, 16384]",
+                 sh->n_groups);
+  LORA_ARG_CHECK(sh->n_tensors >= 0 && sh->n_tensors <= 1 << 24, "n_tensors %d outside [0, 2^24]",
+                 sh->n_tensors);
+  // a launch takes fewer than 2^32 threads: 256 a chunk
+  LORA_ARG_CHECK(sh->n_chunks >= 0 && sh->n_chunks < 1 << 24, "n_chunks %d outside [0, 2^24)",
+                 sh->n_chunks);
+  LORA_ARG_CHECK(sh->reserved == 0, "reserved field must be 0");
+  LORA_ARG_CHECK(sh->n_chunks == 0 || sh->n_tensors > 0, "n_chunks %d without tensors", sh->n_chunks);
+  return LORA_OK;
+}
+
+static lora_status grad_checks(const grad_shape* shape, const grad_tensor* table, const float* g,
+                               float max_norm, void* ws, size_t ws_bytes, const char* what) {
+  TRY(check_grad_shape(shape));
+  LORA_ARG_CHECK(shape->n_tensors == 0 || table, "%s: table is NULL", what);
+  LORA_ARG_CHECK(shape->n_chunks == 0 || g, "%s: g is NULL", what);
+  LORA_ARG_CHECK(max_norm >= 0.f, "%s: max_norm must be >= 0 (and not NaN)", what);
+  if (!ws || ws_bytes < grad_ws_bytes(*shape)) {
+    set_error("%s: workspace %zu bytes < %zu needed", what, ws_bytes, grad_ws_bytes(*shape));
+    return LORA_E_WORKSPACE;
+  }
+  return LORA_OK;
+}
+
+size_t grad_workspace_bytes(const grad_shape* shape) {
+  if (check_grad_shape(shape) != LORA_OK) return 0;
+  return grad_ws_bytes(*shape);
+}
+
+lora_status grad_norm(const grad_shape* shape, const grad_tensor* table, const float* g,
+                      float* norms, void* ws, size_t ws_bytes, void* stream) {
+  TRY(grad_checks(shape, table, g, 0.f, ws, ws_bytes, "grad_norm"));
+  LORA_ARG_CHECK(norms != nullptr, "grad_norm: norms is NULL");
+  return launch_grad_norm(*shape, table, g, norms, ws, S(stream));
+}
+
+lora_status grad_clip(const grad_shape* shape, const grad_tensor* table, const float* g,
+                      float max_norm, float* g_out, float* norms, void* ws, size_t ws_bytes,
+                      void* stream) {
+  TRY(grad_checks(shape, table, g, max_norm, ws, ws_bytes, "grad_clip"));
+  LORA_ARG_CHECK(shape->n_chunks == 0 || g_out, "grad_clip: g_out is NULL");
+  return launch_grad_clip(*shape, table, g, max_norm, g_out, norms, ws, S(stream));
+}
+
+lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table, int64_t* steps,
+                              float* p, const float* g, float* m, float* v, float max_norm,
+                              double lr, double beta1, double beta2, double eps,
+                              double weight_decay,
+                              uint16_t* p_bf16, float* norms, void* ws, size_t ws_bytes,
+                              void* stream) {
+  TRY(grad_checks(shape, table, g, max_norm, ws, ws_bytes, "adam_step_clipped"));
+  LORA_ARG_CHECK(beta1 >= 0. && beta1 < 1. && beta2 >= 0. && beta2 < 1., "betas must lie in [0, 1)");
+  LORA_ARG_CHECK(steps != nullptr, "adam_step_clipped: steps is NULL");
+  LORA_ARG_CHECK(shape->n_chunks == 0 || (p && m && v), "adam_step_clipped: p/m/v NULL");
+  timer_begin(LORA_TIMER_ADAM, S(stream));
+  TRY(launch_adam_clipped(*shape, table, steps, p, g, m, v, max_norm, lr, beta1, beta2, eps,
+                          weight_decay, p_bf16, norms, ws, S(stream)));
+  timer_end(LORA_TIMER_ADAM, S(stream));
+  return LORA_OK;
+}
+
 // ------------------------------------------------------------------ timing
 void lora_timing_enable(int on) { g_tim.on = on != 0; }
 

@@ -1,0 +1,387 @@
+// RMS norm with the residual's addition on gfx950: forward (bf16 or 8-bit
+// block-scaled output) and backward.
+//
+//   h = bf16(x + residual),  rstd = 1 / sqrt(mean_j h_j^2 + eps),
+//   v_j = h_j rstd w_j;      y = bf16(v), or per 32 columns
+//   e = the least integer with max|v| <= 448 2^e,  q = e4m3(v 2^-e).
+//   backward, with xh = h rstd and g = dy w:
+//   dx = bf16(dh + rstd (g - xh mean_j(g xh))),   dw_j = sum_t dy_tj xh_tj.
+//
+// Everything is bound by HBM: a row is read once, kept in registers across its
+// reduction and written once.  A team of lanes owns a row and lane l of it
+// holds the 8-column vectors l, l + team, ...: rows of up to 512 columns take
+// part of a wave (several rows a wave, shuffles only), longer ones whole waves
+// of one block that join their sums through LDS.  Teams step over the rows
+// with the grid's stride, so a block reads the weight once.  The team of a row
+// depends on `hidden` alone: a row's bits do not change with the batch.
+#include "common.hpp"
+#include "sgmv.hpp"
+
+namespace lora {
+
+constexpr int NORM_MAX_VPL = 4;      // vectors of 8 columns a lane holds
+constexpr int NORM_SMALL_BLOCK = 256;
+
+// Columns c..c+7 of a row: one 16-byte access where every row is 16-byte
+// aligned (hidden a multiple of 8), else element by element up to column H.
+template <bool VEC>
+__device__ __forceinline__ uint4 norm_load8(const uint16_t* row, int c, int H) {
+  if (VEC) return *(const uint4*)(row + c);
+  uint32_t r[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < H) r[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+template <bool VEC>
+__device__ __forceinline__ void norm_store8(uint16_t* row, int c, int H, uint4 v) {
+  if (VEC) {
+    *(uint4*)(row + c) = v;
+    return;
+  }
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < H) row[c + i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
+}
+__device__ __forceinline__ void unpack8(uint4 v, float* f) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = bf2f_lo(r[q]);
+    f[2 * q + 1] = bf2f_hi(r[q]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack2bf(f[0], f[1]), pack2bf(f[2], f[3]), pack2bf(f[4], f[5]),
+                    pack2bf(f[6], f[7]));
+}
+
+// Sum over the row's team, the same value in each of its lanes: shuffles within
+// the wave, then the waves' sums in wave order.  `red` alternates between two
+// halves by `turn`, so one barrier a row suffices.
+__device__ __forceinline__ float team_sum(float s, int team, float (*red)[16], int turn) {
+  const int in_wave = team < kWave ? team : kWave;
+  for (int o = in_wave >> 1; o > 0; o >>= 1) s += __shfl_xor(s, o, kWave);
+  if (team <= kWave) return s;
+  if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = s;
+  __syncthreads();
+  float t = 0.f;
+  for (int w = 0; w < team / kWave; ++w) t += red[turn][w];
+  return t;
+}
+
+__device__ __forceinline__ float norm_rstd(float ss, int H, float eps) {
+  return __fdiv_rn(1.f, __fsqrt_rn(ss / (float)H + eps));
+}
+
+// The 8-bit form of the 32 columns that lanes 4i..4i+3 hold: the scale's biased
+// exponent byte from the largest finite magnitude's bits (the least power of two
+// with max <= 448 scale, so no finite value saturates), at least 1 (2^-126) and
+// by the finite range at most 247, so that the scale and its reciprocal are
+// normal fp32 numbers; then e4m3 codes, rounded to nearest even.  NaN and
+// +-Inf become the NaN code.
+__device__ __forceinline__ uint2 quantize8(const float* v, int& scale_byte) {
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(v[i]);
+    mx = (a <= 3.4028234663852886e38f && a > mx) ? a : mx;
+  }
+  mx = fmaxf(mx, __shfl_xor(mx, 1, kWave));
+  mx = fmaxf(mx, __shfl_xor(mx, 2, kWave));
+  const int bits = __float_as_int(mx);
+  const int b = max((bits >> 23) - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0), 1);
+  scale_byte = b;
+  const float mul = __int_as_float((254 - b) << 23);   // 2^(127 - b)
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = v[i] * mul;
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(s[4], s[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(s[6], s[7], hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+template <int VPL, bool VEC, bool Q8>
+__global__ __launch_bounds__(1024) void rmsnorm_fwd_kernel(
+    int64_t n, int H, int team, const uint16_t* x, const uint16_t* res,
+    const uint16_t* __restrict__ weight, float eps, uint16_t* h, uint16_t* y,
+    uint8_t* __restrict__ q, uint8_t* __restrict__ qs, float* __restrict__ rstd_out) {
+  __shared__ float red[2][16];
+  const int lane = threadIdx.x % team;
+  const int64_t per_block = blockDim.x / team;
+  const int64_t stride = per_block * gridDim.x;
+  uint4 wv[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int c = (lane + v * team) * 8;
+    wv[v] = c < H ? norm_load8<VEC>(weight, c, H) : make_uint4(0, 0, 0, 0);
+  }
+  int turn = 0;
+  // every lane of a block runs the same number of rounds (the barriers below)
+  for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < n; r0 += stride, turn ^= 1) {
+    const int64_t row = r0 + threadIdx.x / team;
+    const bool live = row < n;
+    const int64_t base = row * H;
+    float f[VPL][8];
+    float ss = 0.f;
+    uint4 xv[VPL], rv[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int c = (lane + v * team) * 8;
+      const bool on = live && c < H;
+      xv[v] = on ? norm_load8<VEC>(x + base, c, H) : make_uint4(0, 0, 0, 0);
+      if (res) rv[v] = on ? norm_load8<VEC>(res + base, c, H) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int c = (lane + v * team) * 8;
+      unpack8(xv[v], f[v]);
+      if (res) {
+        float g[8];
+        unpack8(rv[v], g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[v][i] += g[i];
+        const uint4 hv = pack8(f[v]);
+        if (live && c < H) norm_store8<VEC>(h + base, c, H, hv);
+        unpack8(hv, f[v]);   // the statistics are those of the stored h
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += f[v][i] * f[v][i];
+    }
+    ss = team_sum(ss, team, red, turn);
+    const float rstd = norm_rstd(ss, H, eps);
+    if (rstd_out && lane == 0 && live) rstd_out[row] = rstd;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int c = (lane + v * team) * 8;
+      float w[8], o[8];
+      unpack8(wv[v], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = f[v][i] * rstd * w[i];
+      if (Q8) {
+        int b;
+        const uint2 code = quantize8(o, b);
+        if (live && c < H) {
+          *(uint2*)(q + base + c) = code;
+          if ((lane & 3) == 0) qs[base / 32 + c / 32] = (uint8_t)b;
+        }
+      } else if (live && c < H) {
+        norm_store8<VEC>(y + base, c, H, pack8(o));
+      }
+    }
+  }
+}
+
+// Backward.  With `partial`, each lane keeps its columns' dw terms over the
+// rows its team visits; the block's teams are joined through LDS in team order
+// and the block writes one row of partial [gridDim.x][H].
+template <int VPL, bool VEC>
+__global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(
+    int64_t n, int H, int team, const uint16_t* dy, const uint16_t* dh,
+    const uint16_t* __restrict__ h, const uint16_t* __restrict__ weight,
+    const float* __restrict__ rstd_in, uint16_t* dx, float* __restrict__ partial) {
+  __shared__ float red[2][16];
+  __shared__ float join[NORM_SMALL_BLOCK * 8];
+  const int lane = threadIdx.x % team;
+  const int64_t per_block = blockDim.x / team;
+  const int64_t stride = per_block * gridDim.x;
+  uint4 wv[VPL];
+  float dw[VPL][8];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int c = (lane + v * team) * 8;
+    wv[v] = c < H ? norm_load8<VEC>(weight, c, H) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+  }
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < n; r0 += stride, turn ^= 1) {
+    const int64_t row = r0 + threadIdx.x / team;
+    const bool live = row < n;
+    const int64_t base = row * H;
+    const float rstd = live ? rstd_in[row] : 0.f;
+    uint4 dv[VPL], hv[VPL], uv[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int c = (lane + v * team) * 8;
+      const bool on = live && c < H;
+      dv[v] = on ? norm_load8<VEC>(dy + base, c, H) : make_uint4(0, 0, 0, 0);
+      hv[v] = on ? norm_load8<VEC>(h + base, c, H) : make_uint4(0, 0, 0, 0);
+      if (dh) uv[v] = on ? norm_load8<VEC>(dh + base, c, H) : make_uint4(0, 0, 0, 0);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      float d[8], x[8], w[8];
+      unpack8(dv[v], d);
+      unpack8(hv[v], x);
+      unpack8(wv[v], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = x[i] * rstd;
+        s += d[i] * w[i] * xh;
+        dw[v][i] += d[i] * xh;
+      }
+    }
+    const float c1 = team_sum(s, team, red, turn) / (float)H;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int c = (lane + v * team) * 8;
+      float d[8], x[8], w[8], u[8], o[8];
+      unpack8(dv[v], d);
+      unpack8(hv[v], x);
+      unpack8(wv[v], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = rstd * (d[i] * w[i] - x[i] * rstd * c1);
+      if (dh) {
+        unpack8(uv[v], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += u[i];
+      }
+      if (live && c < H) norm_store8<VEC>(dx + base, c, H, pack8(o));
+    }
+  }
+  if (!partial) return;
+  float* out = partial + (int64_t)blockIdx.x * H;
+  if (team > kWave || per_block == 1) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (lane + v * team) * 8 + i;
+        if (c < H) out[c] = dw[v][i];
+      }
+    return;
+  }
+  // several teams a block (VPL is 1 here): join[team index][column]
+#pragma unroll
+  for (int i = 0; i < 8; ++i) join[threadIdx.x * 8 + i] = dw[0][i];
+  __syncthreads();
+  const int cols = team * 8;
+  for (int c = threadIdx.x; c < H; c += blockDim.x) {
+    float t = 0.f;
+    for (int k = 0; k < (int)per_block; ++k) t += join[k * cols + c];
+    out[c] = t;
+  }
+}
+
+// dw[c] (+)= sum over blocks of partial[b][c], in block order within each of 16
+// fixed groups and then in group order.  64 columns a block.
+__global__ __launch_bounds__(1024) void norm_colsum_kernel(const float* __restrict__ partial,
+                                                           int blocks, int H,
+                                                           float* __restrict__ dw, int accumulate) {
+  __shared__ float s[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float t = 0.f;
+  if (c < H)
+#pragma unroll 4
+    for (int b = w; b < blocks; b += 16) t += partial[(int64_t)b * H + c];
+  s[w][lane] = t;
+  __syncthreads();
+  if (w != 0 || c >= H) return;
+  t = 0.f;
+  for (int k = 0; k < 16; ++k) t += s[k][lane];
+  dw[c] = accumulate ? dw[c] + t : t;
+}
+
+}  // namespace lora
+
+namespace lora_host {
+using namespace lora;
+
+// The team of a row of H columns, the vectors a lane holds and the block.
+struct NormPlan {
+  int team, vpl, block;
+};
+static NormPlan norm_plan(int64_t H) {
+  const int64_t vecs = cdiv(H, 8);
+  if (vecs <= kWave) {
+    int team = 4;   // at least the four lanes of a 32-column scale block
+    while (team < vecs) team *= 2;
+    return {team, 1, NORM_SMALL_BLOCK};
+  }
+  const int vpl = vecs <= 2 * 1024 ? 2 : NORM_MAX_VPL;
+  const int team = (int)align_up(cdiv(vecs, vpl), kWave);
+  return {team, vpl, team};
+}
+
+static unsigned norm_grid(int64_t n, const NormPlan& p, int64_t cap) {
+  return (unsigned)std::max<int64_t>(1, std::min(cdiv(n, p.block / p.team), cap));
+}
+
+// Blocks that keep dw partials: 2^18 threads in all fill the chip's 256 CUs
+// with 16 waves each, and the partials stay under 16 MB.
+int64_t rmsnorm_bwd_blocks(int64_t n, int64_t hidden) {
+  const NormPlan p = norm_plan(hidden);
+  return norm_grid(n, p, std::max<int64_t>(1, (1 << 18) / p.block));
+}
+
+template <int VPL, bool VEC, bool Q8>
+static void fwd_launch(const NormPlan& p, unsigned grid, int64_t n, int64_t H, const uint16_t* x,
+                       const uint16_t* res, const uint16_t* w, float eps, uint16_t* h, uint16_t* y,
+                       uint8_t* q, uint8_t* qs, float* rstd, hipStream_t s) {
+  hipLaunchKernelGGL((rmsnorm_fwd_kernel<VPL, VEC, Q8>), dim3(grid), dim3(p.block), 0, s, n, (int)H,
+                     p.team, x, res, w, eps, h, y, q, qs, rstd);
+}
+
+lora_status launch_rmsnorm_fwd(int64_t n, int64_t H, const uint16_t* x, const uint16_t* res,
+                               const uint16_t* w, float eps, uint16_t* h, uint16_t* y, uint8_t* q,
+                               uint8_t* qs, float* rstd, hipStream_t s) {
+  const NormPlan p = norm_plan(H);
+  const unsigned grid = norm_grid(n, p, std::max<int64_t>(1, (1 << 19) / p.block));
+  const bool vec = H % 8 == 0;
+#define LORA_NORM_FWD(V)                                                                      \
+  if (q)                                                                                      \
+    fwd_launch<V, true, true>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s);           \
+  else if (vec)                                                                               \
+    fwd_launch<V, true, false>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s);          \
+  else                                                                                        \
+    fwd_launch<V, false, false>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s)
+  if (p.vpl == 1) {
+    LORA_NORM_FWD(1);
+  } else if (p.vpl == 2) {
+    LORA_NORM_FWD(2);
+  } else {
+    LORA_NORM_FWD(4);
+  }
+#undef LORA_NORM_FWD
+  return launch_check("rmsnorm_fwd");
+}
+
+template <int VPL>
+static void bwd_launch(const NormPlan& p, unsigned grid, int64_t n, int64_t H, const uint16_t* dy,
+                       const uint16_t* dh, const uint16_t* h, const uint16_t* w, const float* rstd,
+                       uint16_t* dx, float* partial, hipStream_t s) {
+  if (H % 8 == 0)
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<VPL, true>), dim3(grid), dim3(p.block), 0, s, n, (int)H,
+                       p.team, dy, dh, h, w, rstd, dx, partial);
+  else
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<VPL, false>), dim3(grid), dim3(p.block), 0, s, n, (int)H,
+                       p.team, dy, dh, h, w, rstd, dx, partial);
+}
+
+lora_status launch_rmsnorm_bwd(int64_t n, int64_t H, const uint16_t* dy, const uint16_t* dh,
+                               const uint16_t* h, const uint16_t* w, const float* rstd,
+                               uint16_t* dx, float* dw, int accumulate, float* partial,
+                               hipStream_t s) {
+  const NormPlan p = norm_plan(H);
+  const unsigned grid = dw ? (unsigned)rmsnorm_bwd_blocks(n, H)
+                           : norm_grid(n, p, std::max<int64_t>(1, (1 << 19) / p.block));
+  if (p.vpl == 1)
+    bwd_launch<1>(p, grid, n, H, dy, dh, h, w, rstd, dx, dw ? partial : nullptr, s);
+  else if (p.vpl == 2)
+    bwd_launch<2>(p, grid, n, H, dy, dh, h, w, rstd, dx, dw ? partial : nullptr, s);
+  else
+    bwd_launch<4>(p, grid, n, H, dy, dh, h, w, rstd, dx, dw ? partial : nullptr, s);
+  lora_status st = launch_check("rmsnorm_bwd");
+  if (st != LORA_OK || !dw) return st;
+  hipLaunchKernelGGL(norm_colsum_kernel, dim3((unsigned)cdiv(H, 64)), dim3(1024), 0, s, partial,
+                     (int)grid, (int)H, dw, accumulate);
+  return launch_check("norm_colsum");
+}
+
+}  // namespace lora_host

@@ -145,6 +145,39 @@ lora_status launch_fill_i32(int32_t* p, int64_t n, int32_t v, hipStream_t s);
 // *dst |= *src (a status word into another), one tiny launch
 lora_status launch_or_status(const int32_t* src, int32_t* dst, hipStream_t s);
 
+// norm.hip
+int64_t rmsnorm_bwd_blocks(int64_t n, int64_t hidden);   // rows of the dw partials
+lora_status launch_rmsnorm_fwd(int64_t n, int64_t H, const uint16_t* x, const uint16_t* res,
+                               const uint16_t* w, float eps, uint16_t* h, uint16_t* y, uint8_t* q,
+                               uint8_t* qs, float* rstd, hipStream_t s);
+lora_status launch_rmsnorm_bwd(int64_t n, int64_t H, const uint16_t* dy, const uint16_t* dh,
+                               const uint16_t* h, const uint16_t* w, const float* rstd,
+                               uint16_t* dx, float* dw, int accumulate, float* partial,
+                               hipStream_t s);
+
+// w4.hip
+size_t w4_ws_bytes(int64_t n, int max_rank);
+lora_status launch_w4_quantize(const uint16_t* W, int64_t rows, int64_t cols, uint8_t* codes,
+                               uint8_t* scales, hipStream_t s);
+lora_status launch_w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
+                             const uint8_t* xs, const uint8_t* codes, const uint8_t* scales,
+                             uint16_t* y, hipStream_t s);
+lora_status launch_lora_w4(const lora_shape& sh, const void* x, const uint8_t* xs,
+                           const uint8_t* codes, const uint8_t* scales, const uint16_t* A_pack,
+                           const uint16_t* B_pack, const lora_adapter_desc* desc,
+                           const int32_t* ids, uint16_t* y, void* ws, hipStream_t s);
+
+// grads.hip
+size_t grad_ws_bytes(const grad_shape& sh);
+lora_status launch_grad_norm(const grad_shape& sh, const grad_tensor* tab, const float* g,
+                             float* norms, void* ws, hipStream_t s);
+lora_status launch_grad_clip(const grad_shape& sh, const grad_tensor* tab, const float* g,
+                             float max_norm, float* out, float* norms, void* ws, hipStream_t s);
+lora_status launch_adam_clipped(const grad_shape& sh, const grad_tensor* tab, int64_t* steps,
+                                float* p, const float* g, float* m, float* v, float max_norm,
+                                double lr, double beta1, double beta2, double eps, double wd,
+                                uint16_t* p_bf16, float* norms, void* ws, hipStream_t s);
+
 // moe.hip
 lora_status launch_moe_route(const float* logits, int64_t n, int E, int K, int32_t* experts,
                              float* weights, hipStream_t s);

@@ -39,6 +39,9 @@ EXPORTS = [
     "moe_backward", "mlp_workspace_bytes", "mlp_saved_bytes", "mlp_forward", "mlp_backward",
     "lora_timing_enable", "lora_timing_reset", "lora_timing_read",
     "lora_forward_noalloc_scratch_bytes", "lora_forward_noalloc",
+    "rmsnorm_forward", "rmsnorm_forward_q8", "rmsnorm_backward_workspace_bytes", "rmsnorm_backward",
+    "w4_quantize", "w4_linear", "lora_forward_w4_workspace_bytes", "lora_forward_w4",
+    "grad_workspace_bytes", "grad_norm", "grad_clip", "adam_step_clipped",
     "lora_probe_mfma_flops_per_iter", "lora_probe_mfma", "lora_probe_copy", "lora_probe_read",
 ]
 
@@ -79,6 +82,16 @@ class LossConfig(ctypes.Structure):
     _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float)]
 
 
+class GradShape(ctypes.Structure):
+    _fields_ = [("n_elems", ctypes.c_int64), ("n_chunks", ctypes.c_int32),
+                ("n_tensors", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+W4_MAX_TOKENS = 256
+GRAD_CHUNK = 8192
+GRAD_DTYPE = np.dtype([("offset", "<i8"), ("count", "<i8"), ("group", "<i4"), ("first_chunk", "<i4")])
+assert GRAD_DTYPE.itemsize == 24
 DESC_DTYPE = np.dtype([("a_off", "<i8"), ("b_off", "<i8"), ("rank", "<i4"), ("scale", "<f4")])
 assert DESC_DTYPE.itemsize == 24
 
@@ -86,6 +99,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _F = ctypes.c_float
+_D = ctypes.c_double
 _SZ = ctypes.c_size_t
 
 
@@ -130,6 +144,19 @@ def _load() -> ctypes.CDLL:
         "lora_forward_noalloc_scratch_bytes": (_SZ, []),
         "lora_forward_noalloc": (_I32, [ctypes.POINTER(LoraShape), _P, _P, _P, _P, _P, _P, _P, _P,
                                         _P, _P]),
+        "rmsnorm_forward": (_I32, [_I64, _I64, _P, _P, _P, _F, _P, _P, _P, _P]),
+        "rmsnorm_forward_q8": (_I32, [_I64, _I64, _P, _P, _P, _F, _P, _P, _P, _P, _P]),
+        "rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+        "rmsnorm_backward": (_I32, [_I64, _I64, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _SZ, _P]),
+        "w4_quantize": (_I32, [_P, _I64, _I64, _P, _P, _P]),
+        "w4_linear": (_I32, [_I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
+        "lora_forward_w4_workspace_bytes": (_SZ, [ctypes.POINTER(LoraShape)]),
+        "lora_forward_w4": (_I32, [ctypes.POINTER(LoraShape)] + [_P] * 10 + [_SZ, _P]),
+        "grad_workspace_bytes": (_SZ, [ctypes.POINTER(GradShape)]),
+        "grad_norm": (_I32, [ctypes.POINTER(GradShape), _P, _P, _P, _P, _SZ, _P]),
+        "grad_clip": (_I32, [ctypes.POINTER(GradShape), _P, _P, _F, _P, _P, _P, _SZ, _P]),
+        "adam_step_clipped": (_I32, [ctypes.POINTER(GradShape), _P, _P, _P, _P, _P, _P, _F] + [_D] * 5 +
+                              [_P, _P, _P, _SZ, _P]),
         "lora_probe_mfma_flops_per_iter": (_I64, [_I32]),
         "lora_probe_mfma": (_I32, [_I64, _I32, _P, _P]),
         "lora_probe_copy": (_I32, [_P, _P, _I64, _P]),
@@ -409,6 +436,183 @@ def swiglu_forward(gate, up, h, stream=None):
 def swiglu_backward(dh, gate, up, dgate, dup, stream=None):
     _check(LIB.swiglu_backward(gate.numel(), _ptr(dh), _ptr(gate), _ptr(up), _ptr(dgate), _ptr(dup),
                                _stream(stream)))
+
+
+def _arg(cond, msg):
+    if not cond:
+        raise LoraError(LORA_E_INVALID_ARG, msg)
+
+
+def _dense(t: Optional[torch.Tensor], dtypes, shape, name: str):
+    """Checks one operand of the calls below and returns its pointer (None for None)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs a contiguous {' or '.join(map(str, dtypes))} "
+                        f"tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs a device tensor")
+    return t.data_ptr()
+
+
+def _stream_for(t: torch.Tensor, stream=None):
+    """The stream to enqueue on (the current one if None); t must lie on the current device,
+    which is where the library launches."""
+    dev = torch.cuda.current_device()
+    s = torch.cuda.current_stream() if stream is None else stream
+    if t.get_device() != dev or s.device_index != dev:
+        raise LoraError(LORA_E_INVALID_ARG, f"the tensors are on {t.device}, the stream on device "
+                        f"{s.device_index}, the current device is {dev}")
+    return s.cuda_stream
+
+
+_BF16, _F32, _I64T, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int64,), (torch.uint8,)
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _norm_args(x, weight, rstd, residual, h):
+    _arg(x.dim() == 2, "x must be [n][hidden]")
+    n, hidden = x.shape
+    return n, hidden, (_dense(x, _BF16, x.shape, "x"), _dense(residual, _BF16, x.shape, "residual"),
+                       _dense(weight, _BF16, (hidden,), "weight"), _dense(h, _BF16, x.shape, "h"),
+                       _dense(rstd, _F32, (n,), "rstd"))
+
+
+def rmsnorm_forward(x, weight, eps, y, rstd=None, residual=None, h=None, stream=None):
+    """y = norm(x + residual) weight; h receives x + residual (given exactly with residual)."""
+    n, hidden, (px, pr, pw, ph, ps) = _norm_args(x, weight, rstd, residual, h)
+    _check(LIB.rmsnorm_forward(n, hidden, px, pr, pw, eps, ph, _dense(y, _BF16, x.shape, "y"), ps,
+                               _stream_for(x, stream)))
+
+
+def rmsnorm_forward_q8(x, weight, eps, q, q_scales, rstd=None, residual=None, h=None, stream=None):
+    """q: e4m3 codes [n][hidden] (uint8 or float8_e4m3fn); q_scales: E8M0 [n][hidden/32]."""
+    n, hidden, (px, pr, pw, ph, ps) = _norm_args(x, weight, rstd, residual, h)
+    _check(LIB.rmsnorm_forward_q8(n, hidden, px, pr, pw, eps, ph, _dense(q, _E4M3, x.shape, "q"),
+                                  _dense(q_scales, _E8M0, (n, hidden // 32), "q_scales"), ps,
+                                  _stream_for(x, stream)))
+
+
+def rmsnorm_backward_workspace_bytes(n, hidden) -> int:
+    return LIB.rmsnorm_backward_workspace_bytes(n, hidden)
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dx, dh=None, dweight=None, accumulate=False, ws=None,
+                     stream=None):
+    """dweight (with ws of rmsnorm_backward_workspace_bytes) is optional: a frozen weight has none."""
+    _arg(dy.dim() == 2, "dy must be [n][hidden]")
+    n, hidden = dy.shape
+    _check(LIB.rmsnorm_backward(n, hidden, _dense(dy, _BF16, dy.shape, "dy"),
+                                _dense(dh, _BF16, dy.shape, "dh"), _dense(h, _BF16, dy.shape, "h"),
+                                _dense(weight, _BF16, (hidden,), "weight"),
+                                _dense(rstd, _F32, (n,), "rstd"), _dense(dx, _BF16, dy.shape, "dx"),
+                                _dense(dweight, _F32, (hidden,), "dweight"), int(accumulate),
+                                None if ws is None else ws.data_ptr(), 0 if ws is None else _nbytes(ws),
+                                _stream_for(dy, stream)))
+
+
+def w4_quantize(W, codes, scales, stream=None):
+    """W bf16 [d_out][d_in] -> codes uint8 [d_out][d_in/2], scales uint8 [d_out][d_in/32]."""
+    _arg(W.dim() == 2, "W must be [d_out][d_in]")
+    d_out, d_in = W.shape
+    _check(LIB.w4_quantize(_dense(W, _BF16, W.shape, "W"), d_out, d_in,
+                           _dense(codes, _U8, (d_out, d_in // 2), "codes"),
+                           _dense(scales, _E8M0, (d_out, d_in // 32), "scales"), _stream_for(W, stream)))
+
+
+def _w4_args(n, d_in, d_out, x, x_scales, codes, scales, y):
+    return (_dense(x, _BF16 if x_scales is None else _E4M3, (n, d_in), "x"),
+            _dense(x_scales, _E8M0, (n, d_in // 32), "x_scales"),
+            _dense(codes, _U8, (d_out, d_in // 2), "codes"),
+            _dense(scales, _E8M0, (d_out, d_in // 32), "scales"), _dense(y, _BF16, (n, d_out), "y"))
+
+
+def w4_linear(x, codes, scales, y, x_scales=None, stream=None):
+    """y = x W^T with 4-bit W; x bf16, or e4m3 codes with their x_scales."""
+    _arg(x.dim() == 2 and codes.dim() == 2, "x must be [n][d_in] and codes [d_out][d_in/2]")
+    n, d_in = x.shape
+    d_out = codes.shape[0]
+    px, pxs, pc, ps, py = _w4_args(n, d_in, d_out, x, x_scales, codes, scales, y)
+    _check(LIB.w4_linear(n, d_in, d_out, px, pxs, pc, ps, py, _stream_for(codes, stream)))
+
+
+def lora_forward_w4_workspace_bytes(shape: LoraShape) -> int:
+    n = LIB.lora_forward_w4_workspace_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise LoraError(LORA_E_INVALID_ARG, LIB.lora_last_error().decode())
+    return n
+
+
+def lora_forward_w4(shape, x, codes, scales, A_pack, B_pack, desc, ids, y, ws, x_scales=None,
+                    stream=None):
+    """lora_forward on a 4-bit base (see w4_linear for x, codes and the scales)."""
+    px, pxs, pc, ps, py = _w4_args(shape.n_tokens, shape.d_in, shape.d_out, x, x_scales, codes, scales, y)
+    _check(LIB.lora_forward_w4(ctypes.byref(shape), px, pxs, pc, ps, A_pack.data_ptr(),
+                               B_pack.data_ptr(), desc.data_ptr(),
+                               _dense(ids, (torch.int32,), (shape.n_tokens,), "ids"), py,
+                               ws.data_ptr(), _nbytes(ws), _stream_for(codes, stream)))
+
+
+def make_grad_table(tensors, n_groups, n_elems, device="cuda"):
+    """tensors: (offset, count, group) triples of one flat buffer of n_elems, in any order.
+    Returns the GradShape and the device table (sorted by group) of the calls below."""
+    t = np.array([tuple(map(int, e)) for e in tensors], np.int64).reshape(-1, 3)
+    _arg(np.all(t[:, :2] >= 0) and np.all(t[:, 0] + t[:, 1] <= n_elems),
+         f"a tensor lies outside a buffer of {n_elems}")
+    _arg(np.all((t[:, 2] >= 0) & (t[:, 2] < n_groups)), f"a group outside [0, {n_groups})")
+    by_place = t[np.argsort(t[:, 0], kind="stable")]
+    by_place = by_place[by_place[:, 1] > 0]
+    _arg(np.all(by_place[:-1, 0] + by_place[:-1, 1] <= by_place[1:, 0]), "tensors overlap")
+    t = t[np.argsort(t[:, 2], kind="stable")]
+    chunks = -(-t[:, 1] // GRAD_CHUNK)
+    _arg(chunks.sum() < 1 << 24, "too many elements for one table")
+    d = np.zeros(len(t), GRAD_DTYPE)
+    d["offset"], d["count"], d["group"], d["first_chunk"] = t[:, 0], t[:, 1], t[:, 2], np.cumsum(chunks) - chunks
+    table = torch.from_numpy(d.view(np.uint8).copy()).to(device)
+    return GradShape(int(n_elems), int(chunks.sum()), len(t), int(n_groups), 0), table
+
+
+def grad_workspace_bytes(shape: GradShape) -> int:
+    n = LIB.grad_workspace_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise LoraError(LORA_E_INVALID_ARG, LIB.lora_last_error().decode())
+    return n
+
+
+def _grad_args(shape, table, flat, norms):
+    _arg(table.numel() * table.element_size() >= shape.n_tensors * GRAD_DTYPE.itemsize,
+         "table is shorter than n_tensors entries")
+    return (table.data_ptr(), *(_dense(t, _F32, (shape.n_elems,), name) for name, t in flat),
+            _dense(norms, _F32, (shape.n_groups,), "norms"))
+
+
+def grad_norm(shape, table, g, norms, ws, stream=None):
+    """norms[a] = the norm of group a's gradient (shape, table: make_grad_table)."""
+    pt, pg, pn = _grad_args(shape, table, (("g", g),), norms)
+    _check(LIB.grad_norm(ctypes.byref(shape), pt, pg, pn, ws.data_ptr(), _nbytes(ws), _stream_for(g, stream)))
+
+
+def grad_clip(shape, table, g, max_norm, out, norms, ws, stream=None):
+    """out = g scaled to at most max_norm per group; out may be g, norms may be None."""
+    pt, pg, po, pn = _grad_args(shape, table, (("g", g), ("out", out)), norms)
+    _check(LIB.grad_clip(ctypes.byref(shape), pt, pg, max_norm, po, pn, ws.data_ptr(), _nbytes(ws),
+                         _stream_for(g, stream)))
+
+
+def adam_step_clipped(shape, table, steps, p, g, m, v, max_norm, lr, beta1=0.9, beta2=0.999,
+                      eps=1e-8, weight_decay=0.0, p_bf16=None, norms=None, ws=None, stream=None):
+    """One AdamW step per group on its clipped gradient; steps: device int64 [n_groups], the
+    steps made so far, counted up by the call.  ws: workspace of grad_workspace_bytes(shape)
+    (a fresh zeroed one if None)."""
+    pt, pp, pg, pm, pv, pn = _grad_args(shape, table, (("p", p), ("g", g), ("m", m), ("v", v)), norms)
+    if ws is None:
+        ws = empty_workspace(grad_workspace_bytes(shape), device=p.device)
+    _check(LIB.adam_step_clipped(ctypes.byref(shape), pt, _dense(steps, _I64T, (shape.n_groups,), "steps"),
+                                 pp, pg, pm, pv, max_norm, lr, beta1, beta2, eps, weight_decay,
+                                 _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16"), pn, ws.data_ptr(),
+                                 _nbytes(ws), _stream_for(p, stream)))
+    return ws
 
 
 def lora_probe_mfma(iters, blocks, sink, stream=None):

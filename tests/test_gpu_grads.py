@@ -1,0 +1,237 @@
+"""grad_norm, grad_clip and adam_step_clipped against oracle.clip.
+
+Tolerances, from the arithmetic: the sums are 64-bit, so a norm is off by its
+rounding to fp32, 2^-24; the factor c adds 2^-24 and its product with g another,
+2^-22 with room.  AdamW's m and v are sums of two products with fp32 constants, g
+scaled before (and squared): at most 8 roundings, 2^-21 of the two terms'
+magnitudes.  p has three roundings of its own (2^-22), the error of m carried
+through the quotient, and that of the denominator and the quotient, within 2^-20
+of the step.
+"""
+import numpy as np
+import pytest
+
+import oracle.clip as OC
+import workloads.bf16 as B
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from gpu_util import bits_of, dev_bf16, dev_f32, f64_of  # noqa: E402
+import rl_lora_linear_amd.lib as L  # noqa: E402
+
+LR, B1, B2, EPS = 1e-3, 0.9, 0.999, 1e-8
+
+
+def _tensors(kind):
+    """(tensors, n_groups, n_elems)"""
+    if kind == "one element":
+        return [(0, 1, 0)], 1, 1
+    if kind == "one tensor":
+        return [(0, 100003, 0)], 1, 100003
+    if kind == "empty groups":      # groups 0, 2 and 4 have no tensor, group 3 an empty one
+        return [(8, 40, 1), (64, 0, 3)], 5, 80
+    if kind == "chunk borders":
+        out, at = [], 0
+        for i, c in enumerate((8191, 8192, 8193, 16384, 1, 4, 5)):
+            out.append((at, c, i % 2))
+            at += c + 4 - c % 4 + 4
+        return out, 2, at
+    if kind == "unaligned":         # offsets at every residue of 4, layers listed before adapters
+        out, at = [], 3
+        for layer in range(6):
+            for a in range(4):
+                c = 701 * (a + 1) + 13 * layer
+                out.append((at, c, a))
+                at += c + layer % 3
+        return out, 4, at + 5
+    rng = np.random.default_rng(1)  # many: 3000 tensors over 50 groups
+    out, at = [], 0
+    for i in range(3000):
+        c = int(rng.integers(0, 2000))
+        out.append((at, c, int(rng.integers(0, 50))))
+        at += c + int(rng.integers(0, 3)) * 4
+    return out, 50, at + 1
+
+
+KINDS = ["one element", "one tensor", "empty groups", "chunk borders", "unaligned", "many"]
+
+
+def _inside(tensors, n):
+    m = np.zeros(n, bool)
+    for o, c, _ in tensors:
+        m[o:o + c] = True
+    return m
+
+
+def _close(got, want, rel, extra=0.0):
+    got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
+    bad = ~(np.abs(got - want) <= rel * np.abs(want) + extra)
+    assert not bad.any(), (np.argwhere(bad)[:3], got[bad][:3], want[bad][:3])
+
+
+def _setup(kind, seed=0):
+    tensors, G, n = _tensors(kind)
+    rng = np.random.default_rng(seed)
+    g = (rng.standard_normal(n) * np.exp2(rng.integers(-20, 4, n))).astype(np.float32)
+    shape, table = L.make_grad_table(tensors, G, n)
+    return tensors, G, n, rng, g, shape, table, L.empty_workspace(L.grad_workspace_bytes(shape))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_norm_and_clip(kind):
+    tensors, G, n, rng, g, shape, table, ws = _setup(kind)
+    dg, norms = dev_f32(g), torch.full((G,), -1.0, device="cuda")
+    L.grad_norm(shape, table, dg, norms, ws)
+    want = OC.norms(tensors, G, g)
+    _close(f64_of(norms), want, 2.0 ** -23)
+    live = want[want > 0]
+    for max_norm in (float(live.min()) * 0.5, float(np.median(live)), float("inf"), 0.0):
+        out, norms2 = torch.full((n,), 7.0, device="cuda"), torch.empty(G, device="cuda")
+        L.grad_clip(shape, table, dg, max_norm, out, norms2, ws)
+        res, _ = OC.clip(tensors, G, g, max_norm, out=np.full(n, 7.0))
+        got, inside = f64_of(out), _inside(tensors, n)
+        assert np.array_equal(got[~inside], np.full((~inside).sum(), 7.0))
+        _close(got[inside], res[inside], 2.0 ** -22, extra=2.0 ** -149)
+        assert np.array_equal(norms2.cpu().numpy(), norms.cpu().numpy())
+        # in place: the same bits
+        same = dg.clone()
+        L.grad_clip(shape, table, same, max_norm, same, None, ws)
+        assert np.array_equal(same.cpu().numpy()[inside], out.cpu().numpy()[inside])
+        if max_norm == float("inf"):
+            assert np.array_equal(same.cpu().numpy(), g)
+    assert np.array_equal(dg.cpu().numpy(), g) and L.lora_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e6])
+@pytest.mark.parametrize("wd", [0.0, 0.1])
+@pytest.mark.parametrize("kind", KINDS)
+def test_adam(kind, wd, max_norm):
+    tensors, G, n, rng, g, shape, table, ws = _setup(kind)
+    p, m = rng.standard_normal(n).astype(np.float32), (rng.standard_normal(n) * 0.1).astype(np.float32)
+    v = (rng.random(n) * 0.01 + 1e-4).astype(np.float32)
+    steps = rng.integers(0, 50, G)
+    dp, dm, dv, st = dev_f32(p), dev_f32(m), dev_f32(v), torch.from_numpy(steps).to("cuda")
+    pb, norms = dev_bf16(np.zeros(n, np.uint16)), torch.empty(G, device="cuda")
+    want = (p, m, v, steps)
+    inside = _inside(tensors, n)
+    for it in range(2):      # the second call from the first's state: the counters go on
+        before = [f64_of(a) for a in (dp, dm, dv)]
+        L.adam_step_clipped(shape, table, st, dp, dev_f32(g), dm, dv, max_norm, LR, B1, B2, EPS, wd, p_bf16=pb, norms=norms, ws=ws)
+        want = OC.adam_clipped(tensors, G, steps + it, *before[:1], g, *before[1:], max_norm, LR, B1, B2, EPS, wd)
+        _close(f64_of(norms), want[4], 2.0 ** -23)
+        cg, _ = OC.clip(tensors, G, g, max_norm)
+        gp, gm, gv = (f64_of(a) for a in (dp, dm, dv))
+        slack = 2.0 ** -21 * (np.abs(B1 * before[1]) + np.abs((1 - B1) * cg))
+        _close(gm, want[1], 0, extra=slack)
+        _close(gv, want[2], 2.0 ** -21)
+        t = np.zeros(n)
+        for o, c, a in tensors:
+            t[o:o + c] = steps[a] + it + 1
+        t[~inside] = 1
+        per_m = LR / (1 - B1 ** t) / (np.sqrt(want[2] / (1 - B2 ** t)) + EPS)
+        _close(gp, want[0], 0, extra=2.0 ** -22 * np.abs(before[0]) + per_m * (slack + 2.0 ** -20 * np.abs(want[1])))
+        assert np.array_equal(st.cpu().numpy(), steps + it + 1)
+        for got, old in zip((gp, gm, gv), before):
+            assert np.array_equal(got[~inside], old[~inside])
+        assert np.array_equal(bits_of(pb)[inside], B.to_bf16_bits_f32(dp.cpu().numpy())[inside])
+        assert not bits_of(pb)[~inside].any()
+    assert L.lora_device_status(ws) == 0
+
+
+def test_adam_without_clipping_is_near_adam_step_multi():
+    tensors, G, n, rng, g, shape, table, ws = _setup("one tensor")
+    p = rng.standard_normal(n).astype(np.float32)
+    a = [dev_f32(p), dev_f32(np.zeros(n)), dev_f32(np.zeros(n))]
+    b = [t.clone() for t in a]
+    st = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for t in range(3):
+        L.adam_step_clipped(shape, table, st, a[0], dev_f32(g), a[1], a[2], float("inf"), LR, ws=ws)
+        L.adam_step_multi([(0, n, t + 1)], b[0], dev_f32(g), b[1], b[2], LR)
+    # adam_step_multi's 1 - beta2 is that of an fp32 0.999: v differs by 1.3e-5, sqrt(v) with its
+    # correction cancels it but for some 1e-6 of the three steps
+    _close(f64_of(a[2]), f64_of(b[2]), 2e-5)
+    _close(f64_of(a[0]), f64_of(b[0]), 2.0 ** -22, extra=3 * LR * 1e-4)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("where", ["first", "last", "aligned tail"])
+def test_non_finite_group_is_left_alone(bad, where):
+    tensors, G, n, rng, g, shape, table, ws = _setup("unaligned")
+    mine = sorted(t for t in tensors if t[2] == 2)
+    at = {"first": mine[0][0], "last": mine[-1][0] + mine[-1][1] - 1, "aligned tail": mine[2][0] + mine[2][1] - 1}[where]
+    g[at] = bad
+    other = np.zeros(n, bool)
+    for o, c, a in tensors:
+        other[o:o + c] = a != 2
+    inside = _inside(tensors, n)
+    dg, out, norms = dev_f32(g), torch.zeros(n, device="cuda"), torch.empty(G, device="cuda")
+    L.grad_clip(shape, table, dg, 0.1, out, norms, ws)
+    assert L.lora_device_status(ws) == L.FLAG_NONFINITE_GRAD
+    nn = f64_of(norms)
+    assert not np.isfinite(nn[2]) and np.all(np.isfinite(np.delete(nn, 2)))
+    mask = inside & ~other
+    assert np.array_equal(out.cpu().numpy()[mask].view(np.uint32), g[mask].view(np.uint32))
+    assert np.all(np.isfinite(out.cpu().numpy()[other]))
+    p = rng.standard_normal(n).astype(np.float32)
+    dp, dm, dv = dev_f32(p), dev_f32(np.zeros(n)), dev_f32(np.zeros(n))
+    st = torch.full((G,), 4, dtype=torch.int64, device="cuda")
+    pb = dev_bf16(np.zeros(n, np.uint16))
+    L.adam_step_clipped(shape, table, st, dp, dg, dm, dv, 0.1, LR, p_bf16=pb, ws=ws)
+    assert L.lora_device_status(ws) == L.FLAG_NONFINITE_GRAD
+    assert list(st.cpu().numpy()) == [5, 5, 4, 5]
+    got = dp.cpu().numpy()
+    assert np.array_equal(got[mask], p[mask]) and not bits_of(pb)[mask].any() and not dm.cpu().numpy()[mask].any()
+    # the others step: their m is a share of their g (p itself may move by less than its last bit)
+    assert np.array_equal(dm.cpu().numpy()[other] != 0, g[other] != 0) and np.any(got[other] != p[other])
+
+
+def test_large_finite_gradients_do_not_overflow():
+    n = 5000
+    g = np.full(n, 3e38, np.float32)
+    shape, table = L.make_grad_table([(0, n, 0)], 1, n)
+    ws, out, norms = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.empty(n, device="cuda"), torch.empty(1, device="cuda")
+    L.grad_clip(shape, table, dev_f32(g), 1.0, out, norms, ws)
+    # the norm itself is beyond fp32, the clipped gradient is not
+    assert np.isinf(f64_of(norms)[0]) and L.lora_device_status(ws) == 0
+    _close(f64_of(out), np.full(n, 1 / np.sqrt(n)), 2.0 ** -21)
+
+
+def test_broken_tables_stay_inside_the_buffer():
+    """Entries that break the rules are flagged and touch nothing outside n_elems."""
+    n = 20000
+    guard = torch.full((3 * n,), 5.0, device="cuda")
+    g, out = torch.ones(n, device="cuda"), guard[n:2 * n]
+    for bad in ([(0, 8192, 0, 0), (15000, 8192, 0, 1)], [(-8, 100, 0, 0), (0, 8, 0, 1)], [(0, 100, 7, 0), (0, 8, 0, 1)],
+                [(0, 100, 0, 5), (0, 8, 0, 6)], [(0, 100, 0, -1), (200, 100, 0, 1)], [(0, 1 << 62, 0, 0), (0, 8, 0, 1)]):
+        d = np.array(bad, L.GRAD_DTYPE)
+        table = torch.from_numpy(d.view(np.uint8).copy()).to("cuda")
+        shape = L.GradShape(n, 2, 2, 1)
+        ws, norms = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.empty(1, device="cuda")
+        L.grad_clip(shape, table, g, 0.5, out, norms, ws)
+        assert L.lora_device_status(ws) & L.FLAG_BAD_DESC
+        assert bool((guard[:n] == 5).all()) and bool((guard[2 * n:] == 5).all())
+
+
+def test_no_tensors():
+    shape, table = L.make_grad_table([], 3, 16)
+    ws, norms = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.full((3,), -1.0, device="cuda")
+    g = torch.ones(16, device="cuda")
+    L.grad_clip(shape, table, g, 1.0, g, norms, ws)
+    assert bool((norms == 0).all()) and bool((g == 1).all())
+
+
+def test_elements_past_32_bits():
+    """A tensor whose offset does not fit 32 bits."""
+    n = (1 << 32) + 1000
+    g = torch.zeros(n, device="cuda")
+    g[n - 900:] = 2.0
+    shape, table = L.make_grad_table([(n - 900, 900, 0), (0, 100, 1)], 2, n)
+    ws, norms = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.empty(2, device="cuda")
+    L.grad_clip(shape, table, g, 6.0, g, norms, ws)
+    assert list(f64_of(norms)) == [60.0, 0.0]
+    _close(f64_of(g[n - 900:]), np.full(900, 0.2), 2.0 ** -21)
+    assert not bool(g[:n - 900].any())

@@ -1,0 +1,266 @@
+"""w4_quantize, w4_linear and lora_forward_w4 against oracle.w4 and oracle.lora.
+
+Tolerance of y, from the arithmetic: its rounding to bf16 is off by at most 2^-8
+of the value; the fp32 sum of d_in products runs over at most d_in/8 terms in
+sequence in a wave (all 32 of one matrix instruction counted), 8 wave sums and 64
+rank terms behind them, each step off by 2^-24 of the sum of magnitudes; u adds
+d_in/64 + 6 steps of its own to the delta's part of that sum.
+"""
+import numpy as np
+import pytest
+
+import oracle.lora as OL
+import oracle.norm as ON
+import oracle.w4 as OQ
+import workloads.bf16 as B
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from gpu_util import bits_of, dev_bf16, dev_i32, f64_of  # noqa: E402
+import rl_lora_linear_amd.lib as L  # noqa: E402
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda")
+
+
+def _weights(rng, d_out, d_in):
+    """Random codes (every one of the 16) and scales over some binades."""
+    return rng.integers(0, 256, (d_out, d_in // 2), dtype=np.uint8), rng.integers(110, 130, (d_out, d_in // 32)).astype(np.uint8)
+
+
+def _x(rng, n, d_in, x8):
+    """(device x, device scales or None, float64 values)."""
+    v = rng.standard_normal((n, d_in)) * np.exp2(rng.integers(-6, 6, (n, 1)))
+    v[:, rng.random(d_in) < 0.02] *= 30
+    if not x8:
+        b = B.to_bf16_bits(v)
+        return dev_bf16(b), None, B.bf16_bits_to_f64(b)
+    codes = rng.integers(0, 256, (n, d_in), dtype=np.uint8)
+    codes[(codes & 127) == 127] = 0x38
+    s = rng.integers(115, 135, (n, d_in // 32)).astype(np.uint8)
+    val = torch.from_numpy(codes).view(torch.float8_e4m3fn).to(torch.float64).numpy() * np.repeat(np.exp2(s.astype(float) - 127), 32, axis=1)
+    return _dev(codes), _dev(s), val
+
+
+def _check(y, want, mag, d_in):
+    got = f64_of(y)
+    tol = 2.0 ** -8 * np.abs(want) + (d_in / 8 + 80) * 2.0 ** -24 * (1 + 2.0 ** -8) * mag
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4], tol[bad][:4])
+
+
+SIZES = [(1, 64, 64), (1, 4096, 64), (2, 192, 128), (7, 320, 192), (15, 1024, 320), (16, 1088, 64), (17, 512, 128),
+         (31, 2112, 64), (33, 640, 192), (64, 1024, 256), (65, 256, 64), (100, 1600, 128), (129, 192, 320), (255, 576, 64), (256, 1024, 192),
+         (1, 12288, 128), (5, 16448, 64)]
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("n,d_in,d_out", SIZES)
+def test_linear(n, d_in, d_out, x8):
+    rng = np.random.default_rng(n * 31 + d_in + d_out)
+    codes, scales = _weights(rng, d_out, d_in)
+    x, xs, xv = _x(rng, n, d_in, x8)
+    W = OQ.values(codes, scales)
+    y = torch.full((n + 1, d_out), float("nan"), dtype=torch.bfloat16, device="cuda")
+    L.w4_linear(x, _dev(codes), _dev(scales), y[:n], x_scales=xs)
+    _check(y[:n], xv @ W.T, np.abs(xv) @ np.abs(W).T, d_in)
+    assert bool(torch.isnan(y[n]).all())      # the row behind the last token
+
+
+def _adapters(rng, ranks, d_in, d_out):
+    sizes = np.array(ranks) * (d_in + d_out)
+    a_off = np.concatenate([[0], np.cumsum(sizes)[:-1]]).astype(np.int64)
+    b_off = a_off + np.array(ranks) * d_in
+    pack = B.to_bf16_bits(rng.standard_normal(int(sizes.sum())) * 0.1)
+    v = B.bf16_bits_to_f64(pack)
+    A = [v[a:a + r * d_in].reshape(r, d_in) for a, r in zip(a_off, ranks)]
+    Bm = [v[b:b + r * d_out].reshape(d_out, r) for b, r in zip(b_off, ranks)]
+    scale = (32.0 / np.maximum(1, np.array(ranks))).astype(np.float32)
+    return pack, a_off, b_off, A, Bm, scale
+
+
+def _magnitude(xv, W, A, Bm, s, ids):
+    """Sum of magnitudes behind each y (the delta's with its inner sums' magnitudes)."""
+    mag = np.abs(xv) @ np.abs(W).T
+    for t, a in enumerate(ids):
+        if 0 <= a < len(A) and A[a].size:
+            # u's own error (d_in/64 + 6 steps) is smaller than the d_in/8 + 80 allowed below
+            mag[t] += s[a] * (np.abs(Bm[a]) @ (np.abs(A[a]) @ np.abs(xv[t])))
+    return mag
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("n,d_in,d_out", SIZES)
+def test_lora_forward(n, d_in, d_out, x8):
+    rng = np.random.default_rng(n * 37 + d_in + d_out)
+    codes, scales = _weights(rng, d_out, d_in)
+    scales = np.minimum(scales, 122).astype(np.uint8)
+    x, xs, xv = _x(rng, n, d_in, x8)
+    ranks = [8, 16, 24, 32, 40, 48, 56, 64, 8]
+    pack, a_off, b_off, A, Bm, s = _adapters(rng, ranks, d_in, d_out)
+    desc = L.make_desc(a_off, b_off, ranks, s)
+    ids = rng.integers(-1, len(ranks) + 1, n).astype(np.int32)
+    ids[0] = len(ranks) - 1 if n == 1 else -1
+    shape = L.make_shape(n, d_in, d_out, len(pack), len(pack), len(ranks), 64, L.IDS_INTERLEAVED)
+    ws = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape))
+    y = torch.full((n, d_out), float("nan"), dtype=torch.bfloat16, device="cuda")
+    p = dev_bf16(pack)
+    args = (_dev(codes), _dev(scales), p, p, desc, dev_i32(ids))
+    L.lora_forward_w4(shape, x, *args, y, ws, x_scales=xs)
+    W = OQ.values(codes, scales)
+    want, _ = OL.lora_forward(xv, W, A, Bm, s.astype(np.float64), ids)
+    _check(y, want, _magnitude(xv, W, A, Bm, s, ids), d_in)
+    flags = L.lora_device_status(ws)
+    assert flags == (L.FLAG_ID_RANGE if ((ids < 0) | (ids >= len(ranks))).any() else 0)
+    y2 = torch.empty_like(y)
+    L.lora_forward_w4(shape, x, *args, y2, ws, x_scales=xs)
+    assert np.array_equal(bits_of(y), bits_of(y2))
+    # a token without an adapter: the base product's bits
+    base = torch.empty_like(y)
+    L.w4_linear(x, args[0], args[1], base, x_scales=xs)
+    out = (ids < 0) | (ids >= len(ranks))
+    assert np.array_equal(bits_of(y)[out], bits_of(base)[out])
+
+
+def test_bad_descriptors_and_order():
+    rng = np.random.default_rng(3)
+    d_in, d_out, ranks = 128, 64, [16, 16, 16, 16, 16]
+    codes, scales = _weights(rng, d_out, d_in)
+    pack, a_off, b_off, A, Bm, s = _adapters(rng, ranks, d_in, d_out)
+    n = 6
+    x, _, xv = _x(rng, n, d_in, False)
+    W = OQ.values(codes, scales)
+    p = dev_bf16(pack)
+    ids = np.array([0, 1, 2, 3, 4, 0], np.int32)
+    base = torch.empty(n, d_out, dtype=torch.bfloat16, device="cuda")
+    L.w4_linear(x, _dev(codes), _dev(scales), base)
+
+    def call(a=a_off, b=b_off, r=ranks, order=L.IDS_INTERLEAVED, who=ids, elems=len(pack), max_rank=16):
+        shape = L.make_shape(n, d_in, d_out, elems, elems, 5, max_rank, order)
+        ws = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape))
+        y = torch.empty(n, d_out, dtype=torch.bfloat16, device="cuda")
+        L.lora_forward_w4(shape, x, _dev(codes), _dev(scales), p, p, L.make_desc(a, b, r, s), dev_i32(who), y, ws)
+        return y, L.lora_device_status(ws)
+
+    good, flags = call()
+    assert flags == 0
+    for what in ("past the pack", "negative", "unaligned", "rank", "rank above max_rank"):
+        a, b, r = a_off.copy(), b_off.copy(), list(ranks)
+        if what == "past the pack":
+            b[2] = len(pack) - 8
+        elif what == "negative":
+            a[2] = -8
+        elif what == "unaligned":
+            a[2] += 4
+        elif what == "rank":
+            r[2] = 12
+        else:
+            r[2] = 24
+        y, flags = call(a, b, r)
+        assert flags == L.FLAG_BAD_DESC, what
+        assert np.array_equal(bits_of(y)[2], bits_of(base)[2]), what
+        keep = [0, 1, 3, 4, 5]
+        assert np.array_equal(bits_of(y)[keep], bits_of(good)[keep]), what
+    y, flags = call(r=[16, 16, 0, 16, 16])      # rank 0: an unused slot, no flag
+    assert flags == 0 and np.array_equal(bits_of(y)[2], bits_of(base)[2])
+    y, flags = call(order=L.IDS_SORTED)
+    assert flags == L.FLAG_UNSORTED and np.array_equal(bits_of(y), bits_of(good))
+    y, flags = call(order=L.IDS_SORTED, who=np.sort(ids))
+    assert flags == 0
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 64), (128, 1600), (320, 4096)])
+def test_quantize(rows, cols):
+    rng = np.random.default_rng(rows)
+    W = B.round_bf16(rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-20, 20, (rows, 1))))
+    W[0, :32] = 0
+    W[1, :32] = np.tile([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], 4) * np.tile([1, -1], 16)   # ties
+    codes = torch.full((rows, cols // 2), 255, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows, cols // 32), 255, dtype=torch.uint8, device="cuda")
+    L.w4_quantize(dev_bf16(B.to_bf16_bits(W)), codes, scales)
+    want_c, want_s = OQ.quantize(W)
+    assert np.array_equal(scales.cpu().numpy(), want_s)
+    assert np.array_equal(OQ.values(codes.cpu().numpy(), want_s), OQ.values(want_c, want_s))
+
+
+def test_largest_and_smallest_scales():
+    """Scale bytes 1 and 250: exact products far from one."""
+    d_in = 64
+    codes = np.full((64, d_in // 2), 0x22, np.uint8)           # ones
+    x = torch.ones(1, d_in, dtype=torch.bfloat16, device="cuda")
+    for byte in (10, 127, 240):
+        scales = np.full((64, 2), byte, np.uint8)
+        y = torch.empty(1, 64, dtype=torch.bfloat16, device="cuda")
+        L.w4_linear(x, _dev(codes), _dev(scales), y)
+        assert np.all(f64_of(y) == 64 * 2.0 ** (byte - 127))
+    for byte in (10, 127, 240):
+        xs = np.full((1, 2), byte, np.uint8)
+        xq = np.full((1, d_in), 0x38, np.uint8)                # ones in e4m3
+        y = torch.empty(1, 64, dtype=torch.bfloat16, device="cuda")
+        L.w4_linear(_dev(xq), _dev(codes), _dev(np.full((64, 2), 127, np.uint8)), y, x_scales=_dev(xs))
+        assert np.all(f64_of(y) == 64 * 2.0 ** (byte - 127))
+
+
+def test_non_finite_x_and_scales():
+    """A non-finite x reaches its own token alone; the NaN scale its own row."""
+    rng = np.random.default_rng(9)
+    codes, scales = _weights(rng, 64, 256)
+    codes[:, 50] = 0x22                                        # ones at columns 100 and 101
+    x = torch.ones(3, 256, dtype=torch.bfloat16, device="cuda")
+    x[1, 100] = float("inf")
+    y = torch.empty(3, 64, dtype=torch.bfloat16, device="cuda")
+    L.w4_linear(x, _dev(codes), _dev(scales), y)
+    got = f64_of(y)
+    assert np.all(np.isinf(got[1])) and np.all(np.isfinite(got[[0, 2]]))
+    scales[5, 1] = 255
+    L.w4_linear(x, _dev(codes), _dev(scales), y)
+    got = f64_of(y)
+    assert np.all(np.isnan(got[:, 5])) and np.all(np.isfinite(np.delete(got[[0, 2]], 5, axis=1)))
+
+
+def test_eight_bit_norm_feeds_the_product():
+    """rmsnorm_forward_q8's own output as x, through lora_forward_w4."""
+    rng = np.random.default_rng(10)
+    n, H, d_out, ranks = 9, 512, 256, [16, 8]
+    hb, wb = B.to_bf16_bits(rng.standard_normal((n, H))), B.to_bf16_bits(1 + 0.1 * rng.standard_normal(H))
+    q = torch.empty(n, H, dtype=torch.float8_e4m3fn, device="cuda")
+    qs = torch.empty(n, H // 32, dtype=torch.float8_e8m0fnu, device="cuda")
+    L.rmsnorm_forward_q8(dev_bf16(hb), dev_bf16(wb), 1e-6, q, qs)
+    val = q.float().cpu().numpy().astype(np.float64) * np.repeat(qs.float().cpu().numpy().astype(np.float64), 32, axis=1)
+    v, _ = ON.rmsnorm_forward(B.bf16_bits_to_f64(hb), B.bf16_bits_to_f64(wb), 1e-6)
+    assert np.linalg.norm(val - v) < 2.0 ** -4 * np.linalg.norm(v)
+    codes, scales = OQ.quantize(B.round_bf16(0.05 * rng.standard_normal((d_out, H))))
+    pack, a_off, b_off, A, Bm, s = _adapters(rng, ranks, H, d_out)
+    ids = rng.integers(0, 2, n).astype(np.int32)
+    shape = L.make_shape(n, H, d_out, len(pack), len(pack), 2, 16, L.IDS_INTERLEAVED)
+    ws, p = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape)), dev_bf16(pack)
+    y = torch.empty(n, d_out, dtype=torch.bfloat16, device="cuda")
+    L.lora_forward_w4(shape, q, _dev(codes), _dev(scales), p, p, L.make_desc(a_off, b_off, ranks, s), dev_i32(ids), y, ws, x_scales=qs)
+    W = OQ.values(codes, scales)
+    want, _ = OL.lora_forward(val, W, A, Bm, s.astype(np.float64), ids)
+    _check(y, want, _magnitude(val, W, A, Bm, s, ids), H)
+    assert L.lora_device_status(ws) == 0
+
+
+def test_codes_past_four_gigabytes():
+    """Row offsets beyond 32 bits: 2^17 rows of 2^16 + 64 columns; sampled outputs."""
+    d_in, d_out = (1 << 16) + 64, 1 << 17
+    codes = torch.zeros(d_out, d_in // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.full((d_out, d_in // 32), 127, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(11)
+    rows = np.array([0, 1, 65535, 65536, d_out - 64, d_out - 1])
+    part = rng.integers(0, 256, (len(rows), d_in // 2), dtype=np.uint8)
+    codes[torch.from_numpy(rows).to("cuda")] = _dev(part)
+    x, _, xv = _x(rng, 2, d_in, False)
+    y = torch.empty(2, d_out, dtype=torch.bfloat16, device="cuda")
+    L.w4_linear(x, codes, scales, y)
+    W = OQ.values(part, np.full((len(rows), d_in // 32), 127, np.uint8))
+    _check(y[:, torch.from_numpy(rows).to("cuda")].contiguous(), xv @ W.T, np.abs(xv) @ np.abs(W).T, d_in)
+    rest = torch.ones(d_out, dtype=torch.bool, device="cuda")
+    rest[torch.from_numpy(rows).to("cuda")] = False
+    assert bool((y[:, rest] == 0).all())
