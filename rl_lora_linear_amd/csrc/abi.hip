@@ -1207,7 +1207,8 @@ lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
                       uint16_t* y, void* stream) {
   TRY(w4_dims(d_in, d_out, "w4_linear"));
   TRY(w4_tokens(n, "w4_linear"));
-  LORA_ARG_CHECK(codes && scales && aligned16(codes), "w4_linear: codes or scales NULL, or codes not 16-byte aligned");
+  LORA_ARG_CHECK(codes && scales && aligned16(codes) && aligned16(scales),
+                 "w4_linear: codes or scales NULL or not 16-byte aligned");
   LORA_ARG_CHECK(n == 0 || (x && y && aligned16(x) && aligned16(y)),
                  "w4_linear: x or y NULL or not 16-byte aligned");
   if (n == 0) return LORA_OK;
@@ -1230,8 +1231,8 @@ lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_
   TRY(w4_tokens(sh.n_tokens, "lora_forward_w4"));
   LORA_ARG_CHECK(codes && scales && A_pack && B_pack && desc,
                  "codes, scales, A_pack, B_pack and desc must be non-NULL");
-  LORA_ARG_CHECK(aligned16(codes) && aligned16(A_pack) && aligned16(B_pack),
-                 "codes and the packs must be 16-byte aligned");
+  LORA_ARG_CHECK(aligned16(codes) && aligned16(scales) && aligned16(A_pack) && aligned16(B_pack),
+                 "codes, scales and the packs must be 16-byte aligned");
   LORA_ARG_CHECK(sh.n_tokens == 0 || (x && adapter_ids && y), "x, adapter_ids and y must be non-NULL");
   LORA_ARG_CHECK(sh.n_tokens == 0 || (aligned16(x) && aligned16(y)), "x and y must be 16-byte aligned");
   if (!ws || ws_bytes < w4_ws_bytes(sh.n_tokens, sh.max_rank)) {

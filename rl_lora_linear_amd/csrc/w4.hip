@@ -19,9 +19,6 @@
 
 namespace lora {
 
-constexpr int W4_WAVES = 8;
-constexpr int W4_CHUNK = 128;   // k of one step: four scale blocks, one per lane group
-
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float e8m0(int byte) {   // 0 is 2^-127 (a subnormal), 255 is NaN
@@ -129,6 +126,38 @@ __global__ __launch_bounds__(64 * W4S_WAVES) void w4_shrink_kernel(
 }
 
 // ------------------------------------------------------------------ product
+// One block of 16 waves per CU holds 16 tokens and streams row tiles of 16 past
+// them.  The waves split k in pieces of 256 columns ("pairs": two steps of four
+// scale blocks): wave w keeps its pairs' x as MFMA fragments in registers for all
+// of its tiles and moves its own pairs of codes through a ring of its own in LDS,
+// so the loop has no barrier.  LDS-DMA fills the ring two pairs ahead (64 KB and
+// more in flight per CU).  Loading the fragments straight into registers would
+// touch 16 rows per quarter wave: the texture path then serves 16 bytes a clock,
+// a quarter of what it does for the whole 128-byte lines that the DMA asks for.
+// At the end of a tile the waves' sums are joined through LDS (one barrier); a
+// wave owns one token's LoRA delta, whose factor rows are one more ring entry.
+constexpr int W4_PAIR = 256;                     // columns of one ring entry
+constexpr int W4_DIRECT_TOKENS = 4;              // tokens whose x is read without LDS
+constexpr int W4_OPS = 3;                        // DMA instructions per entry
+constexpr int W4_SCALES = 2048;                  // entry: 16 rows x 128 B of codes, then
+constexpr int W4_ENTRY = 2048 + 256;             // 16 rows x 12 B holding 8 B of scales
+constexpr int W4_RINGS = 48 * W4_ENTRY;          // all waves' rings
+// LDS of a block of NW waves and T token tiles: the rings, the waves' sums (of two
+// tiles in turn where T is 1), the deltas likewise and the tokens' u.  Before the
+// rings start, x passes through it all.
+template <int NW, int T>
+struct W4Lds {
+  static constexpr int DEPTH = 48 / NW;                        // ring entries per wave
+  static constexpr int TURNS = T == 1 ? 2 : 1;
+  static constexpr int JOIN = W4_RINGS;                        // [TURNS][NW][T][64] f32x4
+  static constexpr int DELTA = JOIN + TURNS * NW * T * 64 * 16;   // [TURNS][16 T tokens][16 rows] f32
+  static constexpr int U = DELTA + TURNS * T * 16 * 16 * 4;    // [16 T tokens][64] f32
+  static constexpr int BYTES = U + T * 16 * 64 * 4;
+  static constexpr int X = BYTES / NW / 4096 * 4096;           // a wave's part for x
+  static_assert(X >= 8192, "a pair of 16 tokens' x");
+  static_assert(BYTES <= 160 * 1024, "one block a CU");
+};
+
 struct W4Delta {
   const uint16_t* B_pack;   // null: no adapters
   const float* u;
@@ -136,111 +165,316 @@ struct W4Delta {
   int32_t max_rank;
 };
 
-template <int R, int T, bool X8>
-__global__ __launch_bounds__(64 * W4_WAVES) void w4_product_kernel(
-    int n, int d_in, int d_out, const void* __restrict__ x_, const uint8_t* __restrict__ xs,
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, W4Delta dl,
-    uint16_t* __restrict__ y) {
-  extern __shared__ f32x4 join[];   // [W4_WAVES][R * T][64]
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+// One LDS-DMA per lane, global (base + voff) -> LDS (m0v + lane * size).
+__device__ __forceinline__ void dma16(uint32_t voff, const void* base, uint32_t m0v) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0v), "v"(voff), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ void dma4(uint32_t voff, const void* base, uint32_t m0v) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(m0v), "v"(voff), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+struct W4Args {
+  const uint8_t* x;        // bf16, or e4m3 codes
+  const uint8_t* xs;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  uint16_t* y;
+  W4Delta dl;
+  int32_t n, d_in, d_out;
+  int32_t row_blocks;      // blocks that split the row tiles; the grid is these times the token tiles
+};
+
+// NW waves, each holding the x of P pairs of 16 T tokens.  LONG: d_in beyond what
+// the waves can hold of x; they then take it in phases and read their x again for
+// every tile.
+template <int NW, int P, int T, bool X8, bool LONG>
+__global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  using M = W4Lds<NW, T>;
+  constexpr int TOKS = (16 * T + NW - 1) / NW;   // most tokens whose delta a wave owns
+  static_assert(TOKS <= 2, "the delta entries of a tile");
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 15, g = lane >> 4;
-  const int row0 = blockIdx.x * 16 * R, tok0 = blockIdx.y * 16 * T;
-  const int chunks = (d_in + W4_CHUNK - 1) / W4_CHUNK;
-  const int per = (chunks + W4_WAVES - 1) / W4_WAVES;
-  const int c0 = w * per, c1 = min(chunks, c0 + per);
-  f32x4 acc[R][T];
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int t = 0; t < T; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // this block's tiles: rb, rb + row_blocks, ... (blocks that run together read
+  // neighbouring rows)
+  const int rb = blockIdx.x % a.row_blocks, tok0 = (blockIdx.x / a.row_blocks) * 16 * T;
+  const int n_tiles = (a.d_out / 16 - rb + a.row_blocks - 1) / a.row_blocks;
+  const int toks = min(a.n - tok0, 16 * T);
+  const int half = a.d_in / 2;          // bytes of a row of codes
+  const int blocks = a.d_in / 32;       // scale bytes of a row
+  const int pairs = (a.d_in + W4_PAIR - 1) / W4_PAIR;
+  const int phases = LONG ? (pairs + NW * P - 1) / (NW * P) : 1;
+  // pair j of this wave is (j / P * NW + w) * P + j % P
+  const int last = pairs - ((phases - 1) * NW + w) * P;
+  const int mine = (phases - 1) * P + min(max(last, 0), P);
 
-#pragma unroll 2
-  for (int c = c0; c < c1; ++c) {
-    const int k = c * W4_CHUNK + g * 32;
-    const bool kin = k < d_in;   // d_in is a multiple of 64: the last step may be half
-    uint4 wc[R];
-    float ws[R];
+  // x fragments: lane (l, g) of chunk h of a pair holds scale block 8 q + 4 h + g of
+  // token l of a token tile.  Lanes past the last token take the last one's (their
+  // columns of the product are separate and never stored); blocks past d_in are zeros.
+  bf16x8 xf[T][P][2][4];
+  auto put_x = [&](int t, int i, int h, bool in, const uint4* v, float sc) {
+    if constexpr (X8) {
+      xf[t][i][h][0] = x8_widen(v[0].x, v[0].y, sc);
+      xf[t][i][h][1] = x8_widen(v[0].z, v[0].w, sc);
+      xf[t][i][h][2] = x8_widen(v[1].x, v[1].y, sc);
+      xf[t][i][h][3] = x8_widen(v[1].z, v[1].w, sc);
+    } else {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int64_t row = row0 + 16 * i + l;
-      wc[i] = kin ? *(const uint4*)(codes + (row * d_in + k) / 2) : make_uint4(0, 0, 0, 0);
-      ws[i] = __int_as_float((kin ? (int)scales[(row * d_in + k) / 32] : 127) << 23);
+      for (int q = 0; q < 4; ++q) xf[t][i][h][q] = as_bf16x8(v[q]);
     }
+    if (!in) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) xf[t][i][h][q] = as_bf16x8(make_uint4(0, 0, 0, 0));
+    }
+  };
+  constexpr int XB = X8 ? 32 : 64;      // bytes of a scale block of x
+  auto x_scale = [&](int64_t t, int blk) {
+    return X8 ? __int_as_float((int)a.xs[t * blocks + blk] << 23) : 1.f;
+  };
+  auto load_x = [&](int ph) {           // straight from memory
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-      const int64_t tk = tok0 + 16 * t + l;
-      uint4 xv[4];
-      if (tk < n && kin) {
-        if (X8) {
-          const uint4* p = (const uint4*)((const uint8_t*)x_ + tk * d_in + k);
-          const float sc = e8m0(xs[(tk * d_in + k) / 32]);
-          const uint4 a = p[0], b = p[1];
-          xv[0] = __builtin_bit_cast(uint4, x8_widen(a.x, a.y, sc));
-          xv[1] = __builtin_bit_cast(uint4, x8_widen(a.z, a.w, sc));
-          xv[2] = __builtin_bit_cast(uint4, x8_widen(b.x, b.y, sc));
-          xv[3] = __builtin_bit_cast(uint4, x8_widen(b.z, b.w, sc));
-        } else {
-          const uint4* p = (const uint4*)((const uint16_t*)x_ + tk * d_in + k);
+      const int64_t tk = tok0 + min(16 * t + l, toks - 1);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) xv[q] = p[q];
-        }
-      } else {
+      for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) xv[q] = make_uint4(0, 0, 0, 0);
-      }
+        for (int h = 0; h < 2; ++h) {
+          const int blk = ((ph * NW + w) * P + i) * 8 + h * 4 + g;
+          const int at = min(blk, blocks - 1);
+          const uint4* p = (const uint4*)(a.x + (tk * blocks + at) * XB);
+          uint4 v[XB / 16];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const uint32_t cw[4] = {wc[i].x, wc[i].y, wc[i].z, wc[i].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          acc[i][t] = mfma16(w4_widen(cw[q], ws[i]), as_bf16x8(xv[q]), acc[i][t]);
-      }
-    }
-  }
-
-  // the LoRA delta's part of wave w: rank columns 8w .. 8w + 7
-  if (dl.B_pack) {
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int tk = tok0 + 16 * t + l;
-      if (tk >= n) continue;
-      const W4Token tm = dl.tok[tk];
-      if (8 * w >= tm.rank) continue;
-      const float4* up = (const float4*)(dl.u + (int64_t)tk * dl.max_rank + 8 * w);
-      const float4 ua = up[0], ub = up[1];
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t row = row0 + 16 * i + 4 * g + e;
-          const uint4 b = *(const uint4*)(dl.B_pack + tm.b_off + row * tm.rank + 8 * w);
-          float s = ua.x * bf2f_lo(b.x);
-          s += ua.y * bf2f_hi(b.x);
-          s += ua.z * bf2f_lo(b.y);
-          s += ua.w * bf2f_hi(b.y);
-          s += ub.x * bf2f_lo(b.z);
-          s += ub.y * bf2f_hi(b.z);
-          s += ub.z * bf2f_lo(b.w);
-          s += ub.w * bf2f_hi(b.w);
-          acc[i][t][e] += s;
+          for (int q = 0; q < XB / 16; ++q) v[q] = p[q];
+          put_x(t, i, h, blk < blocks, v, x_scale(tk, at));
         }
     }
+  };
+  // through LDS, some pairs at a time: whole lines of a token's row, its 16-byte pieces
+  // swizzled by token so that the 16 lanes of a group read 16 different banks
+  auto stage_x = [&]() {
+    constexpr int PIECES = 8 * XB / 16;            // of a token's row in a pair
+    constexpr int ROWS = kWave / PIECES;           // tokens per instruction
+    constexpr int PAIR = 16 * PIECES * 16;         // bytes of a pair of 16 tokens
+    constexpr int ROUND = M::X / PAIR;             // of them that fit at a time
+    char* mem = lds + w * M::X;
+    const uint32_t m0v = lds_at(mem);
+    const uint8_t* base = a.x + (int64_t)tok0 * blocks * XB;
+    const uint32_t end = (uint32_t)blocks * XB - 16;
+    const int s = lane % PIECES;
+#pragma unroll
+    for (int i0 = 0; i0 < T * P; i0 += ROUND) {
+#pragma unroll
+      for (int i = i0; i < T * P && i < i0 + ROUND; ++i)
+#pragma unroll
+        for (int m = 0; m < 16 / ROWS; ++m) {
+          const int t = m * ROWS + lane / PIECES;
+          dma16(min(i / P * 16 + t, toks - 1) * (uint32_t)(blocks * XB) +
+                    min((uint32_t)((w * P + i % P) * PIECES + (s ^ t)) * 16, end),
+                base, m0v + (i - i0) * PAIR + m * 1024);
+        }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int i = i0; i < T * P && i < i0 + ROUND; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int blk = (w * P + i % P) * 8 + h * 4 + g;
+          uint4 v[XB / 16];
+#pragma unroll
+          for (int k = 0; k < XB / 16; ++k)
+            v[k] = *(const uint4*)(mem + (i - i0) * PAIR +
+                                   (l * PIECES + (((h * 4 + g) * (XB / 16) + k) ^ l)) * 16);
+          put_x(i / P, i % P, h, blk < blocks, v,
+                x_scale(tok0 + min(i / P * 16 + l, toks - 1), min(blk, blocks - 1)));
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    asm volatile("s_barrier" ::: "memory");        // the rings overlap other waves' parts
+  };
+  const bool staged = !LONG && toks > W4_DIRECT_TOKENS;
+  if (staged) stage_x();
+
+  char* ring = lds + w * (M::DEPTH * W4_ENTRY);
+  const uint32_t ring0 = lds_at(ring);
+  // what this lane fetches of an entry: the 16-byte pieces of row r8 (+ 8) that its
+  // slot holds (pieces are swizzled by row, see lds_sw), and a word of scales
+  const uint32_t r8 = lane >> 3;
+  const uint32_t off0 = r8 * half + ((lane & 7) ^ lds_sw(r8)) * 16;
+  const uint32_t off1 = (r8 + 8) * half + ((lane & 7) ^ lds_sw(r8 + 8)) * 16;
+  const int srow = min(lane / 3, 15);
+  const uint32_t soff = ((srow * blocks) & ~3) + min(lane - srow * 3, 2) * 4;
+  int rank[TOKS];
+  const uint16_t* B[TOKS];
+  int per_tile = mine, total = mine * n_tiles;     // (deltas are added below)
+  int it = 0, ij = 0, issued = 0;                  // the next entry to issue
+  uint32_t islot = ring0;
+  const uint8_t* cbase = a.codes + (int64_t)rb * 16 * half;
+  const uint8_t* sbase = a.scales + (int64_t)rb * 16 * blocks;
+  auto next_tile = [&]() {
+    ij = 0;
+    ++it;
+    cbase += (int64_t)a.row_blocks * 16 * half;
+    sbase += (int64_t)a.row_blocks * 16 * blocks;
+  };
+  auto issue_next = [&]() {
+    if (ij < mine) {
+      const uint32_t q = LONG ? (ij / P * NW + w) * P + ij % P : w * P + ij;
+      // (pieces past the row's end take its last one: their x is zero)
+      dma16(min(off0 + q * 128, (r8 + 1) * half - 16), cbase, islot);
+      dma16(min(off1 + q * 128, (r8 + 9) * half - 16), cbase, islot + 1024);
+      dma4(min(soff + q * 8, 16 * blocks - 4), sbase, islot + W4_SCALES);
+    } else {   // a token's 16 factor rows: at most 2 KB
+      int r = rank[0];
+      const uint16_t* b = B[0];
+      if (TOKS > 1 && (ij > mine || r == 0)) {
+        r = rank[TOKS - 1];
+        b = B[TOKS - 1];
+      }
+      const uint16_t* base = b + ((int64_t)rb + (int64_t)it * a.row_blocks) * 16 * r;
+      dma16(min(lane * 16, r * 32 - 16), base, islot);
+      dma16(min(lane * 16 + 1024, r * 32 - 16), base, islot + 1024);
+      dma4(0, base, islot + W4_SCALES);   // (the third instruction of an entry)
+    }
+    ++issued;
+    islot += W4_ENTRY;
+    if (islot == ring0 + M::DEPTH * W4_ENTRY) islot = ring0;
+    if (++ij == per_tile) next_tile();
+  };
+  // the first tile's codes are on their way before the adapters are looked up
+  if (a.dl.B_pack) {
+    per_tile = mine + TOKS;   // (no next tile yet)
+    total = min(total, mine);
+  }
+  while (issued < M::DEPTH && issued < total) issue_next();
+
+  // the delta's tokens of this wave: w + i NW
+  int deltas = 0;
+  float* u = (float*)(lds + M::U);
+  float* delta = (float*)(lds + M::DELTA);
+#pragma unroll
+  for (int i = 0; i < TOKS; ++i) {
+    const int t = w + i * NW;
+    rank[i] = 0;
+    B[i] = nullptr;
+    if (a.dl.B_pack && t < toks) {
+      const W4Token tm = a.dl.tok[tok0 + t];
+      rank[i] = __builtin_amdgcn_readfirstlane(tm.rank);
+      B[i] = a.dl.B_pack + uniform64(tm.b_off);
+      u[t * 64 + lane] = lane < rank[i] ? a.dl.u[(int64_t)(tok0 + t) * a.dl.max_rank + lane] : 0.f;
+    }
+    deltas += rank[i] > 0 ? 1 : 0;
+    if (t < 16 * T && lane < 16 * M::TURNS)   // zeros stay where a token has no delta
+      delta[((lane >> 4) * 16 * T + t) * 16 + (lane & 15)] = 0.f;
+  }
+  per_tile = mine + deltas;
+  if (ij == per_tile) next_tile();   // no delta here
+  total = per_tile * n_tiles;
+  while (issued < M::DEPTH && issued < total) issue_next();
+  if (!LONG && !staged) {
+    load_x(0);
+    // x has landed here, by a vmcnt(0) that the compiler sees: a wait of its own at the
+    // first use, in the loop, would drain the ring there in every round
+    __builtin_amdgcn_s_waitcnt(0x0F70);
   }
 
+  float* join = (float*)(lds + M::JOIN);
+  const char* e = ring;
+  // Before an entry is read: while entries remain to be issued, exactly DEPTH - 1
+  // younger ones are in flight; at the end all that remain are waited for.
+  auto wait_entry = [&]() {
+    if (issued < total) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W4_OPS * (M::DEPTH - 1)) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+  auto next_entry = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the slot is refilled
+    e += W4_ENTRY;
+    if (e == ring + M::DEPTH * W4_ENTRY) e = ring;
+    if (issued < total) issue_next();
+  };
+  for (int tile = 0; tile < n_tiles; ++tile) {
+    const int turn = M::TURNS == 2 ? tile & 1 : 0;
+    f32x4 acc[T][2];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+    for (int t = 0; t < T; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int ph = 0; ph < phases; ++ph) {
+      if (LONG) load_x(ph);
 #pragma unroll
-    for (int t = 0; t < T; ++t) join[(w * R * T + i * T + t) * 64 + lane] = acc[i][t];
-  __syncthreads();
-  for (int it = threadIdx.x; it < R * T * 64; it += 64 * W4_WAVES) {
-    f32x4 s = join[it];
+      for (int i = 0; i < P; ++i) {
+        if (ph * P + i >= mine) break;
+        const int q = (ph * NW + w) * P + i;
+        wait_entry();
+        uint4 cw[2];
+        int sc[2];
 #pragma unroll
-    for (int v = 1; v < W4_WAVES; ++v) s += join[v * R * T * 64 + it];
-    const int ln = it & 63, i = (it >> 6) / T, t = (it >> 6) % T;
-    const int64_t tk = tok0 + 16 * t + (ln & 15);
-    if (tk < n)
-      *(uint2*)(y + tk * d_out + row0 + 16 * i + 4 * (ln >> 4)) =
-          make_uint2(pack2bf(s[0], s[1]), pack2bf(s[2], s[3]));
+        for (int h = 0; h < 2; ++h) {
+          cw[h] = *(const uint4*)(e + (l * 8 + ((4 * h + g) ^ lds_sw(l))) * 16);
+          // a row's own bytes only: those past its end may be another row's NaN
+          sc[h] = *(const uint8_t*)(e + W4_SCALES + l * 12 + ((l * blocks) & 2) +
+                                    min(4 * h + g, blocks - 1 - q * 8));
+        }
+        next_entry();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t c[4] = {cw[h].x, cw[h].y, cw[h].z, cw[h].w};
+            const bf16x8 wf = w4_widen(c[k], __int_as_float(sc[h] << 23));
+#pragma unroll
+            for (int t = 0; t < T; ++t) acc[t][h] = mfma16(wf, xf[t][i][h][k], acc[t][h]);
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TOKS; ++i) {
+      // a token's delta: four lanes a row, 8 ranks and the 8 that lie 32 further each
+      if (rank[i] == 0) continue;
+      wait_entry();
+      const int row = lane >> 2, j = (lane & 3) * 8;
+      const float* ui = u + (w + i * NW) * 64;
+      float s = 0.f;
+#pragma unroll 1
+      for (int k = j; k < rank[i]; k += 32) {
+        const uint4 b = *(const uint4*)(e + (row * rank[i] + k) * 2);
+        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          s += ui[k + 2 * q] * bf2f_lo(bw[q]);
+          s += ui[k + 2 * q + 1] * bf2f_hi(bw[q]);
+        }
+      }
+      next_entry();
+      s += __shfl_xor(s, 1, kWave);
+      s += __shfl_xor(s, 2, kWave);
+      if ((lane & 3) == 0) delta[(turn * 16 * T + w + i * NW) * 16 + row] = s;
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      ((f32x4*)join)[((turn * NW + w) * T + t) * 64 + lane] = acc[t][0] + acc[t][1];
+    // writes of this tile visible to all; the other buffer is free again after it.
+    // The DMA in flight is not waited for.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (w < 4 * T) {   // output 64 w + lane: of accumulator lane i / 4 of tile t, its row i % 4
+      const int t = w / 4, i = (w % 4) * 64 + lane, al = i >> 2;
+      const float* p = join + (turn * NW * T + t) * 256 + i;
+      float s = p[0];
+#pragma unroll 5
+      for (int v = 1; v < NW; ++v) s += p[v * T * 256];
+      const int tk = 16 * t + (al & 15), row = 4 * (al >> 4) + (i & 3);
+      if (a.dl.B_pack) s += delta[(turn * 16 * T + tk) * 16 + row];
+      const float s1 = __shfl_xor(s, 1, kWave);
+      if ((lane & 1) == 0 && tk < toks)
+        *(uint32_t*)(a.y + (int64_t)(tok0 + tk) * a.d_out + (rb + tile * a.row_blocks) * 16 + row) =
+            pack2bf(s, s1);
+    }
+    if (M::TURNS == 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 }
 
@@ -310,36 +544,49 @@ size_t w4_ws_bytes(int64_t n, int max_rank) {
   return cv.used;
 }
 
-template <int R, int T, bool X8>
-static lora_status product(int n, int d_in, int d_out, const void* x, const uint8_t* xs,
-                           const uint8_t* codes, const uint8_t* scales, const W4Delta& dl,
-                           uint16_t* y, hipStream_t s) {
-  constexpr int lds = W4_WAVES * R * T * 64 * (int)sizeof(f32x4);
-  static const hipError_t attr = hipFuncSetAttribute((const void*)w4_product_kernel<R, T, X8>,
+template <int NW, int P, int T, bool X8, bool LONG>
+static lora_status product(W4Args a, hipStream_t s) {
+  // the dynamic LDS bound, raised once (a thread-safe one-time initialisation, then read-only)
+  constexpr int lds = W4Lds<NW, T>::BYTES;
+  static const hipError_t attr = hipFuncSetAttribute((const void*)w4_product_kernel<NW, P, T, X8, LONG>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   TRY_HIP(attr);
-  hipLaunchKernelGGL((w4_product_kernel<R, T, X8>),
-                     dim3((unsigned)(d_out / (16 * R)), (unsigned)cdiv(n, 16 * T)),
-                     dim3(64 * W4_WAVES), lds, s, n, d_in, d_out, x, xs, codes, scales, dl, y);
+  // One block per CU: the token tiles times as many row blocks as that leaves, a
+  // multiple of 8 (the XCDs) where there is more than one token tile, so that the
+  // token tiles of the same rows share an XCD's L2.
+  const int64_t tok_tiles = cdiv(a.n, 16 * T);
+  int64_t rb = std::max<int64_t>(1, device_cus() / tok_tiles);
+  if (tok_tiles > 1 && rb >= 8) rb &= ~(int64_t)7;
+  a.row_blocks = (int)std::min<int64_t>(rb, a.d_out / 16);
+  hipLaunchKernelGGL((w4_product_kernel<NW, P, T, X8, LONG>), dim3((unsigned)(a.row_blocks * tok_tiles)),
+                     dim3(64 * NW), lds, s, a);
   return launch_check("w4_product");
 }
 
+// The fewest registers of x that hold d_in: 16 waves with one or two pairs each,
+// 8 with five or six.  Two token tiles a block where one pair leaves room.
 template <bool X8>
-static lora_status product_for(int n, int d_in, int d_out, const void* x, const uint8_t* xs,
-                               const uint8_t* codes, const uint8_t* scales, const W4Delta& dl,
-                               uint16_t* y, hipStream_t s) {
-  if (n <= 16) return product<1, 1, X8>(n, d_in, d_out, x, xs, codes, scales, dl, y, s);
-  if (n <= 32) return product<1, 2, X8>(n, d_in, d_out, x, xs, codes, scales, dl, y, s);
-  if (n <= 64) return product<1, 4, X8>(n, d_in, d_out, x, xs, codes, scales, dl, y, s);
-  return product<4, 4, X8>(n, d_in, d_out, x, xs, codes, scales, dl, y, s);
+static lora_status product_for(const W4Args& a, hipStream_t s) {
+  const int64_t pairs = cdiv(a.d_in, W4_PAIR);
+  if (pairs <= 16)
+    return a.n > 16 ? product<16, 1, 2, X8, false>(a, s) : product<16, 1, 1, X8, false>(a, s);
+  if (pairs <= 32) return product<16, 2, 1, X8, false>(a, s);
+  if (pairs <= 40) return product<8, 5, 1, X8, false>(a, s);
+  if (pairs <= 48) return product<8, 6, 1, X8, false>(a, s);
+  return product<8, 4, 1, X8, true>(a, s);
+}
+
+static lora_status launch_product(int64_t n, int64_t d_in, int64_t d_out, const void* x,
+                                  const uint8_t* xs, const uint8_t* codes, const uint8_t* scales,
+                                  const W4Delta& dl, uint16_t* y, hipStream_t s) {
+  const W4Args a{(const uint8_t*)x, xs, codes, scales, y, dl, (int)n, (int)d_in, (int)d_out, 0};
+  return xs ? product_for<true>(a, s) : product_for<false>(a, s);
 }
 
 lora_status launch_w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
                              const uint8_t* xs, const uint8_t* codes, const uint8_t* scales,
                              uint16_t* y, hipStream_t s) {
-  const W4Delta none{};
-  return xs ? product_for<true>((int)n, (int)d_in, (int)d_out, x, xs, codes, scales, none, y, s)
-            : product_for<false>((int)n, (int)d_in, (int)d_out, x, xs, codes, scales, none, y, s);
+  return launch_product(n, d_in, d_out, x, xs, codes, scales, W4Delta{}, y, s);
 }
 
 lora_status launch_lora_w4(const lora_shape& sh, const void* x, const uint8_t* xs,
@@ -363,8 +610,7 @@ lora_status launch_lora_w4(const lora_shape& sh, const void* x, const uint8_t* x
   lora_status st = launch_check("w4_shrink");
   if (st != LORA_OK) return st;
   const W4Delta dl{B_pack, u, tok, sh.max_rank};
-  return xs ? product_for<true>(n, d_in, d_out, x, xs, codes, scales, dl, y, s)
-            : product_for<false>(n, d_in, d_out, x, xs, codes, scales, dl, y, s);
+  return launch_product(n, d_in, d_out, x, xs, codes, scales, dl, y, s);
 }
 
 }  // namespace lora_host
