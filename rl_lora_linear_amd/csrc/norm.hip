@@ -14,6 +14,8 @@
 // of one block that join their sums through LDS.  Teams step over the rows
 // with the grid's stride, so a block reads the weight once.  The team of a row
 // depends on `hidden` alone: a row's bits do not change with the batch.
+#include <type_traits>
+
 #include "common.hpp"
 #include "sgmv.hpp"
 
@@ -24,8 +26,14 @@ constexpr int NORM_SMALL_BLOCK = 256;
 
 // Columns c..c+7 of a row: one 16-byte access where every row is 16-byte
 // aligned (hidden a multiple of 8), else element by element up to column H.
-template <bool VEC>
+// NT: a non-temporal access, see norm_streams.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool VEC, bool NT = false>
 __device__ __forceinline__ uint4 norm_load8(const uint16_t* row, int c, int H) {
+  if (VEC && NT) {
+    const u32x4 v = __builtin_nontemporal_load((const u32x4*)(row + c));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
   if (VEC) return *(const uint4*)(row + c);
   uint32_t r[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -33,8 +41,12 @@ __device__ __forceinline__ uint4 norm_load8(const uint16_t* row, int c, int H) {
     if (c + i < H) r[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
-template <bool VEC>
+template <bool VEC, bool NT>
 __device__ __forceinline__ void norm_store8(uint16_t* row, int c, int H, uint4 v) {
+  if (VEC && NT) {
+    __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, (u32x4*)(row + c));
+    return;
+  }
   if (VEC) {
     *(uint4*)(row + c) = v;
     return;
@@ -104,8 +116,8 @@ __device__ __forceinline__ uint2 quantize8(const float* v, int& scale_byte) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-template <int VPL, bool VEC, bool Q8>
-__global__ __launch_bounds__(1024) void rmsnorm_fwd_kernel(
+template <int VPL, bool VEC, bool NT, bool Q8>
+__global__ __launch_bounds__(VPL == 1 ? NORM_SMALL_BLOCK : 1024) void rmsnorm_fwd_kernel(
     int64_t n, int H, int team, const uint16_t* x, const uint16_t* res,
     const uint16_t* __restrict__ weight, float eps, uint16_t* h, uint16_t* y,
     uint8_t* __restrict__ q, uint8_t* __restrict__ qs, float* __restrict__ rstd_out) {
@@ -122,19 +134,18 @@ __global__ __launch_bounds__(1024) void rmsnorm_fwd_kernel(
   int turn = 0;
   // every lane of a block runs the same number of rounds (the barriers below)
   for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < n; r0 += stride, turn ^= 1) {
-    const int64_t row = r0 + threadIdx.x / team;
+    const int64_t row = r0 + threadIdx.x / team, base = row * H;
     const bool live = row < n;
-    const int64_t base = row * H;
-    float f[VPL][8];
-    float ss = 0.f;
     uint4 xv[VPL], rv[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int c = (lane + v * team) * 8;
       const bool on = live && c < H;
-      xv[v] = on ? norm_load8<VEC>(x + base, c, H) : make_uint4(0, 0, 0, 0);
-      if (res) rv[v] = on ? norm_load8<VEC>(res + base, c, H) : make_uint4(0, 0, 0, 0);
+      xv[v] = on ? norm_load8<VEC, NT>(x + base, c, H) : make_uint4(0, 0, 0, 0);
+      if (res) rv[v] = on ? norm_load8<VEC, NT>(res + base, c, H) : make_uint4(0, 0, 0, 0);
     }
+    float f[VPL][8];
+    float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int c = (lane + v * team) * 8;
@@ -145,7 +156,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_fwd_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[v][i] += g[i];
         const uint4 hv = pack8(f[v]);
-        if (live && c < H) norm_store8<VEC>(h + base, c, H, hv);
+        if (live && c < H) norm_store8<VEC, NT>(h + base, c, H, hv);
         unpack8(hv, f[v]);   // the statistics are those of the stored h
       }
 #pragma unroll
@@ -169,7 +180,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_fwd_kernel(
           if ((lane & 3) == 0) qs[base / 32 + c / 32] = (uint8_t)b;
         }
       } else if (live && c < H) {
-        norm_store8<VEC>(y + base, c, H, pack8(o));
+        norm_store8<VEC, NT>(y + base, c, H, pack8(o));
       }
     }
   }
@@ -177,12 +188,15 @@ __global__ __launch_bounds__(1024) void rmsnorm_fwd_kernel(
 
 // Backward.  With `partial`, each lane keeps its columns' dw terms over the
 // rows its team visits; the block's teams are joined through LDS in team order
-// and the block writes one row of partial [gridDim.x][H].
-template <int VPL, bool VEC>
-__global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(
+// and the block writes one row of partial [gridDim.x][H].  A row of more than
+// 16384 columns does not fit the registers beside dw: it is read again, from the
+// caches, once its sum is known.
+template <int VPL, bool VEC, bool NT>
+__global__ __launch_bounds__(VPL == 1 ? NORM_SMALL_BLOCK : 1024) void rmsnorm_bwd_kernel(
     int64_t n, int H, int team, const uint16_t* dy, const uint16_t* dh,
     const uint16_t* __restrict__ h, const uint16_t* __restrict__ weight,
     const float* __restrict__ rstd_in, uint16_t* dx, float* __restrict__ partial) {
+  constexpr bool AGAIN = VPL == NORM_MAX_VPL;
   __shared__ float red[2][16];
   __shared__ float join[NORM_SMALL_BLOCK * 8];
   const int lane = threadIdx.x % team;
@@ -193,28 +207,41 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     const int c = (lane + v * team) * 8;
-    wv[v] = c < H ? norm_load8<VEC>(weight, c, H) : make_uint4(0, 0, 0, 0);
+    if (!AGAIN) wv[v] = c < H ? norm_load8<VEC>(weight, c, H) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
   }
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < n; r0 += stride, turn ^= 1) {
-    const int64_t row = r0 + threadIdx.x / team;
+    const int64_t row = r0 + threadIdx.x / team, base = row * H;
     const bool live = row < n;
-    const int64_t base = row * H;
     const float rstd = live ? rstd_in[row] : 0.f;
     uint4 dv[VPL], hv[VPL], uv[VPL];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
+    auto load = [&](int v) {
       const int c = (lane + v * team) * 8;
       const bool on = live && c < H;
-      dv[v] = on ? norm_load8<VEC>(dy + base, c, H) : make_uint4(0, 0, 0, 0);
-      hv[v] = on ? norm_load8<VEC>(h + base, c, H) : make_uint4(0, 0, 0, 0);
-      if (dh) uv[v] = on ? norm_load8<VEC>(dh + base, c, H) : make_uint4(0, 0, 0, 0);
-    }
+      dv[v] = on ? norm_load8<VEC, NT && !AGAIN>(dy + base, c, H) : make_uint4(0, 0, 0, 0);
+      hv[v] = on ? norm_load8<VEC, NT && !AGAIN>(h + base, c, H) : make_uint4(0, 0, 0, 0);
+      if (AGAIN) wv[v] = c < H ? norm_load8<VEC>(weight, c, H) : make_uint4(0, 0, 0, 0);
+    };
+    auto load_dh = [&](int v) {
+      const int c = (lane + v * team) * 8;
+      if (dh)
+        uv[v] = live && c < H ? norm_load8<VEC, NT>(dh + base, c, H) : make_uint4(0, 0, 0, 0);
+    };
+    if (!AGAIN)
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        load(v);
+        load_dh(v);
+      }
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
+      if (AGAIN) {
+        asm volatile("" ::: "memory");   // not all of the row's loads at once
+        load(v);
+      }
       float d[8], x[8], w[8];
       unpack8(dv[v], d);
       unpack8(hv[v], x);
@@ -229,6 +256,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(
     const float c1 = team_sum(s, team, red, turn) / (float)H;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
+      if (AGAIN) {
+        asm volatile("" ::: "memory");   // a second read, not a kept register
+        load(v);
+        load_dh(v);
+      }
       const int c = (lane + v * team) * 8;
       float d[8], x[8], w[8], u[8], o[8];
       unpack8(dv[v], d);
@@ -241,12 +273,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += u[i];
       }
-      if (live && c < H) norm_store8<VEC>(dx + base, c, H, pack8(o));
+      if (live && c < H) norm_store8<VEC, NT>(dx + base, c, H, pack8(o));
     }
   }
   if (!partial) return;
   float* out = partial + (int64_t)blockIdx.x * H;
-  if (team > kWave || per_block == 1) {
+  if (per_block == 1) {
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
 #pragma unroll
@@ -268,24 +300,48 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(
   }
 }
 
-// dw[c] (+)= sum over blocks of partial[b][c], in block order within each of 16
-// fixed groups and then in group order.  64 columns a block.
+// dw[c] (+)= sum over blocks of partial[b][c].  A block takes 32 columns (whole
+// 128-byte lines); its 128 groups of 8 lanes sum every 128th row, and the groups are
+// joined in a fixed order.
+constexpr int COLSUM_COLS = 32, COLSUM_GROUPS = 128;
+
 __global__ __launch_bounds__(1024) void norm_colsum_kernel(const float* __restrict__ partial,
                                                            int blocks, int H,
                                                            float* __restrict__ dw, int accumulate) {
-  __shared__ float s[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  float t = 0.f;
-  if (c < H)
+  __shared__ float s[COLSUM_GROUPS][COLSUM_COLS];
+  __shared__ float s2[32][COLSUM_COLS];
+  const int group = threadIdx.x / 8, c4 = (threadIdx.x % 8) * 4;
+  const int c = blockIdx.x * COLSUM_COLS + c4;
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+  const bool vec = (H & 3) == 0;   // rows 16-byte aligned
 #pragma unroll 4
-    for (int b = w; b < blocks; b += 16) t += partial[(int64_t)b * H + c];
-  s[w][lane] = t;
+  for (int b = group; b < blocks; b += COLSUM_GROUPS) {
+    const float* p = partial + (int64_t)b * H + c;
+    if (vec && c < H) {
+      const f32x4 v = *(const f32x4*)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] += v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < H) t[i] += p[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[group][c4 + i] = t[i];
   __syncthreads();
-  if (w != 0 || c >= H) return;
-  t = 0.f;
-  for (int k = 0; k < 16; ++k) t += s[k][lane];
-  dw[c] = accumulate ? dw[c] + t : t;
+  const int col = threadIdx.x % COLSUM_COLS, part = threadIdx.x / COLSUM_COLS;
+  float a = 0.f;
+#pragma unroll
+  for (int k = 0; k < COLSUM_GROUPS / 32; ++k) a += s[part * (COLSUM_GROUPS / 32) + k][col];
+  s2[part][col] = a;
+  __syncthreads();
+  const int out = blockIdx.x * COLSUM_COLS + col;
+  if (part != 0 || out >= H) return;
+  a = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) a += s2[k][col];
+  dw[out] = accumulate ? dw[out] + a : a;
 }
 
 }  // namespace lora
@@ -313,42 +369,54 @@ static unsigned norm_grid(int64_t n, const NormPlan& p, int64_t cap) {
   return (unsigned)std::max<int64_t>(1, std::min(cdiv(n, p.block / p.team), cap));
 }
 
-// Blocks that keep dw partials: 2^18 threads in all fill the chip's 256 CUs
-// with 16 waves each, and the partials stay under 16 MB.
-int64_t rmsnorm_bwd_blocks(int64_t n, int64_t hidden) {
-  const NormPlan p = norm_plan(hidden);
-  return norm_grid(n, p, std::max<int64_t>(1, (1 << 18) / p.block));
+// Blocks of a pass that keeps nothing: 2^20 threads in all, more than run at once.
+static unsigned norm_free_grid(int64_t n, const NormPlan& p) {
+  return norm_grid(n, p, std::max<int64_t>(1, (1 << 20) / p.block));
 }
 
-template <int VPL, bool VEC, bool Q8>
+// Blocks that keep dw partials: at least one a CU, and 2^17 threads in all (8 waves a
+// CU), so that the partials, written and read again, stay under 16 MB.
+int64_t rmsnorm_bwd_blocks(int64_t n, int64_t hidden) {
+  const NormPlan p = norm_plan(hidden);
+  return norm_grid(n, p, std::max<int64_t>(256, (1 << 17) / p.block));
+}
+
+// Calls that move more than 96 MB, three eighths of the last-level cache, make
+// non-temporal accesses: little of theirs would be found there again, and lines that
+// others wrote are not pushed out under their reads.  Forward / backward at 8192 x
+// 4096 (268 MB): 46.4 / 44.9 us, 50.0 / 50.5 with ordinary accesses; at 4096 rows 24.8 /
+// 23.7 against 26.3 / 26.6; at 2048 rows (67 MB, inputs in the cache) 13.7 / 13.7
+// against 12.2 / 13.0.
+static bool norm_streams(int64_t n, int64_t H, int arrays) {
+  return n * H * 2 * arrays > (int64_t)96 << 20;
+}
+
+template <int VPL, bool Q8>
 static void fwd_launch(const NormPlan& p, unsigned grid, int64_t n, int64_t H, const uint16_t* x,
                        const uint16_t* res, const uint16_t* w, float eps, uint16_t* h, uint16_t* y,
                        uint8_t* q, uint8_t* qs, float* rstd, hipStream_t s) {
-  hipLaunchKernelGGL((rmsnorm_fwd_kernel<VPL, VEC, Q8>), dim3(grid), dim3(p.block), 0, s, n, (int)H,
-                     p.team, x, res, w, eps, h, y, q, qs, rstd);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(p.block), 0, s, n, (int)H, p.team, x, res, w, eps, h,
+                       y, q, qs, rstd);
+  };
+  if (H % 8 != 0) go(rmsnorm_fwd_kernel<VPL, false, false, false>);
+  else if (norm_streams(n, H, res ? 4 : 2)) go(rmsnorm_fwd_kernel<VPL, true, true, Q8>);
+  else go(rmsnorm_fwd_kernel<VPL, true, false, Q8>);
 }
 
 lora_status launch_rmsnorm_fwd(int64_t n, int64_t H, const uint16_t* x, const uint16_t* res,
                                const uint16_t* w, float eps, uint16_t* h, uint16_t* y, uint8_t* q,
                                uint8_t* qs, float* rstd, hipStream_t s) {
   const NormPlan p = norm_plan(H);
-  const unsigned grid = norm_grid(n, p, std::max<int64_t>(1, (1 << 19) / p.block));
-  const bool vec = H % 8 == 0;
-#define LORA_NORM_FWD(V)                                                                      \
-  if (q)                                                                                      \
-    fwd_launch<V, true, true>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s);           \
-  else if (vec)                                                                               \
-    fwd_launch<V, true, false>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s);          \
-  else                                                                                        \
-    fwd_launch<V, false, false>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s)
-  if (p.vpl == 1) {
-    LORA_NORM_FWD(1);
-  } else if (p.vpl == 2) {
-    LORA_NORM_FWD(2);
-  } else {
-    LORA_NORM_FWD(4);
-  }
-#undef LORA_NORM_FWD
+  const unsigned grid = norm_free_grid(n, p);
+  const auto go = [&](auto vpl) {
+    constexpr int V = decltype(vpl)::value;
+    if (q) fwd_launch<V, true>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s);
+    else fwd_launch<V, false>(p, grid, n, H, x, res, w, eps, h, y, q, qs, rstd, s);
+  };
+  if (p.vpl == 1) go(std::integral_constant<int, 1>{});
+  else if (p.vpl == 2) go(std::integral_constant<int, 2>{});
+  else go(std::integral_constant<int, NORM_MAX_VPL>{});
   return launch_check("rmsnorm_fwd");
 }
 
@@ -356,12 +424,13 @@ template <int VPL>
 static void bwd_launch(const NormPlan& p, unsigned grid, int64_t n, int64_t H, const uint16_t* dy,
                        const uint16_t* dh, const uint16_t* h, const uint16_t* w, const float* rstd,
                        uint16_t* dx, float* partial, hipStream_t s) {
-  if (H % 8 == 0)
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<VPL, true>), dim3(grid), dim3(p.block), 0, s, n, (int)H,
-                       p.team, dy, dh, h, w, rstd, dx, partial);
-  else
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<VPL, false>), dim3(grid), dim3(p.block), 0, s, n, (int)H,
-                       p.team, dy, dh, h, w, rstd, dx, partial);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(p.block), 0, s, n, (int)H, p.team, dy, dh, h, w, rstd,
+                       dx, partial);
+  };
+  if (H % 8 != 0) go(rmsnorm_bwd_kernel<VPL, false, false>);
+  else if (norm_streams(n, H, dh ? 4 : 3)) go(rmsnorm_bwd_kernel<VPL, true, true>);
+  else go(rmsnorm_bwd_kernel<VPL, true, false>);
 }
 
 lora_status launch_rmsnorm_bwd(int64_t n, int64_t H, const uint16_t* dy, const uint16_t* dh,
@@ -369,17 +438,14 @@ lora_status launch_rmsnorm_bwd(int64_t n, int64_t H, const uint16_t* dy, const u
                                uint16_t* dx, float* dw, int accumulate, float* partial,
                                hipStream_t s) {
   const NormPlan p = norm_plan(H);
-  const unsigned grid = dw ? (unsigned)rmsnorm_bwd_blocks(n, H)
-                           : norm_grid(n, p, std::max<int64_t>(1, (1 << 19) / p.block));
-  if (p.vpl == 1)
-    bwd_launch<1>(p, grid, n, H, dy, dh, h, w, rstd, dx, dw ? partial : nullptr, s);
-  else if (p.vpl == 2)
-    bwd_launch<2>(p, grid, n, H, dy, dh, h, w, rstd, dx, dw ? partial : nullptr, s);
-  else
-    bwd_launch<4>(p, grid, n, H, dy, dh, h, w, rstd, dx, dw ? partial : nullptr, s);
+  const unsigned grid = dw ? (unsigned)rmsnorm_bwd_blocks(n, H) : norm_free_grid(n, p);
+  float* part = dw ? partial : nullptr;
+  if (p.vpl == 1) bwd_launch<1>(p, grid, n, H, dy, dh, h, w, rstd, dx, part, s);
+  else if (p.vpl == 2) bwd_launch<2>(p, grid, n, H, dy, dh, h, w, rstd, dx, part, s);
+  else bwd_launch<NORM_MAX_VPL>(p, grid, n, H, dy, dh, h, w, rstd, dx, part, s);
   lora_status st = launch_check("rmsnorm_bwd");
   if (st != LORA_OK || !dw) return st;
-  hipLaunchKernelGGL(norm_colsum_kernel, dim3((unsigned)cdiv(H, 64)), dim3(1024), 0, s, partial,
+  hipLaunchKernelGGL(norm_colsum_kernel, dim3((unsigned)cdiv(H, COLSUM_COLS)), dim3(1024), 0, s, partial,
                      (int)grid, (int)H, dw, accumulate);
   return launch_check("norm_colsum");
 }
