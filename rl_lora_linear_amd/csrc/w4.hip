@@ -21,11 +21,12 @@ namespace lora {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ float e8m0(int byte) {   // 0 is 2^-127 (a subnormal), 255 is NaN
-  return __int_as_float(byte == 0 ? 0x400000 : byte == 255 ? 0x7FC00000 : byte << 23);
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
+                                         __builtin_bit_cast(bf16x2, b), c, false);
 }
 // Codes 2i, 2i + 1 of four bytes as a bf16 pair, times 2^(byte - 127); `scale` has the
-// scale byte as its exponent field.
+// scale byte as its exponent field (the unit takes that field alone: 0 is 2^-127, 255 NaN).
 template <int I>
 __device__ __forceinline__ uint32_t w4_pair(uint32_t codes, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));
@@ -96,28 +97,27 @@ __global__ __launch_bounds__(64 * W4S_WAVES) void w4_shrink_kernel(
     if (ad.sorted && t > 0 && ad.ids[t - 1] > id) set_flag(status, LORA_FLAG_UNSORTED);
   }
   if (j >= ad.max_rank) return;
-  float s = 0.f;
+  float s = 0.f, s1 = 0.f;
   if (j < rank) {
     const uint16_t* a = ad.A_pack + d.a_off + (int64_t)j * d_in;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = lane * 8; k < d_in; k += 512) {
       const uint4 av = *(const uint4*)(a + k);
       uint4 xv;
       if (X8) {
         const uint2 c = *(const uint2*)((const uint8_t*)x_ + (int64_t)t * d_in + k);
-        const float sc = e8m0(xs[((int64_t)t * d_in + k) / 32]);
-        const bf16x8 w = x8_widen(c.x, c.y, sc);
-        xv = __builtin_bit_cast(uint4, w);
+        const float sc = __int_as_float((int)xs[((int64_t)t * d_in + k) / 32] << 23);
+        xv = __builtin_bit_cast(uint4, x8_widen(c.x, c.y, sc));
       } else {
         xv = *(const uint4*)((const uint16_t*)x_ + (int64_t)t * d_in + k);
       }
-      const uint32_t aw[4] = {av.x, av.y, av.z, av.w}, xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        s += bf2f_lo(aw[q]) * bf2f_lo(xw[q]);
-        s += bf2f_hi(aw[q]) * bf2f_hi(xw[q]);
-      }
+      // two exact products and an fp32 sum per instruction
+      s = dot2(av.x, xv.x, s);
+      s1 = dot2(av.y, xv.y, s1);
+      s = dot2(av.z, xv.z, s);
+      s1 = dot2(av.w, xv.w, s1);
     }
+    s += s1;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, kWave);
     s *= d.scale;
