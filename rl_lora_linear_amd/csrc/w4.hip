@@ -195,8 +195,8 @@ struct W4Args {
 
 // NW waves, each holding the x of P pairs of 16 T tokens.  LONG: d_in beyond what
 // the waves can hold of x; they then take it in phases and read their x again for
-// every tile.
-template <int NW, int P, int T, bool X8, bool LONG>
+// every tile.  DELTA: with adapters.
+template <int NW, int P, int T, bool X8, bool LONG, bool DELTA>
 __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   using M = W4Lds<NW, T>;
@@ -318,19 +318,15 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   uint32_t islot = ring0;
   const uint8_t* cbase = a.codes + (int64_t)rb * 16 * half;
   const uint8_t* sbase = a.scales + (int64_t)rb * 16 * blocks;
-  auto next_tile = [&]() {
-    ij = 0;
-    ++it;
-    cbase += (int64_t)a.row_blocks * 16 * half;
-    sbase += (int64_t)a.row_blocks * 16 * blocks;
-  };
+  const int64_t cstep = (int64_t)a.row_blocks * 16 * half, sstep = (int64_t)a.row_blocks * 16 * blocks;
+  const uint32_t row_end = half - 16, scale_end = 16 * blocks - 4;
   auto issue_next = [&]() {
-    if (ij < mine) {
+    if (!DELTA || ij < mine) {
       const uint32_t q = LONG ? (ij / P * NW + w) * P + ij % P : w * P + ij;
       // (pieces past the row's end take its last one: their x is zero)
-      dma16(min(off0 + q * 128, (r8 + 1) * half - 16), cbase, islot);
-      dma16(min(off1 + q * 128, (r8 + 9) * half - 16), cbase, islot + 1024);
-      dma4(min(soff + q * 8, 16 * blocks - 4), sbase, islot + W4_SCALES);
+      dma16(min(off0 + q * 128, r8 * half + row_end), cbase, islot);
+      dma16(min(off1 + q * 128, (r8 + 8) * half + row_end), cbase, islot + 1024);
+      dma4(min(soff + q * 8, scale_end), sbase, islot + W4_SCALES);
     } else {   // a token's 16 factor rows: at most 2 KB
       int r = rank[0];
       const uint16_t* b = B[0];
@@ -344,12 +340,15 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
       dma4(0, base, islot + W4_SCALES);   // (the third instruction of an entry)
     }
     ++issued;
-    islot += W4_ENTRY;
-    if (islot == ring0 + M::DEPTH * W4_ENTRY) islot = ring0;
-    if (++ij == per_tile) next_tile();
+    islot = islot == ring0 + (M::DEPTH - 1) * W4_ENTRY ? ring0 : islot + W4_ENTRY;
+    const bool wrap = ++ij == per_tile;
+    ij = wrap ? 0 : ij;
+    it += wrap ? 1 : 0;
+    cbase += wrap ? cstep : 0;
+    sbase += wrap ? sstep : 0;
   };
   // the first tile's codes are on their way before the adapters are looked up
-  if (a.dl.B_pack) {
+  if (DELTA) {
     per_tile = mine + TOKS;   // (no next tile yet)
     total = min(total, mine);
   }
@@ -364,20 +363,27 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     const int t = w + i * NW;
     rank[i] = 0;
     B[i] = nullptr;
-    if (a.dl.B_pack && t < toks) {
+    if (DELTA && t < toks) {
       const W4Token tm = a.dl.tok[tok0 + t];
       rank[i] = __builtin_amdgcn_readfirstlane(tm.rank);
       B[i] = a.dl.B_pack + uniform64(tm.b_off);
       u[t * 64 + lane] = lane < rank[i] ? a.dl.u[(int64_t)(tok0 + t) * a.dl.max_rank + lane] : 0.f;
     }
     deltas += rank[i] > 0 ? 1 : 0;
-    if (t < 16 * T && lane < 16 * M::TURNS)   // zeros stay where a token has no delta
+    if (DELTA && t < 16 * T && lane < 16 * M::TURNS)   // zeros stay where a token has no delta
       delta[((lane >> 4) * 16 * T + t) * 16 + (lane & 15)] = 0.f;
   }
   per_tile = mine + deltas;
-  if (ij == per_tile) next_tile();   // no delta here
-  total = per_tile * n_tiles;
-  while (issued < M::DEPTH && issued < total) issue_next();
+  if (DELTA) {
+    if (ij == per_tile) {   // no delta here
+      ij = 0;
+      ++it;
+      cbase += cstep;
+      sbase += sstep;
+    }
+    total = per_tile * n_tiles;
+    while (issued < M::DEPTH && issued < total) issue_next();
+  }
   if (!LONG && !staged) {
     load_x(0);
     // x has landed here, by a vmcnt(0) that the compiler sees: a wait of its own at the
@@ -388,72 +394,82 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   float* join = (float*)(lds + M::JOIN);
   const char* e = ring;
   // Before an entry is read: while entries remain to be issued, exactly DEPTH - 1
-  // younger ones are in flight; at the end all that remain are waited for.
-  auto wait_entry = [&]() {
-    if (issued < total) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W4_OPS * (M::DEPTH - 1)) : "memory");
+  // younger ones are in flight; at the end all that remain are waited for.  FULL: all
+  // of the tile's pairs are there and as many entries remain to be issued.
+  auto wait_entry = [&](bool full) {
+    if (full || issued < total)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W4_OPS * (M::DEPTH - 1)) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   };
-  auto next_entry = [&]() {
+  auto next_entry = [&](bool full) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the slot is refilled
-    e += W4_ENTRY;
-    if (e == ring + M::DEPTH * W4_ENTRY) e = ring;
-    if (issued < total) issue_next();
+    e = e == ring + (M::DEPTH - 1) * W4_ENTRY ? ring : e + W4_ENTRY;
+    if (full || issued < total) issue_next();
+  };
+  f32x4 acc[T][2];
+  auto take_pair = [&](int i, int q, bool full) {
+    wait_entry(full);
+    uint4 cw[2];
+    int sc[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      cw[h] = *(const uint4*)(e + (l * 8 + ((4 * h + g) ^ lds_sw(l))) * 16);
+      // a row's own bytes only: those past its end may be another row's NaN
+      sc[h] = *(const uint8_t*)(e + W4_SCALES + l * 12 + ((l * blocks) & 2) +
+                                min(4 * h + g, blocks - 1 - q * 8));
+    }
+    next_entry(full);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c[4] = {cw[h].x, cw[h].y, cw[h].z, cw[h].w};
+        const bf16x8 wf = w4_widen(c[k], __int_as_float(sc[h] << 23));
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[t][h] = mfma16(wf, xf[t][i][h][k], acc[t][h]);
+      }
   };
   for (int tile = 0; tile < n_tiles; ++tile) {
     const int turn = M::TURNS == 2 ? tile & 1 : 0;
-    f32x4 acc[T][2];
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int ph = 0; ph < phases; ++ph) {
-      if (LONG) load_x(ph);
+    if (!LONG && mine == P && issued + per_tile <= total) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        if (ph * P + i >= mine) break;
-        const int q = (ph * NW + w) * P + i;
-        wait_entry();
-        uint4 cw[2];
-        int sc[2];
+      for (int i = 0; i < P; ++i) take_pair(i, w * P + i, true);
+    } else {
+      for (int ph = 0; ph < phases; ++ph) {
+        if (LONG) load_x(ph);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          cw[h] = *(const uint4*)(e + (l * 8 + ((4 * h + g) ^ lds_sw(l))) * 16);
-          // a row's own bytes only: those past its end may be another row's NaN
-          sc[h] = *(const uint8_t*)(e + W4_SCALES + l * 12 + ((l * blocks) & 2) +
-                                    min(4 * h + g, blocks - 1 - q * 8));
+        for (int i = 0; i < P; ++i) {
+          if (ph * P + i >= mine) break;
+          take_pair(i, (ph * NW + w) * P + i, false);
         }
-        next_entry();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t c[4] = {cw[h].x, cw[h].y, cw[h].z, cw[h].w};
-            const bf16x8 wf = w4_widen(c[k], __int_as_float(sc[h] << 23));
-#pragma unroll
-            for (int t = 0; t < T; ++t) acc[t][h] = mfma16(wf, xf[t][i][h][k], acc[t][h]);
-          }
       }
     }
+    if (DELTA) {
 #pragma unroll
-    for (int i = 0; i < TOKS; ++i) {
-      // a token's delta: four lanes a row, 8 ranks and the 8 that lie 32 further each
-      if (rank[i] == 0) continue;
-      wait_entry();
-      const int row = lane >> 2, j = (lane & 3) * 8;
-      const float* ui = u + (w + i * NW) * 64;
-      float s = 0.f;
+      for (int i = 0; i < TOKS; ++i) {
+        // a token's delta: four lanes a row, 8 ranks and the 8 that lie 32 further each
+        if (rank[i] == 0) continue;
+        wait_entry(false);
+        const int row = lane >> 2, j = (lane & 3) * 8;
+        const float* ui = u + (w + i * NW) * 64;
+        float s = 0.f;
 #pragma unroll 1
-      for (int k = j; k < rank[i]; k += 32) {
-        const uint4 b = *(const uint4*)(e + (row * rank[i] + k) * 2);
-        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        for (int k = j; k < rank[i]; k += 32) {
+          const uint4 b = *(const uint4*)(e + (row * rank[i] + k) * 2);
+          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          s += ui[k + 2 * q] * bf2f_lo(bw[q]);
-          s += ui[k + 2 * q + 1] * bf2f_hi(bw[q]);
+          for (int q = 0; q < 4; ++q) {
+            s += ui[k + 2 * q] * bf2f_lo(bw[q]);
+            s += ui[k + 2 * q + 1] * bf2f_hi(bw[q]);
+          }
         }
+        next_entry(false);
+        s += __shfl_xor(s, 1, kWave);
+        s += __shfl_xor(s, 2, kWave);
+        if ((lane & 3) == 0) delta[(turn * 16 * T + w + i * NW) * 16 + row] = s;
       }
-      next_entry();
-      s += __shfl_xor(s, 1, kWave);
-      s += __shfl_xor(s, 2, kWave);
-      if ((lane & 3) == 0) delta[(turn * 16 * T + w + i * NW) * 16 + row] = s;
     }
 #pragma unroll
     for (int t = 0; t < T; ++t)
@@ -468,7 +484,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
 #pragma unroll 5
       for (int v = 1; v < NW; ++v) s += p[v * T * 256];
       const int tk = 16 * t + (al & 15), row = 4 * (al >> 4) + (i & 3);
-      if (a.dl.B_pack) s += delta[(turn * 16 * T + tk) * 16 + row];
+      if (DELTA) s += delta[(turn * 16 * T + tk) * 16 + row];
       const float s1 = __shfl_xor(s, 1, kWave);
       if ((lane & 1) == 0 && tk < toks)
         *(uint32_t*)(a.y + (int64_t)(tok0 + tk) * a.d_out + (rb + tile * a.row_blocks) * 16 + row) =
@@ -544,12 +560,13 @@ size_t w4_ws_bytes(int64_t n, int max_rank) {
   return cv.used;
 }
 
-template <int NW, int P, int T, bool X8, bool LONG>
+template <int NW, int P, int T, bool X8, bool LONG, bool DELTA>
 static lora_status product(W4Args a, hipStream_t s) {
   // the dynamic LDS bound, raised once (a thread-safe one-time initialisation, then read-only)
   constexpr int lds = W4Lds<NW, T>::BYTES;
-  static const hipError_t attr = hipFuncSetAttribute((const void*)w4_product_kernel<NW, P, T, X8, LONG>,
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  const auto kernel = w4_product_kernel<NW, P, T, X8, LONG, DELTA>;
+  static const hipError_t attr =
+      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   TRY_HIP(attr);
   // One block per CU: the token tiles times as many row blocks as that leaves, a
   // multiple of 8 (the XCDs) where there is more than one token tile, so that the
@@ -558,29 +575,30 @@ static lora_status product(W4Args a, hipStream_t s) {
   int64_t rb = std::max<int64_t>(1, device_cus() / tok_tiles);
   if (tok_tiles > 1 && rb >= 8) rb &= ~(int64_t)7;
   a.row_blocks = (int)std::min<int64_t>(rb, a.d_out / 16);
-  hipLaunchKernelGGL((w4_product_kernel<NW, P, T, X8, LONG>), dim3((unsigned)(a.row_blocks * tok_tiles)),
-                     dim3(64 * NW), lds, s, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(a.row_blocks * tok_tiles)), dim3(64 * NW), lds, s, a);
   return launch_check("w4_product");
 }
 
 // The fewest registers of x that hold d_in: 16 waves with one or two pairs each,
 // 8 with five or six.  Two token tiles a block where one pair leaves room.
-template <bool X8>
+template <bool X8, bool DELTA>
 static lora_status product_for(const W4Args& a, hipStream_t s) {
   const int64_t pairs = cdiv(a.d_in, W4_PAIR);
   if (pairs <= 16)
-    return a.n > 16 ? product<16, 1, 2, X8, false>(a, s) : product<16, 1, 1, X8, false>(a, s);
-  if (pairs <= 32) return product<16, 2, 1, X8, false>(a, s);
-  if (pairs <= 40) return product<8, 5, 1, X8, false>(a, s);
-  if (pairs <= 48) return product<8, 6, 1, X8, false>(a, s);
-  return product<8, 4, 1, X8, true>(a, s);
+    return a.n > 16 ? product<16, 1, 2, X8, false, DELTA>(a, s)
+                    : product<16, 1, 1, X8, false, DELTA>(a, s);
+  if (pairs <= 32) return product<16, 2, 1, X8, false, DELTA>(a, s);
+  if (pairs <= 40) return product<8, 5, 1, X8, false, DELTA>(a, s);
+  if (pairs <= 48) return product<8, 6, 1, X8, false, DELTA>(a, s);
+  return product<8, 4, 1, X8, true, DELTA>(a, s);
 }
 
 static lora_status launch_product(int64_t n, int64_t d_in, int64_t d_out, const void* x,
                                   const uint8_t* xs, const uint8_t* codes, const uint8_t* scales,
                                   const W4Delta& dl, uint16_t* y, hipStream_t s) {
   const W4Args a{(const uint8_t*)x, xs, codes, scales, y, dl, (int)n, (int)d_in, (int)d_out, 0};
-  return xs ? product_for<true>(a, s) : product_for<false>(a, s);
+  if (dl.B_pack) return xs ? product_for<true, true>(a, s) : product_for<false, true>(a, s);
+  return xs ? product_for<true, false>(a, s) : product_for<false, false>(a, s);
 }
 
 lora_status launch_w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
