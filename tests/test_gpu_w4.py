@@ -2,7 +2,7 @@
 
 Tolerance of y, from the arithmetic: its rounding to bf16 is off by at most 2^-8
 of the value; the fp32 sum of d_in products runs over at most d_in/8 terms in
-sequence in a wave (all 32 of one matrix instruction counted), 8 wave sums and 64
+sequence in a wave (all 32 of one matrix instruction counted), 16 wave sums and 64
 rank terms behind them, each step off by 2^-24 of the sum of magnitudes; u adds
 d_in/64 + 6 steps of its own to the delta's part of that sum.
 """
@@ -56,7 +56,10 @@ def _check(y, want, mag, d_in):
 
 SIZES = [(1, 64, 64), (1, 4096, 64), (2, 192, 128), (7, 320, 192), (15, 1024, 320), (16, 1088, 64), (17, 512, 128),
          (31, 2112, 64), (33, 640, 192), (64, 1024, 256), (65, 256, 64), (100, 1600, 128), (129, 192, 320), (255, 576, 64), (256, 1024, 192),
-         (1, 12288, 128), (5, 16448, 64)]
+         (1, 12288, 128), (5, 16448, 64),
+         # every number of pairs of 256 columns that a wave holds, a token past a tile
+         (3, 4352, 64), (20, 4416, 128), (2, 8192, 64), (33, 8192, 64), (5, 8256, 64), (17, 10240, 64), (4, 10304, 128), (40, 12288, 64),
+         (40, 13056, 64), (256, 12352, 64)]
 
 
 @pytest.mark.parametrize("x8", [False, True])
@@ -245,6 +248,25 @@ def test_eight_bit_norm_feeds_the_product():
     want, _ = OL.lora_forward(val, W, A, Bm, s.astype(np.float64), ids)
     _check(y, want, _magnitude(val, W, A, Bm, s, ids), H)
     assert L.lora_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 4096, 49216), (16, 4096, 49216), (3, 8192, 24640), (17, 4096, 49216)])
+def test_codes_larger_than_the_caches(n, d_in, d_out):
+    """Codes of a little over 96 MB (read once, non-temporally, by one token tile); sampled rows."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    codes = torch.randint(0, 256, (d_out, d_in // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    scales = torch.randint(110, 130, (d_out, d_in // 32), dtype=torch.uint8, device="cuda", generator=gen)
+    assert codes.numel() > 96 << 20
+    rng = np.random.default_rng(n)
+    rows = np.unique(np.concatenate([[0, 15, 16, d_out - 1], rng.integers(0, d_out, 40)]))
+    for x8 in (False, True):
+        x, xs, xv = _x(rng, n, d_in, x8)
+        y = torch.full((n, d_out), float("nan"), dtype=torch.bfloat16, device="cuda")
+        L.w4_linear(x, codes, scales, y, x_scales=xs)
+        at = torch.from_numpy(rows).to("cuda")
+        W = OQ.values(codes[at].cpu().numpy(), scales[at].cpu().numpy())
+        _check(y[:, at].contiguous(), xv @ W.T, np.abs(xv) @ np.abs(W).T, d_in)
+        assert bool(torch.isfinite(y).all())
 
 
 def test_codes_past_four_gigabytes():
