@@ -473,7 +473,7 @@ lora_status mlp_backward(const mlp_shape* shape, const uint16_t* dy, const uint1
  *   h     bf16 [n][hidden] out  the new residual stream, kept for the backward;
  *                               NULL exactly when residual is NULL (the
  *                               backward then takes x).  h may be x or residual.
- *   y     bf16 [n][hidden] out  may be x
+ *   y     bf16 [n][hidden] out  may be x, not h
  *   rstd  fp32 [n] out, nullable; kept for the backward
  * A row's result depends on that row alone, not on n.  The sum of squares is
  * fp32: a row whose squares overflow it (|h| beyond ~1e19) gives zeros, and

@@ -1129,6 +1129,7 @@ lora_status rmsnorm_forward(int64_t n, int64_t hidden, const uint16_t* x, const 
                             float* rstd, void* stream) {
   TRY(norm_forward_checks(n, hidden, x, residual, weight, eps, h, "rmsnorm_forward"));
   LORA_ARG_CHECK(n == 0 || (y && aligned16(y)), "rmsnorm_forward: y NULL or not 16-byte aligned");
+  LORA_ARG_CHECK(n == 0 || y != h, "rmsnorm_forward: y and h are the same buffer");
   if (n == 0) return LORA_OK;
   return launch_rmsnorm_fwd(n, hidden, x, residual, weight, eps, h, y, nullptr, nullptr, rstd,
                             S(stream));
@@ -1169,6 +1170,7 @@ lora_status rmsnorm_backward(int64_t n, int64_t hidden, const uint16_t* dy, cons
               (long long)n, (long long)hidden);
     return LORA_E_WORKSPACE;
   }
+  LORA_ARG_CHECK(!dweight || aligned16(ws), "rmsnorm_backward: the workspace must be 16-byte aligned");
   if (n == 0 && !dweight) return LORA_OK;
   return launch_rmsnorm_bwd(n, hidden, dy, dh, h, weight, rstd, dx, dweight, accumulate,
                             dweight ? (float*)((char*)ws + 256) : nullptr, S(stream));
@@ -1240,6 +1242,7 @@ lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_
               w4_ws_bytes(sh.n_tokens, sh.max_rank));
     return LORA_E_WORKSPACE;
   }
+  LORA_ARG_CHECK(aligned16(ws), "lora_forward_w4: the workspace must be 16-byte aligned");
   if (sh.n_tokens == 0) return LORA_OK;
   return launch_lora_w4(sh, x, x_scales, codes, scales, A_pack, B_pack, desc, adapter_ids, y, ws,
                         S(stream));
@@ -1272,6 +1275,7 @@ static lora_status grad_checks(const grad_shape* shape, const grad_tensor* table
     set_error("%s: workspace %zu bytes < %zu needed", what, ws_bytes, grad_ws_bytes(*shape));
     return LORA_E_WORKSPACE;
   }
+  LORA_ARG_CHECK(aligned16(ws), "%s: the workspace must be 16-byte aligned", what);
   return LORA_OK;
 }
 

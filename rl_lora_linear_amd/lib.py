@@ -455,6 +455,13 @@ def _dense(t: Optional[torch.Tensor], dtypes, shape, name: str):
     return t.data_ptr()
 
 
+def _device_ptr(t: torch.Tensor, name: str):
+    """The pointer of an operand whose shape the library checks itself."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs a contiguous device tensor")
+    return t.data_ptr()
+
+
 def _stream_for(t: torch.Tensor, stream=None):
     """The stream to enqueue on (the current one if None); t must lie on the current device,
     which is where the library launches."""
@@ -508,7 +515,7 @@ def rmsnorm_backward(dy, h, weight, rstd, dx, dh=None, dweight=None, accumulate=
                                 _dense(weight, _BF16, (hidden,), "weight"),
                                 _dense(rstd, _F32, (n,), "rstd"), _dense(dx, _BF16, dy.shape, "dx"),
                                 _dense(dweight, _F32, (hidden,), "dweight"), int(accumulate),
-                                None if ws is None else ws.data_ptr(), 0 if ws is None else _nbytes(ws),
+                                None if ws is None else _device_ptr(ws, "ws"), 0 if ws is None else _nbytes(ws),
                                 _stream_for(dy, stream)))
 
 
@@ -548,10 +555,13 @@ def lora_forward_w4(shape, x, codes, scales, A_pack, B_pack, desc, ids, y, ws, x
                     stream=None):
     """lora_forward on a 4-bit base (see w4_linear for x, codes and the scales)."""
     px, pxs, pc, ps, py = _w4_args(shape.n_tokens, shape.d_in, shape.d_out, x, x_scales, codes, scales, y)
-    _check(LIB.lora_forward_w4(ctypes.byref(shape), px, pxs, pc, ps, A_pack.data_ptr(),
-                               B_pack.data_ptr(), desc.data_ptr(),
+    for pack, elems, name in ((A_pack, shape.a_pack_elems, "A_pack"), (B_pack, shape.b_pack_elems, "B_pack")):
+        _arg(pack.dtype == torch.bfloat16 and pack.numel() >= elems, f"{name}: needs {elems} bfloat16 elements")
+    _arg(_nbytes(desc) >= shape.n_adapters * DESC_DTYPE.itemsize, "desc is shorter than n_adapters entries")
+    _check(LIB.lora_forward_w4(ctypes.byref(shape), px, pxs, pc, ps, _device_ptr(A_pack, "A_pack"),
+                               _device_ptr(B_pack, "B_pack"), _device_ptr(desc, "desc"),
                                _dense(ids, (torch.int32,), (shape.n_tokens,), "ids"), py,
-                               ws.data_ptr(), _nbytes(ws), _stream_for(codes, stream)))
+                               _device_ptr(ws, "ws"), _nbytes(ws), _stream_for(codes, stream)))
 
 
 def make_grad_table(tensors, n_groups, n_elems, device="cuda"):
@@ -583,20 +593,20 @@ def grad_workspace_bytes(shape: GradShape) -> int:
 def _grad_args(shape, table, flat, norms):
     _arg(table.numel() * table.element_size() >= shape.n_tensors * GRAD_DTYPE.itemsize,
          "table is shorter than n_tensors entries")
-    return (table.data_ptr(), *(_dense(t, _F32, (shape.n_elems,), name) for name, t in flat),
-            _dense(norms, _F32, (shape.n_groups,), "norms"))
+    ptrs = [_dense(t, _F32, (shape.n_elems,), name) for name, t in flat]
+    return (_device_ptr(table, "table"), *ptrs, _dense(norms, _F32, (shape.n_groups,), "norms"))
 
 
 def grad_norm(shape, table, g, norms, ws, stream=None):
     """norms[a] = the norm of group a's gradient (shape, table: make_grad_table)."""
     pt, pg, pn = _grad_args(shape, table, (("g", g),), norms)
-    _check(LIB.grad_norm(ctypes.byref(shape), pt, pg, pn, ws.data_ptr(), _nbytes(ws), _stream_for(g, stream)))
+    _check(LIB.grad_norm(ctypes.byref(shape), pt, pg, pn, _device_ptr(ws, "ws"), _nbytes(ws), _stream_for(g, stream)))
 
 
 def grad_clip(shape, table, g, max_norm, out, norms, ws, stream=None):
     """out = g scaled to at most max_norm per group; out may be g, norms may be None."""
     pt, pg, po, pn = _grad_args(shape, table, (("g", g), ("out", out)), norms)
-    _check(LIB.grad_clip(ctypes.byref(shape), pt, pg, max_norm, po, pn, ws.data_ptr(), _nbytes(ws),
+    _check(LIB.grad_clip(ctypes.byref(shape), pt, pg, max_norm, po, pn, _device_ptr(ws, "ws"), _nbytes(ws),
                          _stream_for(g, stream)))
 
 
@@ -610,7 +620,7 @@ def adam_step_clipped(shape, table, steps, p, g, m, v, max_norm, lr, beta1=0.9, 
         ws = empty_workspace(grad_workspace_bytes(shape), device=p.device)
     _check(LIB.adam_step_clipped(ctypes.byref(shape), pt, _dense(steps, _I64T, (shape.n_groups,), "steps"),
                                  pp, pg, pm, pv, max_norm, lr, beta1, beta2, eps, weight_decay,
-                                 _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16"), pn, ws.data_ptr(),
+                                 _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16"), pn, _device_ptr(ws, "ws"),
                                  _nbytes(ws), _stream_for(p, stream)))
     return ws
 

@@ -216,6 +216,19 @@ def test_broken_tables_stay_inside_the_buffer():
         assert bool((guard[:n] == 5).all()) and bool((guard[2 * n:] == 5).all())
 
 
+def test_host_operands_are_refused():
+    n = 100
+    shape, table = L.make_grad_table([(0, n, 0)], 1, n)
+    ws, g, norms = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.ones(n, device="cuda"), torch.empty(1, device="cuda")
+    for name, args in (("table", (table.cpu(), g, norms, ws)), ("g", (table, g.cpu(), norms, ws)), ("norms", (table, g, norms.cpu(), ws)),
+                       ("ws", (table, g, norms, ws.cpu()))):
+        with pytest.raises(L.LoraError, match=name):
+            L.grad_norm(shape, *args)
+    with pytest.raises(L.LoraError, match="steps"):
+        L.adam_step_clipped(shape, table, torch.zeros(1, dtype=torch.int64), g, g, g, g, 1.0, 1e-3, ws=ws)
+    assert L.lora_device_status(ws) == 0
+
+
 def test_no_tensors():
     shape, table = L.make_grad_table([], 3, 16)
     ws, norms = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.full((3,), -1.0, device="cuda")

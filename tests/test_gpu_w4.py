@@ -226,6 +226,27 @@ def test_non_finite_x_and_scales():
     assert np.all(np.isnan(got[:, 5])) and np.all(np.isfinite(np.delete(got[[0, 2]], 5, axis=1)))
 
 
+def test_host_operands_are_refused():
+    """Every operand of the adapter call left on the host, or too short, raises before any launch."""
+    d_in, d_out, n = 64, 64, 2
+    dev = lambda *s, dtype=torch.uint8: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    bf = torch.bfloat16
+    good = {"x": dev(n, d_in, dtype=bf), "codes": dev(d_out, 32), "scales": dev(d_out, 2), "A_pack": dev(4096, dtype=bf), "B_pack": dev(4096, dtype=bf),
+            "desc": dev(48), "ids": dev(n, dtype=torch.int32), "y": dev(n, d_out, dtype=bf)}
+    shape = L.make_shape(n, d_in, d_out, 4096, 4096, 2, 16)
+    good["ws"] = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape))
+    L.lora_forward_w4(shape, *good.values())
+    for name in good:
+        with pytest.raises(L.LoraError, match=name):
+            L.lora_forward_w4(shape, *{**good, name: good[name].cpu()}.values())
+    for name in ("A_pack", "B_pack", "desc"):
+        with pytest.raises(L.LoraError, match=name):
+            L.lora_forward_w4(shape, *{**good, name: good[name][:-1]}.values())
+    with pytest.raises(L.LoraError):
+        L.lora_forward_w4(shape, *{**good, "ws": good["ws"][:32]}.values())
+    assert L.lora_device_status(good["ws"]) == 0
+
+
 def test_eight_bit_norm_feeds_the_product():
     """rmsnorm_forward_q8's own output as x, through lora_forward_w4."""
     rng = np.random.default_rng(10)

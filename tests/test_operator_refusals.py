@@ -25,7 +25,7 @@ def _is(L, st, kind, word=b""):
 
 def test_norm(L):
     lib, E = L.LIB, L.LORA_E_INVALID_ARG
-    fwd = lambda n=4, H=64, x=P, r=P, w=P, eps=1e-6, h=P, y=P: lib.rmsnorm_forward(n, H, x, r, w, eps, h, y, None, None)  # noqa: E731
+    fwd = lambda n=4, H=64, x=P, r=P, w=P, eps=1e-6, h=ctypes.c_void_p(1 << 20), y=P: lib.rmsnorm_forward(n, H, x, r, w, eps, h, y, None, None)  # noqa: E731
     _is(L, fwd(n=-1), E)
     _is(L, fwd(n=1 << 30), E)
     _is(L, fwd(H=0), E)
@@ -39,6 +39,7 @@ def test_norm(L):
     _is(L, fwd(r=None), E, b"go together")
     for k in ("x", "r", "w", "h", "y"):
         _is(L, fwd(**{k: ODD}), E, b"aligned")
+    _is(L, fwd(h=P, y=P), E, b"same buffer")
     assert fwd(n=0, x=None, y=None) == L.LORA_OK
     q8 = lambda H=64, q=P, s=P: lib.rmsnorm_forward_q8(4, H, P, None, P, 1e-6, None, q, s, None, None)  # noqa: E731
     _is(L, q8(H=40), L.LORA_E_UNSUPPORTED, b"multiple of 32")
@@ -51,6 +52,7 @@ def test_norm(L):
     _is(L, bwd(dx=ODD), E, b"aligned")
     _is(L, bwd(H=40000), L.LORA_E_UNSUPPORTED)
     _is(L, bwd(ws=None), L.LORA_E_WORKSPACE)
+    _is(L, bwd(ws=ODD), E, b"aligned")
     _is(L, bwd(nb=lib.rmsnorm_backward_workspace_bytes(4, 64) - 1), L.LORA_E_WORKSPACE)
     assert bwd(n=0, dy=None, dh=None, h=None, r=None, dx=None, dw=None, ws=None, nb=0) == L.LORA_OK
     assert lib.rmsnorm_backward_workspace_bytes(-1, 64) == 0 == lib.rmsnorm_backward_workspace_bytes(4, 32769)
@@ -69,7 +71,7 @@ def test_four_bit(L):
     _is(L, lin(o=0), E)
     for k in ("x", "c", "s", "y"):
         _is(L, lin(**{k: None}), E)
-    for k in ("x", "c", "y"):
+    for k in ("x", "c", "s", "y"):
         _is(L, lin(**{k: ODD}), E, b"aligned")
     assert lin(n=0, x=None, y=None) == L.LORA_OK
     _is(L, lib.w4_quantize(P, 64, 100, P, P, None), L.LORA_E_UNSUPPORTED)
@@ -81,7 +83,7 @@ def test_four_bit(L):
     call = lambda s=sh, x=P, c=P, sc=P, A=P, B=P, d=P, ids=P, y=P, ws=P, nb=need: lib.lora_forward_w4(ctypes.byref(s), x, None, c, sc, A, B, d, ids, y, ws, nb, None)  # noqa: E731
     for k in ("x", "c", "sc", "A", "B", "d", "ids", "y"):
         _is(L, call(**{k: None}), E)
-    for k in ("x", "c", "A", "B", "y"):
+    for k in ("x", "c", "sc", "A", "B", "y", "ws"):
         _is(L, call(**{k: ODD}), E, b"aligned")
     _is(L, call(ws=None), L.LORA_E_WORKSPACE)
     _is(L, call(nb=need - 1), L.LORA_E_WORKSPACE)
@@ -109,6 +111,7 @@ def test_gradients(L):
         _is(L, norm(**{k: None}), E)
     _is(L, norm(ws=None), L.LORA_E_WORKSPACE)
     _is(L, norm(nb=need - 1), L.LORA_E_WORKSPACE)
+    _is(L, norm(ws=ODD), E, b"aligned")
     clip = lambda m=1.0, o=P: lib.grad_clip(ctypes.byref(good), P, P, m, o, P, P, need, None)  # noqa: E731
     _is(L, clip(m=-1.0), E, b"max_norm")
     _is(L, clip(m=float("nan")), E, b"max_norm")
@@ -151,4 +154,10 @@ def test_binding_checks_tensors(L):
         L.grad_norm(shape, table, torch.zeros(9), torch.zeros(1), table)
     with pytest.raises(L.LoraError, match="shorter"):
         L.grad_norm(L.GradShape(10, 1, 2, 1), table, torch.zeros(10), torch.zeros(1), table)
+    sh = L.make_shape(2, 64, 64, 100, 100, 4, 16)
+    pack, desc, ids = torch.zeros(100, dtype=torch.bfloat16), torch.zeros(96, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(L.LoraError, match="x: needs a device"):
+        L.lora_forward_w4(sh, x, codes, sc, pack, pack, desc, ids, y, codes)
+    with pytest.raises(L.LoraError, match="table: needs|g: needs a device"):
+        L.grad_norm(shape, table, torch.zeros(10), torch.zeros(1), table)
     assert np.array_equal(x.float().numpy(), np.zeros((2, 64)))
