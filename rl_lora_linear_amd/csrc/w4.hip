@@ -142,16 +142,17 @@ constexpr int W4_OPS = 3;                        // DMA instructions per entry
 constexpr int W4_SCALES = 2048;                  // entry: 16 rows x 128 B of codes, then
 constexpr int W4_ENTRY = 2048 + 256;             // 16 rows x 12 B holding 8 B of scales
 constexpr int W4_RINGS = 48 * W4_ENTRY;          // all waves' rings
-// LDS of a block of NW waves and T token tiles: the rings, the waves' sums (of two
-// tiles in turn where T is 1), the deltas likewise and the tokens' u.  Before the
-// rings start, x passes through it all.
-template <int NW, int T>
+// LDS of a block of NW waves in TEAMS teams and T token tiles: the rings, the waves'
+// sums (of two rounds in turn where T is 1), the deltas likewise and the tokens' u.
+// Before the rings start, x passes through it all.
+template <int NW, int TEAMS, int T>
 struct W4Lds {
   static constexpr int DEPTH = 48 / NW;                        // ring entries per wave
   static constexpr int TURNS = T == 1 ? 2 : 1;
   static constexpr int JOIN = W4_RINGS;                        // [TURNS][NW][T][64] f32x4
-  static constexpr int DELTA = JOIN + TURNS * NW * T * 64 * 16;   // [TURNS][16 T tokens][16 rows] f32
-  static constexpr int U = DELTA + TURNS * T * 16 * 16 * 4;    // [16 T tokens][64] f32
+  static constexpr int DELTA = JOIN + TURNS * NW * T * 64 * 16;
+                                                               // [TURNS][TEAMS][16 T tokens][16 rows] f32
+  static constexpr int U = DELTA + TURNS * TEAMS * T * 16 * 16 * 4;   // [16 T tokens][64] f32
   static constexpr int BYTES = U + T * 16 * 64 * 4;
   static constexpr int X = BYTES / NW / 4096 * 4096;           // a wave's part for x
   static_assert(X >= 8192, "a pair of 16 tokens' x");
@@ -197,29 +198,31 @@ struct W4Args {
   int32_t row_blocks;      // blocks that split the row tiles; the grid is these times the token tiles
 };
 
-// NW waves, each holding the x of P pairs of 16 T tokens.  LONG: d_in beyond what
+// NW waves, each holding the x of P pairs of 16 T tokens.  The waves form TEAMS teams
+// that take a row tile each at a time and split k among themselves.  LONG: d_in beyond what
 // the waves can hold of x; they then take it in phases and read their x again for
 // every tile.  DELTA: with adapters.  STREAM: the codes are read non-temporally, see
 // product_for.
-template <int NW, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
+template <int NW, int TEAMS, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
 __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  using M = W4Lds<NW, T>;
-  constexpr int TOKS = (16 * T + NW - 1) / NW;   // most tokens whose delta a wave owns
-  static_assert(TOKS <= 2, "the delta entries of a tile");
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l = lane & 15, g = lane >> 4;
-  // this block's tiles: rb, rb + row_blocks, ... (blocks that run together read
-  // neighbouring rows)
+  using M = W4Lds<NW, TEAMS, T>;
+  constexpr int WT = NW / TEAMS;                 // waves of a team
+  constexpr int TOKS = (16 * T + WT - 1) / WT;   // tokens whose delta a wave owns
+  static_assert(TOKS <= 2 || !DELTA, "the delta entries of a tile");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane & 15, g = lane >> 4, team = wave / WT, w = wave % WT;
+  // this block's rounds of TEAMS tiles: rb, rb + row_blocks, ... (blocks that run
+  // together read neighbouring rows)
   const int rb = blockIdx.x % a.row_blocks, tok0 = (blockIdx.x / a.row_blocks) * 16 * T;
-  const int n_tiles = (a.d_out / 16 - rb + a.row_blocks - 1) / a.row_blocks;
+  const int n_tiles = (a.d_out / (16 * TEAMS) - rb + a.row_blocks - 1) / a.row_blocks;
   const int toks = min(a.n - tok0, 16 * T);
   const int half = a.d_in / 2;          // bytes of a row of codes
   const int blocks = a.d_in / 32;       // scale bytes of a row
   const int pairs = (a.d_in + W4_PAIR - 1) / W4_PAIR;
-  const int phases = LONG ? (pairs + NW * P - 1) / (NW * P) : 1;
-  // pair j of this wave is (j / P * NW + w) * P + j % P
-  const int last = pairs - ((phases - 1) * NW + w) * P;
+  const int phases = LONG ? (pairs + WT * P - 1) / (WT * P) : 1;
+  // pair j of this wave is (j / P * WT + w) * P + j % P
+  const int last = pairs - ((phases - 1) * WT + w) * P;
   const int mine = (phases - 1) * P + min(max(last, 0), P);
 
   // x fragments: lane (l, g) of chunk h of a pair holds scale block 8 q + 4 h + g of
@@ -253,7 +256,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
       for (int i = 0; i < P; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int blk = ((ph * NW + w) * P + i) * 8 + h * 4 + g;
+          const int blk = ((ph * WT + w) * P + i) * 8 + h * 4 + g;
           const int at = min(blk, blocks - 1);
           const uint4* p = (const uint4*)(a.x + (tk * blocks + at) * XB);
           uint4 v[XB / 16];
@@ -270,7 +273,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     constexpr int ROWS = kWave / PIECES;           // tokens per instruction
     constexpr int PAIR = 16 * PIECES * 16;         // bytes of a pair of 16 tokens
     constexpr int ROUND = M::X / PAIR;             // of them that fit at a time
-    char* mem = lds + w * M::X;
+    char* mem = lds + wave * M::X;
     const uint32_t m0v = lds_at(mem);
     const uint8_t* base = a.x + (int64_t)tok0 * blocks * XB;
     const uint32_t end = (uint32_t)blocks * XB - 16;
@@ -307,7 +310,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   const bool staged = !LONG && toks > W4_DIRECT_TOKENS;
   if (staged) stage_x();
 
-  char* ring = lds + w * (M::DEPTH * W4_ENTRY);
+  char* ring = lds + wave * (M::DEPTH * W4_ENTRY);
   const uint32_t ring0 = lds_at(ring);
   // what this lane fetches of an entry: the 16-byte pieces of row r8 (+ 8) that its
   // slot holds (pieces are swizzled by row, see lds_sw), and a word of scales
@@ -321,13 +324,14 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   int per_tile = mine, total = mine * n_tiles;     // (deltas are added below)
   int it = 0, ij = 0, issued = 0;                  // the next entry to issue
   uint32_t islot = ring0;
-  const uint8_t* cbase = a.codes + (int64_t)rb * 16 * half;
-  const uint8_t* sbase = a.scales + (int64_t)rb * 16 * blocks;
-  const int64_t cstep = (int64_t)a.row_blocks * 16 * half, sstep = (int64_t)a.row_blocks * 16 * blocks;
+  const uint8_t* cbase = a.codes + (int64_t)(rb * TEAMS + team) * 16 * half;
+  const uint8_t* sbase = a.scales + (int64_t)(rb * TEAMS + team) * 16 * blocks;
+  const int64_t cstep = (int64_t)a.row_blocks * TEAMS * 16 * half;
+  const int64_t sstep = (int64_t)a.row_blocks * TEAMS * 16 * blocks;
   const uint32_t row_end = half - 16, scale_end = 16 * blocks - 4;
   auto issue_next = [&]() {
     if (!DELTA || ij < mine) {
-      const uint32_t q = LONG ? (ij / P * NW + w) * P + ij % P : w * P + ij;
+      const uint32_t q = LONG ? (ij / P * WT + w) * P + ij % P : w * P + ij;
       // (pieces past the row's end take its last one: their x is zero)
       const uint32_t v0 = min(off0 + q * 128, r8 * half + row_end);
       const uint32_t v1 = min(off1 + q * 128, (r8 + 8) * half + row_end);
@@ -346,7 +350,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
         r = rank[TOKS - 1];
         b = B[TOKS - 1];
       }
-      const uint16_t* base = b + ((int64_t)rb + (int64_t)it * a.row_blocks) * 16 * r;
+      const uint16_t* base = b + ((rb + (int64_t)it * a.row_blocks) * TEAMS + team) * 16 * r;
       dma16(min(lane * 16, r * 32 - 16), base, islot);
       dma16(min(lane * 16 + 1024, r * 32 - 16), base, islot + 1024);
       dma4(0, base, islot + W4_SCALES);   // (the third instruction of an entry)
@@ -366,13 +370,13 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   }
   while (issued < M::DEPTH && issued < total) issue_next();
 
-  // the delta's tokens of this wave: w + i NW
+  // the delta's tokens of this wave: w + i WT
   int deltas = 0;
   float* u = (float*)(lds + M::U);
   float* delta = (float*)(lds + M::DELTA);
 #pragma unroll
   for (int i = 0; i < TOKS; ++i) {
-    const int t = w + i * NW;
+    const int t = w + i * WT;
     rank[i] = 0;
     B[i] = nullptr;
     if (DELTA && t < toks) {
@@ -383,7 +387,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     }
     deltas += rank[i] > 0 ? 1 : 0;
     if (DELTA && t < 16 * T && lane < 16 * M::TURNS)   // zeros stay where a token has no delta
-      delta[((lane >> 4) * 16 * T + t) * 16 + (lane & 15)] = 0.f;
+      delta[(((lane >> 4) * TEAMS + team) * 16 * T + t) * 16 + (lane & 15)] = 0.f;
   }
   per_tile = mine + deltas;
   if (DELTA) {
@@ -454,7 +458,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           if (ph * P + i >= mine) break;
-          take_pair(i, (ph * NW + w) * P + i, false);
+          take_pair(i, (ph * WT + w) * P + i, false);
         }
       }
     }
@@ -465,7 +469,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
         if (rank[i] == 0) continue;
         wait_entry(false);
         const int row = lane >> 2, j = (lane & 3) * 8;
-        const float* ui = u + (w + i * NW) * 64;
+        const float* ui = u + (w + i * WT) * 64;
         float s = 0.f;
 #pragma unroll 1
         for (int k = j; k < rank[i]; k += 32) {
@@ -480,27 +484,29 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
         next_entry(false);
         s += __shfl_xor(s, 1, kWave);
         s += __shfl_xor(s, 2, kWave);
-        if ((lane & 3) == 0) delta[(turn * 16 * T + w + i * NW) * 16 + row] = s;
+        if ((lane & 3) == 0) delta[((turn * TEAMS + team) * 16 * T + w + i * WT) * 16 + row] = s;
       }
     }
 #pragma unroll
     for (int t = 0; t < T; ++t)
-      ((f32x4*)join)[((turn * NW + w) * T + t) * 64 + lane] = acc[t][0] + acc[t][1];
+      ((f32x4*)join)[((turn * NW + wave) * T + t) * 64 + lane] = acc[t][0] + acc[t][1];
     // writes of this tile visible to all; the other buffer is free again after it.
     // The DMA in flight is not waited for.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (w < 4 * T) {   // output 64 w + lane: of accumulator lane i / 4 of tile t, its row i % 4
+    // output 64 (w % 4) + lane of a team's token tile: accumulator lane i / 4's row i % 4
+    static_assert(WT >= 4 * T, "waves to sum a team's tiles");
+    if (w < 4 * T) {
       const int t = w / 4, i = (w % 4) * 64 + lane, al = i >> 2;
-      const float* p = join + (turn * NW * T + t) * 256 + i;
+      const float* p = join + ((turn * NW + team * WT) * T + t) * 256 + i;
       float s = p[0];
 #pragma unroll 5
-      for (int v = 1; v < NW; ++v) s += p[v * T * 256];
+      for (int v = 1; v < WT; ++v) s += p[v * T * 256];
       const int tk = 16 * t + (al & 15), row = 4 * (al >> 4) + (i & 3);
-      if (DELTA) s += delta[(turn * 16 * T + tk) * 16 + row];
+      if (DELTA) s += delta[((turn * TEAMS + team) * 16 * T + tk) * 16 + row];
       const float s1 = __shfl_xor(s, 1, kWave);
+      const int64_t tile_row = ((int64_t)(rb + tile * a.row_blocks) * TEAMS + team) * 16;
       if ((lane & 1) == 0 && tk < toks)
-        *(uint32_t*)(a.y + (int64_t)(tok0 + tk) * a.d_out + (rb + tile * a.row_blocks) * 16 + row) =
-            pack2bf(s, s1);
+        *(uint32_t*)(a.y + (int64_t)(tok0 + tk) * a.d_out + tile_row + row) = pack2bf(s, s1);
     }
     if (M::TURNS == 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
@@ -572,11 +578,11 @@ size_t w4_ws_bytes(int64_t n, int max_rank) {
   return cv.used;
 }
 
-template <int NW, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
+template <int NW, int TEAMS, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
 static lora_status product(W4Args a, hipStream_t s) {
   // the dynamic LDS bound, raised once (a thread-safe one-time initialisation, then read-only)
-  constexpr int lds = W4Lds<NW, T>::BYTES;
-  const auto kernel = w4_product_kernel<NW, P, T, X8, LONG, DELTA, STREAM>;
+  constexpr int lds = W4Lds<NW, TEAMS, T>::BYTES;
+  const auto kernel = w4_product_kernel<NW, TEAMS, P, T, X8, LONG, DELTA, STREAM>;
   static const hipError_t attr =
       hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   TRY_HIP(attr);
@@ -586,7 +592,7 @@ static lora_status product(W4Args a, hipStream_t s) {
   const int64_t tok_tiles = cdiv(a.n, 16 * T);
   int64_t rb = std::max<int64_t>(1, device_cus() / tok_tiles);
   if (tok_tiles > 1 && rb >= 8) rb &= ~(int64_t)7;
-  a.row_blocks = (int)std::min<int64_t>(rb, a.d_out / 16);
+  a.row_blocks = (int)std::min<int64_t>(rb, a.d_out / (16 * TEAMS));
   hipLaunchKernelGGL(kernel, dim3((unsigned)(a.row_blocks * tok_tiles)), dim3(64 * NW), lds, s, a);
   return launch_check("w4_product");
 }
@@ -601,18 +607,30 @@ static lora_status product_for(const W4Args& a, hipStream_t s) {
     // non-temporally where one token tile reads them once: 151936 x 4096 54.2 us against
     // 60.8, 32768 x 8192 28.3 against 30.6; 12288 x 4096 (25 MB, found in that cache) 9.2
     // against 8.8.
-    if (a.n <= 16 && (int64_t)a.d_out * a.d_in / 2 > (int64_t)96 << 20) {
-      if (pairs <= 16) return product<16, 1, 1, X8, false, false, true>(a, s);
-      if (pairs <= 32) return product<16, 2, 1, X8, false, false, true>(a, s);
+    const bool streams = a.n <= 16 && (int64_t)a.d_out * a.d_in / 2 > (int64_t)96 << 20;
+    // Up to 2048 columns one row tile would leave half of the waves without a pair: two
+    // teams take two tiles, where there are more tiles than CUs (one token 1024 -> 49152
+    // 9.5 us against 13.0, 2048 -> 49152 12.3 against 13.9; 2048 -> 4096, 256 tiles, 4.2
+    // against 4.0).  With adapters a wave of two teams would have two tokens' deltas
+    // (sixteen tokens 2048 -> 12288 14.7 us against 13.7).
+    if (a.n <= 16 && pairs <= 8 && a.d_out / 16 > device_cus())
+      return streams ? product<16, 2, 1, 1, X8, false, false, true>(a, s)
+                     : product<16, 2, 1, 1, X8, false, false>(a, s);
+    if (streams && pairs <= 16) {
+      // up to 4096 columns two teams halve the rounds (one token's 151936 x 4096 57.0 us
+      // against 60.3), but read x twice (sixteen tokens 67.0 against 63.0)
+      return a.n <= W4_DIRECT_TOKENS ? product<16, 2, 2, 1, X8, false, false, true>(a, s)
+                                     : product<16, 1, 1, 1, X8, false, false, true>(a, s);
     }
+    if (streams && pairs <= 32) return product<16, 1, 2, 1, X8, false, false, true>(a, s);
   }
   if (pairs <= 16)
-    return a.n > 16 ? product<16, 1, 2, X8, false, DELTA>(a, s)
-                    : product<16, 1, 1, X8, false, DELTA>(a, s);
-  if (pairs <= 32) return product<16, 2, 1, X8, false, DELTA>(a, s);
-  if (pairs <= 40) return product<8, 5, 1, X8, false, DELTA>(a, s);
-  if (pairs <= 48) return product<8, 6, 1, X8, false, DELTA>(a, s);
-  return product<8, 4, 1, X8, true, DELTA>(a, s);
+    return a.n > 16 ? product<16, 1, 1, 2, X8, false, DELTA>(a, s)
+                    : product<16, 1, 1, 1, X8, false, DELTA>(a, s);
+  if (pairs <= 32) return product<16, 1, 2, 1, X8, false, DELTA>(a, s);
+  if (pairs <= 40) return product<8, 1, 5, 1, X8, false, DELTA>(a, s);
+  if (pairs <= 48) return product<8, 1, 6, 1, X8, false, DELTA>(a, s);
+  return product<8, 1, 4, 1, X8, true, DELTA>(a, s);
 }
 
 static lora_status launch_product(int64_t n, int64_t d_in, int64_t d_out, const void* x,

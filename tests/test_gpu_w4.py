@@ -59,7 +59,9 @@ SIZES = [(1, 64, 64), (1, 4096, 64), (2, 192, 128), (7, 320, 192), (15, 1024, 32
          (1, 12288, 128), (5, 16448, 64),
          # every number of pairs of 256 columns that a wave holds, a token past a tile
          (3, 4352, 64), (20, 4416, 128), (2, 8192, 64), (33, 8192, 64), (5, 8256, 64), (17, 10240, 64), (4, 10304, 128), (40, 12288, 64),
-         (40, 13056, 64), (256, 12352, 64)]
+         (40, 13056, 64), (256, 12352, 64),
+         # more row tiles than CUs, of few columns: two teams of waves a block
+         (1, 64, 4224), (16, 320, 4160), (3, 2048, 4288), (5, 1984, 8256)]
 
 
 @pytest.mark.parametrize("x8", [False, True])
@@ -271,7 +273,7 @@ def test_eight_bit_norm_feeds_the_product():
     assert L.lora_device_status(ws) == 0
 
 
-@pytest.mark.parametrize("n,d_in,d_out", [(1, 4096, 49216), (16, 4096, 49216), (3, 8192, 24640), (17, 4096, 49216)])
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 4096, 49216), (16, 4096, 49216), (3, 8192, 24640), (17, 4096, 49216), (2, 1024, 196672), (9, 2048, 98368)])
 def test_codes_larger_than_the_caches(n, d_in, d_out):
     """Codes of a little over 96 MB (read once, non-temporally, by one token tile); sampled rows."""
     gen = torch.Generator(device="cuda").manual_seed(n)
