@@ -7,7 +7,7 @@
 // Two launches.  The first walks the chunks (8192 elements of one tensor) and
 // leaves, per block and group, the sum of squares in 64 bits, so that no square of
 // a finite gradient overflows.  In the second every block joins its group's sums
-// again, in block order -- at most 1024 of them, read from L2 while its own first
+// again, in block order -- at most 4096 of them, read from L2 while its own first
 // elements are on their way -- instead of a launch between the two that would
 // only add its latency, and then scales or steps its chunks.  A group is skipped
 // exactly when its sum is not finite, that is when any of its elements is NaN or
@@ -22,11 +22,12 @@ constexpr int GRAD_THREADS = 256;
 constexpr int GRAD_CHUNK = LORA_GRAD_CHUNK;
 static_assert(GRAD_CHUNK % (GRAD_THREADS * 4) == 0, "whole 16-byte rounds per chunk");
 
-// A group's factors.  c_a = coef 2^exp2: applied with ldexp it rounds as one fp32
-// product, and keeps its bits where c_a itself would be an fp32 subnormal (gradients
-// near the fp32 range).
+// A group's factors.  c_a = coef 2^exp2, with exp2 = 0 wherever c_a is a normal fp32
+// number: one product, and c_a = 1 leaves every g as it is, subnormals too.  A smaller
+// c_a (gradients near the fp32 range) keeps its bits in coef, and ldexp rounds only
+// where the result is subnormal.
 struct GradFactors {
-  float coef;          // 0.5 2^1 for a skipped group
+  float coef;          // 1 for a skipped group
   int32_t exp2;
   float step_size;     // lr / (1 - beta1^step)
   float inv_sqrt_bc2;  // 1 / sqrt(1 - beta2^step)
@@ -195,12 +196,14 @@ __device__ __forceinline__ GradFactors grad_factors(const grad_shape& sh, const 
       s += ws.slot[b + a];
   s = grad_block_sum(s, red);
   norm = sqrt(s);
-  GradFactors f{0.5f, 1, 0.f, 0.f, 0};
+  GradFactors f{1.f, 0, 0.f, 0.f, 0};
   if (!__builtin_isfinite(s)) {
     f.skip = 1;
     return f;
   }
-  f.coef = (float)frexp(fmin(1.0, (double)max_norm / (norm + 1e-6)), &f.exp2);
+  const double c = fmin(1.0, (double)max_norm / (norm + 1e-6));
+  f.coef = (float)c;
+  if (c < 0x1p-126) f.coef = (float)frexp(c, &f.exp2);
   if (ad.steps) {
     const int64_t step = ws.steps[a] + 1;
     f.step_size = (float)(ad.lr / (1.0 - power(ad.beta1, step)));

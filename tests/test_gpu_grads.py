@@ -200,6 +200,18 @@ def test_large_finite_gradients_do_not_overflow():
     _close(f64_of(out), np.full(n, 1 / np.sqrt(n)), 2.0 ** -21)
 
 
+def test_subnormal_gradients_are_not_rounded():
+    """A factor of 1 (no clipping, or a group that is skipped) leaves every element's bits."""
+    tiny = np.arange(1, 1001, dtype=np.uint32).view(np.float32)      # 1 .. 1000 times 2^-149
+    g = np.concatenate((tiny, -tiny, np.float32([np.inf]), tiny))
+    for split in (2000, 1):     # the Inf in a group of its own tail, then with nearly everything
+        shape, table = L.make_grad_table([(0, split, 0), (split, len(g) - split, 1)], 2, len(g))
+        ws, out = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.empty(len(g), device="cuda")
+        L.grad_clip(shape, table, dev_f32(g), float("inf"), out, None, ws)
+        assert np.array_equal(out.cpu().numpy().view(np.uint32), g.view(np.uint32))
+        assert L.lora_device_status(ws) == L.FLAG_NONFINITE_GRAD
+
+
 def test_broken_tables_stay_inside_the_buffer():
     """Entries that break the rules are flagged and touch nothing outside n_elems."""
     n = 20000
