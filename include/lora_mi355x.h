@@ -567,9 +567,10 @@ lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_
  *   device array of n_tensors entries, sorted by group; tensors must not
  *   overlap; first_chunk_0 = 0 and first_chunk_{i+1} = first_chunk_i +
  *   ceil(count_i / LORA_GRAD_CHUNK); n_chunks is the sum over all entries.
- * Elements outside every tensor are never touched.  An entry that breaks these
- * rules is never used as an address beyond n_elems: its chunks are left out and
- * LORA_FLAG_BAD_DESC is set (what the groups of such a table give is undefined). */
+ * Elements outside every tensor are never touched.  The device checks every entry
+ * (but for overlaps): one that breaks these rules sets LORA_FLAG_BAD_DESC and is
+ * never used as an address beyond n_elems.  What the groups of such a table give is
+ * undefined. */
 #define LORA_GRAD_CHUNK 8192
 typedef struct {
   int64_t offset;       /* first element in the flat buffer */
@@ -607,17 +608,16 @@ lora_status grad_clip(const grad_shape* shape, const grad_tensor* table, const f
 
 /* grad_clip and one AdamW step per group in one call, without writing the
  * clipped gradient: each element as in adam_step on min(1, max_norm / (norm +
- * 1e-6)) g, the constants taken from the 64-bit lr, betas, eps and decay.  steps: DEVICE int64 [n_groups], the steps each group has made; the
- * call makes step steps[a] + 1 and stores it, so a captured graph counts on with
- * every replay.  A group with a non-finite gradient keeps p, m, v, its bf16 copy
+ * 1e-6)) g, the constants taken from the 64-bit lr, betas, eps and decay.
+ * steps: DEVICE int64 [n_groups], the steps each group has made; the call makes
+ * step steps[a] + 1 and stores it, so a captured graph counts on with every replay.  A group with a non-finite gradient keeps p, m, v, its bf16 copy
  * and its counter, and LORA_FLAG_NONFINITE_GRAD is set.  p, m, v updated in
  * place, g read only, p_bf16 (nullable) receives bf16(p); norms (nullable) as
  * for grad_clip. */
 lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table, int64_t* steps,
                               float* p, const float* g, float* m, float* v, float max_norm,
                               double lr, double beta1, double beta2, double eps,
-                              double weight_decay,
-                              uint16_t* p_bf16, float* norms, void* ws, size_t ws_bytes,
+                              double weight_decay, uint16_t* p_bf16, float* norms, void* ws, size_t ws_bytes,
                               void* stream);
 
 /* ---- forward without allocation ------------------------------------- */

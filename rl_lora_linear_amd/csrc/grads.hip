@@ -72,6 +72,17 @@ __device__ __forceinline__ int grad_find(const grad_shape& sh, const grad_tensor
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Entry i by itself, in order, and with the chunks it has to have.
+__device__ __forceinline__ bool grad_entry_ok(const grad_shape& sh, const grad_tensor* tab, int i) {
+  const grad_tensor t = tab[i];
+  if (t.offset < 0 || t.count < 0 || t.offset > sh.n_elems || t.count > sh.n_elems - t.offset ||
+      t.group < (i > 0 ? tab[i - 1].group : 0) || t.group < 0 || t.group >= sh.n_groups)
+    return false;
+  const int end = i + 1 < sh.n_tensors ? tab[i + 1].first_chunk : sh.n_chunks;
+  return (i > 0 || t.first_chunk == 0) &&
+         end - (int64_t)t.first_chunk == (t.count + GRAD_CHUNK - 1) / GRAD_CHUNK;
+}
+
 __device__ __forceinline__ GradSpan grad_span(const grad_shape& sh, const grad_tensor& t, int c,
                                               int32_t* status) {
   const int64_t at = (int64_t)(c - t.first_chunk) * GRAD_CHUNK;
@@ -130,11 +141,12 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_partial_kernel(
     grad_shape sh, const grad_tensor* __restrict__ tab, const float* __restrict__ g,
     const int64_t* __restrict__ steps, GradWs ws) {
   __shared__ double red[GRAD_THREADS / kWave];
-  // the groups' first chunks and the step counters, by the grid's threads
+  // the groups' first chunks, the step counters and the table's check, by the grid's threads
   const int threads = gridDim.x * GRAD_THREADS, id = blockIdx.x * GRAD_THREADS + threadIdx.x;
   for (int i = id; i < max(sh.n_tensors, 1); i += threads) {
-    const int before = i > 0 ? tab[i - 1].group : -1;
-    const int here = sh.n_tensors > 0 ? tab[i].group : -1;
+    const int before = i > 0 ? min(tab[i - 1].group, sh.n_groups) : -1;
+    const int here = sh.n_tensors > 0 ? min(tab[i].group, sh.n_groups) : -1;
+    if (sh.n_tensors > 0 && !grad_entry_ok(sh, tab, i)) set_flag(ws.status, LORA_FLAG_BAD_DESC);
     for (int a = max(before + 1, 0); a <= min(here, sh.n_groups - 1); ++a)
       ws.start[a] = tab[i].first_chunk;
     if (i + 1 >= sh.n_tensors)

@@ -228,6 +228,23 @@ def test_broken_tables_stay_inside_the_buffer():
         assert bool((guard[:n] == 5).all()) and bool((guard[2 * n:] == 5).all())
 
 
+@pytest.mark.parametrize("n_chunks, bad", [
+    (2, [(0, 9000, 0, 0), (9000, 100, 0, 1)]),                        # the first tensor's second chunk is missing
+    (2, [(0, 100, 0, 0), (200, 9000, 0, 1)]),                         # the last one's
+    (1, [(0, 100, 0, 0), (200, 0, 1, 0)]),                            # an empty tensor before the last chunk's end
+    (2, [(0, 100, 1, 0), (200, 100, 0, 1)]),                          # groups out of order
+    (1, [(0, 0, 0, 0), (30000, 0, 0, 0), (0, 100, 0, 0)]),            # an empty tensor outside
+    (2, [(0, 100, (1 << 31) - 1, 0), (200, 100, 0, 1)]),
+])
+def test_tables_that_leave_elements_out_are_flagged(n_chunks, bad):
+    d = np.array(bad, L.GRAD_DTYPE)
+    table = torch.from_numpy(d.view(np.uint8).copy()).to("cuda")
+    shape = L.GradShape(20000, n_chunks, len(bad), 2)
+    ws, norms, g = L.empty_workspace(L.grad_workspace_bytes(shape)), torch.empty(2, device="cuda"), torch.ones(20000, device="cuda")
+    L.grad_norm(shape, table, g, norms, ws)
+    assert L.lora_device_status(ws) & L.FLAG_BAD_DESC
+
+
 def test_host_operands_are_refused():
     n = 100
     shape, table = L.make_grad_table([(0, n, 0)], 1, n)
