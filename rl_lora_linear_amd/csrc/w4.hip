@@ -205,8 +205,8 @@ struct W4Args {
 // product_for.
 template <int NW, int TEAMS, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
 __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   using M = W4Lds<NW, TEAMS, T>;
+  __shared__ __attribute__((aligned(16))) char lds[M::BYTES];
   constexpr int WT = NW / TEAMS;                 // waves of a team
   constexpr int TOKS = (16 * T + WT - 1) / WT;   // tokens whose delta a wave owns
   static_assert(TOKS <= 2 || !DELTA, "the delta entries of a tile");
@@ -580,12 +580,6 @@ size_t w4_ws_bytes(int64_t n, int max_rank) {
 
 template <int NW, int TEAMS, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
 static lora_status product(W4Args a, hipStream_t s) {
-  // the dynamic LDS bound, raised once (a thread-safe one-time initialisation, then read-only)
-  constexpr int lds = W4Lds<NW, TEAMS, T>::BYTES;
-  const auto kernel = w4_product_kernel<NW, TEAMS, P, T, X8, LONG, DELTA, STREAM>;
-  static const hipError_t attr =
-      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  TRY_HIP(attr);
   // One block per CU: the token tiles times as many row blocks as that leaves, a
   // multiple of 8 (the XCDs) where there is more than one token tile, so that the
   // token tiles of the same rows share an XCD's L2.
@@ -593,7 +587,8 @@ static lora_status product(W4Args a, hipStream_t s) {
   int64_t rb = std::max<int64_t>(1, device_cus() / tok_tiles);
   if (tok_tiles > 1 && rb >= 8) rb &= ~(int64_t)7;
   a.row_blocks = (int)std::min<int64_t>(rb, a.d_out / (16 * TEAMS));
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(a.row_blocks * tok_tiles)), dim3(64 * NW), lds, s, a);
+  hipLaunchKernelGGL((w4_product_kernel<NW, TEAMS, P, T, X8, LONG, DELTA, STREAM>),
+                     dim3((unsigned)(a.row_blocks * tok_tiles)), dim3(64 * NW), 0, s, a);
   return launch_check("w4_product");
 }
 
