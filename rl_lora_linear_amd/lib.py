@@ -443,21 +443,32 @@ def _arg(cond, msg):
         raise LoraError(LORA_E_INVALID_ARG, msg)
 
 
-def _dense(t: Optional[torch.Tensor], dtypes, shape, name: str):
-    """Checks one operand of the calls below and returns its pointer (None for None)."""
+def _on_device(t: torch.Tensor, name: str, dev: int):
+    at = t.get_device()
+    if at < 0:
+        raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs a device tensor")
+    if at != dev and dev >= 0:   # (an operand of device -1 has its own refusal)
+        raise LoraError(LORA_E_INVALID_ARG, f"{name}: on device {at}, the other operands on {dev}")
+
+
+def _dense(t: Optional[torch.Tensor], dtypes, shape, name: str, dev: int):
+    """Checks one operand of the calls below, which lie on device dev, and returns its
+    pointer (None for None)."""
     if t is None:
         return None
     if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
         raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs a contiguous {' or '.join(map(str, dtypes))} "
                         f"tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs a device tensor")
+    if t.get_device() != dev or dev < 0:
+        _on_device(t, name, dev)
     return t.data_ptr()
 
 
-def _device_ptr(t: torch.Tensor, name: str):
+def _device_ptr(t: torch.Tensor, name: str, dev: int):
     """The pointer of an operand whose shape the library checks itself."""
-    if not t.is_cuda or not t.is_contiguous():
+    if t.get_device() != dev or dev < 0:
+        _on_device(t, name, dev)
+    if not t.is_contiguous():
         raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs a contiguous device tensor")
     return t.data_ptr()
 
@@ -481,23 +492,25 @@ _E8M0 = (torch.uint8, torch.float8_e8m0fnu)
 def _norm_args(x, weight, rstd, residual, h):
     _arg(x.dim() == 2, "x must be [n][hidden]")
     n, hidden = x.shape
-    return n, hidden, (_dense(x, _BF16, x.shape, "x"), _dense(residual, _BF16, x.shape, "residual"),
-                       _dense(weight, _BF16, (hidden,), "weight"), _dense(h, _BF16, x.shape, "h"),
-                       _dense(rstd, _F32, (n,), "rstd"))
+    dev = x.get_device()
+    return n, hidden, dev, (_dense(x, _BF16, x.shape, "x", dev),
+                            _dense(residual, _BF16, x.shape, "residual", dev),
+                            _dense(weight, _BF16, (hidden,), "weight", dev),
+                            _dense(h, _BF16, x.shape, "h", dev), _dense(rstd, _F32, (n,), "rstd", dev))
 
 
 def rmsnorm_forward(x, weight, eps, y, rstd=None, residual=None, h=None, stream=None):
     """y = norm(x + residual) weight; h receives x + residual (given exactly with residual)."""
-    n, hidden, (px, pr, pw, ph, ps) = _norm_args(x, weight, rstd, residual, h)
-    _check(LIB.rmsnorm_forward(n, hidden, px, pr, pw, eps, ph, _dense(y, _BF16, x.shape, "y"), ps,
+    n, hidden, dev, (px, pr, pw, ph, ps) = _norm_args(x, weight, rstd, residual, h)
+    _check(LIB.rmsnorm_forward(n, hidden, px, pr, pw, eps, ph, _dense(y, _BF16, x.shape, "y", dev), ps,
                                _stream_for(x, stream)))
 
 
 def rmsnorm_forward_q8(x, weight, eps, q, q_scales, rstd=None, residual=None, h=None, stream=None):
     """q: e4m3 codes [n][hidden] (uint8 or float8_e4m3fn); q_scales: E8M0 [n][hidden/32]."""
-    n, hidden, (px, pr, pw, ph, ps) = _norm_args(x, weight, rstd, residual, h)
-    _check(LIB.rmsnorm_forward_q8(n, hidden, px, pr, pw, eps, ph, _dense(q, _E4M3, x.shape, "q"),
-                                  _dense(q_scales, _E8M0, (n, hidden // 32), "q_scales"), ps,
+    n, hidden, dev, (px, pr, pw, ph, ps) = _norm_args(x, weight, rstd, residual, h)
+    _check(LIB.rmsnorm_forward_q8(n, hidden, px, pr, pw, eps, ph, _dense(q, _E4M3, x.shape, "q", dev),
+                                  _dense(q_scales, _E8M0, (n, hidden // 32), "q_scales", dev), ps,
                                   _stream_for(x, stream)))
 
 
@@ -510,12 +523,13 @@ def rmsnorm_backward(dy, h, weight, rstd, dx, dh=None, dweight=None, accumulate=
     """dweight (with ws of rmsnorm_backward_workspace_bytes) is optional: a frozen weight has none."""
     _arg(dy.dim() == 2, "dy must be [n][hidden]")
     n, hidden = dy.shape
-    _check(LIB.rmsnorm_backward(n, hidden, _dense(dy, _BF16, dy.shape, "dy"),
-                                _dense(dh, _BF16, dy.shape, "dh"), _dense(h, _BF16, dy.shape, "h"),
-                                _dense(weight, _BF16, (hidden,), "weight"),
-                                _dense(rstd, _F32, (n,), "rstd"), _dense(dx, _BF16, dy.shape, "dx"),
-                                _dense(dweight, _F32, (hidden,), "dweight"), int(accumulate),
-                                None if ws is None else _device_ptr(ws, "ws"), 0 if ws is None else _nbytes(ws),
+    dev = dy.get_device()
+    _check(LIB.rmsnorm_backward(n, hidden, _dense(dy, _BF16, dy.shape, "dy", dev),
+                                _dense(dh, _BF16, dy.shape, "dh", dev), _dense(h, _BF16, dy.shape, "h", dev),
+                                _dense(weight, _BF16, (hidden,), "weight", dev),
+                                _dense(rstd, _F32, (n,), "rstd", dev), _dense(dx, _BF16, dy.shape, "dx", dev),
+                                _dense(dweight, _F32, (hidden,), "dweight", dev), int(accumulate),
+                                None if ws is None else _device_ptr(ws, "ws", dev), 0 if ws is None else _nbytes(ws),
                                 _stream_for(dy, stream)))
 
 
@@ -523,16 +537,18 @@ def w4_quantize(W, codes, scales, stream=None):
     """W bf16 [d_out][d_in] -> codes uint8 [d_out][d_in/2], scales uint8 [d_out][d_in/32]."""
     _arg(W.dim() == 2, "W must be [d_out][d_in]")
     d_out, d_in = W.shape
-    _check(LIB.w4_quantize(_dense(W, _BF16, W.shape, "W"), d_out, d_in,
-                           _dense(codes, _U8, (d_out, d_in // 2), "codes"),
-                           _dense(scales, _E8M0, (d_out, d_in // 32), "scales"), _stream_for(W, stream)))
+    dev = W.get_device()
+    _check(LIB.w4_quantize(_dense(W, _BF16, W.shape, "W", dev), d_out, d_in,
+                           _dense(codes, _U8, (d_out, d_in // 2), "codes", dev),
+                           _dense(scales, _E8M0, (d_out, d_in // 32), "scales", dev), _stream_for(W, stream)))
 
 
 def _w4_args(n, d_in, d_out, x, x_scales, codes, scales, y):
-    return (_dense(x, _BF16 if x_scales is None else _E4M3, (n, d_in), "x"),
-            _dense(x_scales, _E8M0, (n, d_in // 32), "x_scales"),
-            _dense(codes, _U8, (d_out, d_in // 2), "codes"),
-            _dense(scales, _E8M0, (d_out, d_in // 32), "scales"), _dense(y, _BF16, (n, d_out), "y"))
+    dev = codes.get_device()
+    return (_dense(x, _BF16 if x_scales is None else _E4M3, (n, d_in), "x", dev),
+            _dense(x_scales, _E8M0, (n, d_in // 32), "x_scales", dev),
+            _dense(codes, _U8, (d_out, d_in // 2), "codes", dev),
+            _dense(scales, _E8M0, (d_out, d_in // 32), "scales", dev), _dense(y, _BF16, (n, d_out), "y", dev))
 
 
 def w4_linear(x, codes, scales, y, x_scales=None, stream=None):
@@ -557,11 +573,12 @@ def lora_forward_w4(shape, x, codes, scales, A_pack, B_pack, desc, ids, y, ws, x
     px, pxs, pc, ps, py = _w4_args(shape.n_tokens, shape.d_in, shape.d_out, x, x_scales, codes, scales, y)
     for pack, elems, name in ((A_pack, shape.a_pack_elems, "A_pack"), (B_pack, shape.b_pack_elems, "B_pack")):
         _arg(pack.dtype == torch.bfloat16 and pack.numel() >= elems, f"{name}: needs {elems} bfloat16 elements")
+    dev = codes.get_device()
     _arg(_nbytes(desc) >= shape.n_adapters * DESC_DTYPE.itemsize, "desc is shorter than n_adapters entries")
-    _check(LIB.lora_forward_w4(ctypes.byref(shape), px, pxs, pc, ps, _device_ptr(A_pack, "A_pack"),
-                               _device_ptr(B_pack, "B_pack"), _device_ptr(desc, "desc"),
-                               _dense(ids, (torch.int32,), (shape.n_tokens,), "ids"), py,
-                               _device_ptr(ws, "ws"), _nbytes(ws), _stream_for(codes, stream)))
+    _check(LIB.lora_forward_w4(ctypes.byref(shape), px, pxs, pc, ps, _device_ptr(A_pack, "A_pack", dev),
+                               _device_ptr(B_pack, "B_pack", dev), _device_ptr(desc, "desc", dev),
+                               _dense(ids, (torch.int32,), (shape.n_tokens,), "ids", dev), py,
+                               _device_ptr(ws, "ws", dev), _nbytes(ws), _stream_for(codes, stream)))
 
 
 def make_grad_table(tensors, n_groups, n_elems, device="cuda"):
@@ -593,20 +610,23 @@ def grad_workspace_bytes(shape: GradShape) -> int:
 def _grad_args(shape, table, flat, norms):
     _arg(table.numel() * table.element_size() >= shape.n_tensors * GRAD_DTYPE.itemsize,
          "table is shorter than n_tensors entries")
-    ptrs = [_dense(t, _F32, (shape.n_elems,), name) for name, t in flat]
-    return (_device_ptr(table, "table"), *ptrs, _dense(norms, _F32, (shape.n_groups,), "norms"))
+    dev = flat[0][1].get_device()
+    ptrs = [_dense(t, _F32, (shape.n_elems,), name, dev) for name, t in flat]
+    return (_device_ptr(table, "table", dev), *ptrs, _dense(norms, _F32, (shape.n_groups,), "norms", dev))
 
 
 def grad_norm(shape, table, g, norms, ws, stream=None):
     """norms[a] = the norm of group a's gradient (shape, table: make_grad_table)."""
     pt, pg, pn = _grad_args(shape, table, (("g", g),), norms)
-    _check(LIB.grad_norm(ctypes.byref(shape), pt, pg, pn, _device_ptr(ws, "ws"), _nbytes(ws), _stream_for(g, stream)))
+    dev = g.get_device()
+    _check(LIB.grad_norm(ctypes.byref(shape), pt, pg, pn, _device_ptr(ws, "ws", dev), _nbytes(ws), _stream_for(g, stream)))
 
 
 def grad_clip(shape, table, g, max_norm, out, norms, ws, stream=None):
     """out = g scaled to at most max_norm per group; out may be g, norms may be None."""
     pt, pg, po, pn = _grad_args(shape, table, (("g", g), ("out", out)), norms)
-    _check(LIB.grad_clip(ctypes.byref(shape), pt, pg, max_norm, po, pn, _device_ptr(ws, "ws"), _nbytes(ws),
+    dev = g.get_device()
+    _check(LIB.grad_clip(ctypes.byref(shape), pt, pg, max_norm, po, pn, _device_ptr(ws, "ws", dev), _nbytes(ws),
                          _stream_for(g, stream)))
 
 
@@ -616,11 +636,12 @@ def adam_step_clipped(shape, table, steps, p, g, m, v, max_norm, lr, beta1=0.9, 
     steps made so far, counted up by the call.  ws: workspace of grad_workspace_bytes(shape)
     (a fresh zeroed one if None)."""
     pt, pp, pg, pm, pv, pn = _grad_args(shape, table, (("p", p), ("g", g), ("m", m), ("v", v)), norms)
+    dev = p.get_device()
     if ws is None:
         ws = empty_workspace(grad_workspace_bytes(shape), device=p.device)
-    _check(LIB.adam_step_clipped(ctypes.byref(shape), pt, _dense(steps, _I64T, (shape.n_groups,), "steps"),
+    _check(LIB.adam_step_clipped(ctypes.byref(shape), pt, _dense(steps, _I64T, (shape.n_groups,), "steps", dev),
                                  pp, pg, pm, pv, max_norm, lr, beta1, beta2, eps, weight_decay,
-                                 _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16"), pn, _device_ptr(ws, "ws"),
+                                 _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16", dev), pn, _device_ptr(ws, "ws", dev),
                                  _nbytes(ws), _stream_for(p, stream)))
     return ws
 

@@ -161,3 +161,39 @@ def test_binding_checks_tensors(L):
     with pytest.raises(L.LoraError, match="table: needs|g: needs a device"):
         L.grad_norm(shape, table, torch.zeros(10), torch.zeros(1), table)
     assert np.array_equal(x.float().numpy(), np.zeros((2, 64)))
+
+
+def test_operands_of_two_devices(L):
+    """Checked on the host: stand-ins for tensors that say where they lie."""
+    class On:
+        def __init__(self, dev, dtype, *shape):
+            self.dev, self.dtype, self.shape = dev, dtype, torch.Size(shape)
+
+        def get_device(self):
+            return self.dev
+
+        def is_contiguous(self):
+            return True
+
+        def dim(self):
+            return len(self.shape)
+
+        def numel(self):
+            return self.shape.numel()
+
+        def element_size(self):
+            return self.dtype.itemsize
+
+        def data_ptr(self):
+            assert self.dev == 0
+            return 64
+
+    b, f, u = torch.bfloat16, torch.float32, torch.uint8
+    x, other = On(0, b, 2, 64), On(1, b, 2, 64)
+    w = On(0, b, 64)
+    for call in (lambda: L.rmsnorm_forward(x, On(1, b, 64), 1e-6, x), lambda: L.rmsnorm_forward(x, w, 1e-6, other),
+                 lambda: L.rmsnorm_backward(x, x, w, On(1, f, 2), x),
+                 lambda: L.w4_linear(x, On(1, u, 64, 32), On(1, u, 64, 2), x),
+                 lambda: L.grad_norm(L.GradShape(4, 1, 1, 1), On(1, u, 24), On(0, f, 4), On(0, f, 1), On(0, u, 512))):
+        with pytest.raises(L.LoraError, match="on device"):
+            call()
