@@ -142,21 +142,35 @@ constexpr int W4_OPS = 3;                        // DMA instructions per entry
 constexpr int W4_SCALES = 2048;                  // entry: 16 rows x 128 B of codes, then
 constexpr int W4_ENTRY = 2048 + 256;             // 16 rows x 12 B holding 8 B of scales
 constexpr int W4_RINGS = 48 * W4_ENTRY;          // all waves' rings
-// LDS of a block of NW waves in TEAMS teams and T token tiles: the rings, the waves'
-// sums (of two rounds in turn where T is 1), the deltas likewise and the tokens' u.
-// Before the rings start, x passes through it all.
-template <int NW, int TEAMS, int T>
+// LDS of a block of NW waves in TEAMS teams and T token tiles: the rings ([slot][wave]),
+// the waves' sums (of two rounds in turn where T is 1), the deltas likewise and the
+// tokens' u.  Before the rings start, x passes through all of it but the first EARLY
+// slots, which fill meanwhile: as many as leave the number of x's rounds as it is.
+template <int NW, int TEAMS, int P, int T, bool X8>
 struct W4Lds {
   static constexpr int DEPTH = 48 / NW;                        // ring entries per wave
+  static constexpr int SLOT = NW * W4_ENTRY;
   static constexpr int TURNS = T == 1 ? 2 : 1;
   static constexpr int JOIN = W4_RINGS;                        // [TURNS][NW][T][64] f32x4
   static constexpr int DELTA = JOIN + TURNS * NW * T * 64 * 16;
                                                                // [TURNS][TEAMS][16 T tokens][16 rows] f32
   static constexpr int U = DELTA + TURNS * TEAMS * T * 16 * 16 * 4;   // [16 T tokens][64] f32
-  static constexpr int BYTES = U + T * 16 * 64 * 4;
-  static constexpr int X = BYTES / NW / 4096 * 4096;           // a wave's part for x
-  static_assert(X >= 8192, "a pair of 16 tokens' x");
-  static_assert(BYTES <= 160 * 1024, "one block a CU");
+  static constexpr int END = U + T * 16 * 64 * 4;
+  static constexpr int MOST = 160 * 1024;                      // one block a CU
+  static constexpr int X_PAIR = 16 * W4_PAIR * (X8 ? 1 : 2);   // bytes of a pair of 16 tokens' x
+  static constexpr int x_pairs(int early) { return std::min((MOST - early * SLOT) / NW / X_PAIR, T * P); }
+  static constexpr int x_rounds(int early) {
+    return x_pairs(early) > 0 ? (T * P + x_pairs(early) - 1) / x_pairs(early) : 1 << 20;
+  }
+  static constexpr int early() {
+    int e = 0;
+    while (e < DEPTH && x_rounds(e + 1) == x_rounds(0)) ++e;
+    return e;
+  }
+  static constexpr int EARLY = early();
+  static constexpr int X_PAIRS = x_pairs(EARLY);
+  static constexpr int BYTES = std::max(END, EARLY * SLOT + NW * X_PAIRS * X_PAIR);
+  static_assert(X_PAIRS > 0 && BYTES <= MOST);
 };
 
 struct W4Delta {
@@ -205,7 +219,7 @@ struct W4Args {
 // product_for.
 template <int NW, int TEAMS, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
 __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
-  using M = W4Lds<NW, TEAMS, T>;
+  using M = W4Lds<NW, TEAMS, P, T, X8>;
   __shared__ __attribute__((aligned(16))) char lds[M::BYTES];
   constexpr int WT = NW / TEAMS;                 // waves of a team
   constexpr int TOKS = (16 * T + WT - 1) / WT;   // tokens whose delta a wave owns
@@ -266,51 +280,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
         }
     }
   };
-  // through LDS, some pairs at a time: whole lines of a token's row, its 16-byte pieces
-  // swizzled by token so that the 16 lanes of a group read 16 different banks
-  auto stage_x = [&]() {
-    constexpr int PIECES = 8 * XB / 16;            // of a token's row in a pair
-    constexpr int ROWS = kWave / PIECES;           // tokens per instruction
-    constexpr int PAIR = 16 * PIECES * 16;         // bytes of a pair of 16 tokens
-    constexpr int ROUND = M::X / PAIR;             // of them that fit at a time
-    char* mem = lds + wave * M::X;
-    const uint32_t m0v = lds_at(mem);
-    const uint8_t* base = a.x + (int64_t)tok0 * blocks * XB;
-    const uint32_t end = (uint32_t)blocks * XB - 16;
-    const int s = lane % PIECES;
-#pragma unroll
-    for (int i0 = 0; i0 < T * P; i0 += ROUND) {
-#pragma unroll
-      for (int i = i0; i < T * P && i < i0 + ROUND; ++i)
-#pragma unroll
-        for (int m = 0; m < 16 / ROWS; ++m) {
-          const int t = m * ROWS + lane / PIECES;
-          dma16(min(i / P * 16 + t, toks - 1) * (uint32_t)(blocks * XB) +
-                    min((uint32_t)((w * P + i % P) * PIECES + (s ^ t)) * 16, end),
-                base, m0v + (i - i0) * PAIR + m * 1024);
-        }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#pragma unroll
-      for (int i = i0; i < T * P && i < i0 + ROUND; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int blk = (w * P + i % P) * 8 + h * 4 + g;
-          uint4 v[XB / 16];
-#pragma unroll
-          for (int k = 0; k < XB / 16; ++k)
-            v[k] = *(const uint4*)(mem + (i - i0) * PAIR +
-                                   (l * PIECES + (((h * 4 + g) * (XB / 16) + k) ^ l)) * 16);
-          put_x(i / P, i % P, h, blk < blocks, v,
-                x_scale(tok0 + min(i / P * 16 + l, toks - 1), min(blk, blocks - 1)));
-        }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
-    asm volatile("s_barrier" ::: "memory");        // the rings overlap other waves' parts
-  };
-  const bool staged = !LONG && toks > W4_DIRECT_TOKENS;
-  if (staged) stage_x();
-
-  char* ring = lds + wave * (M::DEPTH * W4_ENTRY);
+  char* ring = lds + wave * W4_ENTRY;
   const uint32_t ring0 = lds_at(ring);
   // what this lane fetches of an entry: the 16-byte pieces of row r8 (+ 8) that its
   // slot holds (pieces are swizzled by row, see lds_sw), and a word of scales
@@ -356,7 +326,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
       dma4(0, base, islot + W4_SCALES);   // (the third instruction of an entry)
     }
     ++issued;
-    islot = islot == ring0 + (M::DEPTH - 1) * W4_ENTRY ? ring0 : islot + W4_ENTRY;
+    islot = islot == ring0 + (M::DEPTH - 1) * M::SLOT ? ring0 : islot + M::SLOT;
     const bool wrap = ++ij == per_tile;
     ij = wrap ? 0 : ij;
     it += wrap ? 1 : 0;
@@ -368,6 +338,55 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     per_tile = mine + TOKS;   // (no next tile yet)
     total = min(total, mine);
   }
+  // through LDS, some pairs at a time: whole lines of a token's row, its 16-byte pieces
+  // swizzled by token so that the 16 lanes of a group read 16 different banks
+  auto stage_x = [&](auto&& meanwhile) {
+    constexpr int PIECES = 8 * XB / 16;            // of a token's row in a pair
+    constexpr int ROWS = kWave / PIECES;           // tokens per instruction
+    constexpr int PAIR = M::X_PAIR, ROUND = M::X_PAIRS;
+    char* mem = lds + M::EARLY * M::SLOT + wave * (ROUND * PAIR);
+    const uint32_t m0v = lds_at(mem);
+    const uint8_t* base = a.x + (int64_t)tok0 * blocks * XB;
+    const uint32_t end = (uint32_t)blocks * XB - 16;
+    const int s = lane % PIECES;
+#pragma unroll
+    for (int i0 = 0; i0 < T * P; i0 += ROUND) {
+#pragma unroll
+      for (int i = i0; i < T * P && i < i0 + ROUND; ++i)
+#pragma unroll
+        for (int m = 0; m < 16 / ROWS; ++m) {
+          const int t = m * ROWS + lane / PIECES;
+          dma16(min(i / P * 16 + t, toks - 1) * (uint32_t)(blocks * XB) +
+                    min((uint32_t)((w * P + i % P) * PIECES + (s ^ t)) * 16, end),
+                base, m0v + (i - i0) * PAIR + m * 1024);
+        }
+      if (i0 == 0 && meanwhile())
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W4_OPS * M::EARLY) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int i = i0; i < T * P && i < i0 + ROUND; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int blk = (w * P + i % P) * 8 + h * 4 + g;
+          uint4 v[XB / 16];
+#pragma unroll
+          for (int k = 0; k < XB / 16; ++k)
+            v[k] = *(const uint4*)(mem + (i - i0) * PAIR +
+                                   (l * PIECES + (((h * 4 + g) * (XB / 16) + k) ^ l)) * 16);
+          put_x(i / P, i % P, h, blk < blocks, v,
+                x_scale(tok0 + min(i / P * 16 + l, toks - 1), min(blk, blocks - 1)));
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    asm volatile("s_barrier" ::: "memory");        // the rings overlap other waves' parts
+  };
+  const bool staged = !LONG && toks > W4_DIRECT_TOKENS;
+  if (staged)
+    stage_x([&]() {
+      while (issued < M::EARLY && issued < total) issue_next();
+      return issued == M::EARLY;
+    });
   while (issued < M::DEPTH && issued < total) issue_next();
 
   // the delta's tokens of this wave: w + i WT
@@ -419,7 +438,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   };
   auto next_entry = [&](bool full) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the slot is refilled
-    e = e == ring + (M::DEPTH - 1) * W4_ENTRY ? ring : e + W4_ENTRY;
+    e = e == ring + (M::DEPTH - 1) * M::SLOT ? ring : e + M::SLOT;
     if (full || issued < total) issue_next();
   };
   f32x4 acc[T][2];
