@@ -3,17 +3,23 @@
 //
 //   W_ik = e2m1(code_ik) 2^(s_{i, k/32} - 127),   y_t = W x_t (+ s_a B_a A_a x_t).
 //
-// A wave takes 16 R weight rows, 16 T tokens and a slice of k; the block's
-// eight waves split k and are joined through LDS in wave order.  Each lane
-// reads 16 bytes of codes -- one scale's 32 weights -- turns them into bf16
-// pairs with the conversion unit (exact: a 2-bit significand times a power of
-// two) and feeds v_mfma_f32_16x16x32_bf16 four times.  k may be met in any order
-// as long as weights and x agree, so lane group g of the MFMA simply takes
-// scale block 4c + g and both operands load whole 16-byte pieces in memory
-// order: no shuffle, no LDS on the way in.  8-bit x is widened to bf16 in
-// registers (exact as well).  Sums are fp32 throughout, y is rounded once.
-// The scaled 4-bit MFMA would take the codes as they are, but it aligns the 128
-// products of a step to the largest of them and drops what lies ~2^-14 below.
+// One persistent block per CU keeps its tokens' x in registers as MFMA fragments and
+// streams 16-row tiles of codes past it; the block's waves split k and are joined
+// through LDS in wave order.  A lane turns 16 bytes of codes -- one scale's 32 weights
+// -- into bf16 pairs with the conversion unit (exact: a 2-bit significand times a power
+// of two) and feeds v_mfma_f32_16x16x32_bf16 four times.  k may be met in any order as
+// long as weights and x agree, so lane group g of the MFMA simply takes scale block
+// 4 c + g and both operands are read as whole 16-byte pieces in memory order, without
+// shuffles.  8-bit x is widened to bf16 in registers (exact as well).  Sums are fp32
+// throughout, y is rounded once.  The scaled 4-bit MFMA would take the codes as they
+// are, but it aligns the 128 products of a step to the largest of them and drops what
+// lies ~2^-14 below.
+// Bound by the codes' bytes where there are many (one token's 151936 x 4096, 331 MB:
+// 54 to 57 us, 5.8 to 6.1 TB/s of the 7.1 that plain reads reach), by launch, first
+// access and the join where there are few (4096 x 4096 4.4 us, a launch alone 3.9;
+// 12288 x 4096 8.8), by LDS traffic and conversions in large batches of long rows (64
+// tokens 12288 -> 4096 17.2 us).  The adapters' shrink is a launch of its own, 3 us
+// with one token; times in a captured graph.
 #include "common.hpp"
 #include "sgmv.hpp"
 
@@ -56,6 +62,9 @@ struct W4Token {
 // u_t = s_a A_a x_t in fp32, one wave per (token, rank row); rows past the
 // adapter's rank and rows of tokens without one are zero.  Block (0, t) writes
 // token t's W4Token; the grid together checks every descriptor of the table.
+// Bound by reading A, eight 16-byte pieces a lane in flight: 64 tokens of 64 adapters
+// with 12288 columns 10 us, 3.9 TB/s of distinct A (more waves that split k, or one
+// wave for all tokens of an adapter, were slower).
 constexpr int W4S_WAVES = 4;
 
 struct W4Adapters {
@@ -126,7 +135,7 @@ __global__ __launch_bounds__(64 * W4S_WAVES) void w4_shrink_kernel(
 }
 
 // ------------------------------------------------------------------ product
-// One block of 16 waves per CU holds 16 tokens and streams row tiles of 16 past
+// One block per CU holds 16 tokens (32 where T is 2) and streams row tiles of 16 past
 // them.  The waves split k in pieces of 256 columns ("pairs": two steps of four
 // scale blocks): wave w keeps its pairs' x as MFMA fragments in registers for all
 // of its tiles and moves its own pairs of codes through a ring of its own in LDS,
@@ -135,29 +144,31 @@ __global__ __launch_bounds__(64 * W4S_WAVES) void w4_shrink_kernel(
 // touch 16 rows per quarter wave: the texture path then serves 16 bytes a clock,
 // a quarter of what it does for the whole 128-byte lines that the DMA asks for.
 // At the end of a tile the waves' sums are joined through LDS (one barrier); a
-// wave owns one token's LoRA delta, whose factor rows are one more ring entry.
+// wave owns one token's LoRA delta (two where a team has 8 waves or T is 2), whose
+// factor rows are one more ring entry.
 constexpr int W4_PAIR = 256;                     // columns of one ring entry
 constexpr int W4_DIRECT_TOKENS = 4;              // tokens whose x is read without LDS
-constexpr int W4_OPS = 3;                        // DMA instructions per entry
 constexpr int W4_SCALES = 2048;                  // entry: 16 rows x 128 B of codes, then
 constexpr int W4_ENTRY = 2048 + 256;             // 16 rows x 12 B holding 8 B of scales
-constexpr int W4_RINGS = 48 * W4_ENTRY;          // all waves' rings
 // LDS of a block of NW waves in TEAMS teams and T token tiles: the rings ([slot][wave]),
 // the waves' sums (of two rounds in turn where T is 1), the deltas likewise and the
 // tokens' u.  Before the rings start, x passes through all of it but the first EARLY
 // slots, which fill meanwhile: as many as leave the number of x's rounds as it is.
-template <int NW, int TEAMS, int P, int T, bool X8>
+// LONG: an entry holds its pair's x too.
+template <int NW, int TEAMS, int P, int T, bool X8, bool LONG>
 struct W4Lds {
-  static constexpr int DEPTH = 48 / NW;                        // ring entries per wave
-  static constexpr int SLOT = NW * W4_ENTRY;
+  static constexpr int X_PAIR = 16 * W4_PAIR * (X8 ? 1 : 2);   // bytes of a pair of 16 tokens' x
+  static constexpr int ENTRY = W4_ENTRY + (LONG ? X_PAIR + (X8 ? 256 : 0) : 0);
+  static constexpr int OPS = 3 + (LONG ? X_PAIR / 1024 + X8 : 0);   // DMA instructions per entry
+  static constexpr int DEPTH = LONG ? (X8 ? 5 : 3) : 48 / NW;  // entries per wave
+  static constexpr int SLOT = NW * ENTRY;
   static constexpr int TURNS = T == 1 ? 2 : 1;
-  static constexpr int JOIN = W4_RINGS;                        // [TURNS][NW][T][64] f32x4
+  static constexpr int JOIN = DEPTH * SLOT;                    // [TURNS][NW][T][64] f32x4
   static constexpr int DELTA = JOIN + TURNS * NW * T * 64 * 16;
                                                                // [TURNS][TEAMS][16 T tokens][16 rows] f32
   static constexpr int U = DELTA + TURNS * TEAMS * T * 16 * 16 * 4;   // [16 T tokens][64] f32
   static constexpr int END = U + T * 16 * 64 * 4;
   static constexpr int MOST = 160 * 1024;                      // one block a CU
-  static constexpr int X_PAIR = 16 * W4_PAIR * (X8 ? 1 : 2);   // bytes of a pair of 16 tokens' x
   static constexpr int x_pairs(int early) { return std::min((MOST - early * SLOT) / NW / X_PAIR, T * P); }
   static constexpr int x_rounds(int early) {
     return x_pairs(early) > 0 ? (T * P + x_pairs(early) - 1) / x_pairs(early) : 1 << 20;
@@ -169,8 +180,8 @@ struct W4Lds {
   }
   static constexpr int EARLY = early();
   static constexpr int X_PAIRS = x_pairs(EARLY);
-  static constexpr int BYTES = std::max(END, EARLY * SLOT + NW * X_PAIRS * X_PAIR);
-  static_assert(X_PAIRS > 0 && BYTES <= MOST);
+  static constexpr int BYTES = LONG ? END : std::max(END, EARLY * SLOT + NW * X_PAIRS * X_PAIR);
+  static_assert((LONG || X_PAIRS > 0) && BYTES <= MOST);
 };
 
 struct W4Delta {
@@ -219,11 +230,11 @@ struct W4Args {
 // product_for.
 template <int NW, int TEAMS, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
 __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
-  using M = W4Lds<NW, TEAMS, P, T, X8>;
+  using M = W4Lds<NW, TEAMS, P, T, X8, LONG>;
   __shared__ __attribute__((aligned(16))) char lds[M::BYTES];
   constexpr int WT = NW / TEAMS;                 // waves of a team
   constexpr int TOKS = (16 * T + WT - 1) / WT;   // tokens whose delta a wave owns
-  static_assert(TOKS <= 2 || !DELTA, "the delta entries of a tile");
+  static_assert(!LONG || T == 1);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 15, g = lane >> 4, team = wave / WT, w = wave % WT;
   // this block's rounds of TEAMS tiles: rb, rb + row_blocks, ... (blocks that run
@@ -234,10 +245,8 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   const int half = a.d_in / 2;          // bytes of a row of codes
   const int blocks = a.d_in / 32;       // scale bytes of a row
   const int pairs = (a.d_in + W4_PAIR - 1) / W4_PAIR;
-  const int phases = LONG ? (pairs + WT * P - 1) / (WT * P) : 1;
-  // pair j of this wave is (j / P * WT + w) * P + j % P
-  const int last = pairs - ((phases - 1) * WT + w) * P;
-  const int mine = (phases - 1) * P + min(max(last, 0), P);
+  // this wave's pairs: w P .. w P + P - 1; LONG: w, w + WT, ...
+  const int mine = LONG ? (pairs - w + WT - 1) / WT : min(max(pairs - w * P, 0), P);
 
   // x fragments: lane (l, g) of chunk h of a pair holds scale block 8 q + 4 h + g of
   // token l of a token tile.  Lanes past the last token take the last one's (their
@@ -262,7 +271,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   auto x_scale = [&](int64_t t, int blk) {
     return X8 ? __int_as_float((int)a.xs[t * blocks + blk] << 23) : 1.f;
   };
-  auto load_x = [&](int ph) {           // straight from memory
+  auto load_x = [&]() {                 // straight from memory
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int64_t tk = tok0 + min(16 * t + l, toks - 1);
@@ -270,7 +279,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
       for (int i = 0; i < P; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int blk = ((ph * WT + w) * P + i) * 8 + h * 4 + g;
+          const int blk = (w * P + i) * 8 + h * 4 + g;
           const int at = min(blk, blocks - 1);
           const uint4* p = (const uint4*)(a.x + (tk * blocks + at) * XB);
           uint4 v[XB / 16];
@@ -280,7 +289,26 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
         }
     }
   };
-  char* ring = lds + wave * W4_ENTRY;
+  constexpr int PIECES = 8 * XB / 16;   // 16-byte pieces of a token's x in a pair
+  constexpr int X_ROWS = kWave / PIECES;   // tokens that one instruction fetches of
+  // piece (h, k) of token l in a pair's x in LDS: swizzled by token so that the 16 lanes
+  // of a group read 16 different banks
+  auto x_piece = [&](const char* mem, int h, int k) {
+    return *(const uint4*)(mem + (l * PIECES + (((h * 4 + g) * (XB / 16) + k) ^ l)) * 16);
+  };
+  const uint32_t x_end = (uint32_t)blocks * XB - 16;
+  // what this lane fetches of pair q by the instruction for tokens m X_ROWS ..
+  auto x_off = [&](int t0, int m, int q) {
+    const int t = m * X_ROWS + lane / PIECES;
+    return min(t0 + t, toks - 1) * (uint32_t)(blocks * XB) +
+           min((uint32_t)(q * PIECES + ((lane % PIECES) ^ t)) * 16, x_end);
+  };
+  const uint8_t* xbase = a.x + (int64_t)tok0 * blocks * XB;
+  // x's scales (LONG): the words that hold a token's 8 bytes, wherever they begin
+  const uint32_t xs_low = X8 && LONG ? (uint32_t)(uintptr_t)(a.xs + (int64_t)tok0 * blocks) & 3 : 0;
+  const uint8_t* xsbase = a.xs + (int64_t)tok0 * blocks - xs_low;
+
+  char* ring = lds + wave * M::ENTRY;
   const uint32_t ring0 = lds_at(ring);
   // what this lane fetches of an entry: the 16-byte pieces of row r8 (+ 8) that its
   // slot holds (pieces are swizzled by row, see lds_sw), and a word of scales
@@ -289,6 +317,8 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   const uint32_t off1 = (r8 + 8) * half + ((lane & 7) ^ lds_sw(r8 + 8)) * 16;
   const int srow = min(lane / 3, 15);
   const uint32_t soff = ((srow * blocks) & ~3) + min(lane - srow * 3, 2) * 4;
+  const uint32_t xsoff = ((min(srow, toks - 1) * blocks + xs_low) & ~3) + min(lane - srow * 3, 2) * 4;
+  const uint32_t xs_end = (toks * blocks - 1 + xs_low) & ~3;
   int rank[TOKS];
   const uint16_t* B[TOKS];
   int per_tile = mine, total = mine * n_tiles;     // (deltas are added below)
@@ -301,7 +331,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   const uint32_t row_end = half - 16, scale_end = 16 * blocks - 4;
   auto issue_next = [&]() {
     if (!DELTA || ij < mine) {
-      const uint32_t q = LONG ? (ij / P * WT + w) * P + ij % P : w * P + ij;
+      const uint32_t q = LONG ? ij * WT + w : w * P + ij;
       // (pieces past the row's end take its last one: their x is zero)
       const uint32_t v0 = min(off0 + q * 128, r8 * half + row_end);
       const uint32_t v1 = min(off1 + q * 128, (r8 + 8) * half + row_end);
@@ -313,17 +343,26 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
         dma16(v1, cbase, islot + 1024);
       }
       dma4(min(soff + q * 8, scale_end), sbase, islot + W4_SCALES);
+      if (LONG) {
+#pragma unroll
+        for (int m = 0; m < 16 / X_ROWS; ++m) dma16(x_off(0, m, q), xbase, islot + W4_ENTRY + m * 1024);
+        if (X8) dma4(min(xsoff + q * 8, xs_end), xsbase, islot + W4_ENTRY + M::X_PAIR);
+      }
     } else {   // a token's 16 factor rows: at most 2 KB
-      int r = rank[0];
-      const uint16_t* b = B[0];
-      if (TOKS > 1 && (ij > mine || r == 0)) {
-        r = rank[TOKS - 1];
-        b = B[TOKS - 1];
+      int r = 0, left = ij - mine;
+      const uint16_t* b = nullptr;
+#pragma unroll
+      for (int i = 0; i < TOKS; ++i) {   // the wave's token with `left` others before it
+        if (rank[i] != 0 && left-- == 0) {
+          r = rank[i];
+          b = B[i];
+        }
       }
       const uint16_t* base = b + ((rb + (int64_t)it * a.row_blocks) * TEAMS + team) * 16 * r;
       dma16(min(lane * 16, r * 32 - 16), base, islot);
       dma16(min(lane * 16 + 1024, r * 32 - 16), base, islot + 1024);
-      dma4(0, base, islot + W4_SCALES);   // (the third instruction of an entry)
+#pragma unroll
+      for (int i = 2; i < M::OPS; ++i) dma4(0, base, islot + W4_SCALES);   // (an entry's count)
     }
     ++issued;
     islot = islot == ring0 + (M::DEPTH - 1) * M::SLOT ? ring0 : islot + M::SLOT;
@@ -338,30 +377,20 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     per_tile = mine + TOKS;   // (no next tile yet)
     total = min(total, mine);
   }
-  // through LDS, some pairs at a time: whole lines of a token's row, its 16-byte pieces
-  // swizzled by token so that the 16 lanes of a group read 16 different banks
+  // through LDS, some pairs at a time: whole lines of a token's row
   auto stage_x = [&](auto&& meanwhile) {
-    constexpr int PIECES = 8 * XB / 16;            // of a token's row in a pair
-    constexpr int ROWS = kWave / PIECES;           // tokens per instruction
     constexpr int PAIR = M::X_PAIR, ROUND = M::X_PAIRS;
     char* mem = lds + M::EARLY * M::SLOT + wave * (ROUND * PAIR);
     const uint32_t m0v = lds_at(mem);
-    const uint8_t* base = a.x + (int64_t)tok0 * blocks * XB;
-    const uint32_t end = (uint32_t)blocks * XB - 16;
-    const int s = lane % PIECES;
 #pragma unroll
     for (int i0 = 0; i0 < T * P; i0 += ROUND) {
 #pragma unroll
       for (int i = i0; i < T * P && i < i0 + ROUND; ++i)
 #pragma unroll
-        for (int m = 0; m < 16 / ROWS; ++m) {
-          const int t = m * ROWS + lane / PIECES;
-          dma16(min(i / P * 16 + t, toks - 1) * (uint32_t)(blocks * XB) +
-                    min((uint32_t)((w * P + i % P) * PIECES + (s ^ t)) * 16, end),
-                base, m0v + (i - i0) * PAIR + m * 1024);
-        }
+        for (int m = 0; m < 16 / X_ROWS; ++m)
+          dma16(x_off(i / P * 16, m, w * P + i % P), xbase, m0v + (i - i0) * PAIR + m * 1024);
       if (i0 == 0 && meanwhile())
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W4_OPS * M::EARLY) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(M::OPS * M::EARLY) : "memory");
       else
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
@@ -371,9 +400,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
           const int blk = (w * P + i % P) * 8 + h * 4 + g;
           uint4 v[XB / 16];
 #pragma unroll
-          for (int k = 0; k < XB / 16; ++k)
-            v[k] = *(const uint4*)(mem + (i - i0) * PAIR +
-                                   (l * PIECES + (((h * 4 + g) * (XB / 16) + k) ^ l)) * 16);
+          for (int k = 0; k < XB / 16; ++k) v[k] = x_piece(mem + (i - i0) * PAIR, h, k);
           put_x(i / P, i % P, h, blk < blocks, v,
                 x_scale(tok0 + min(i / P * 16 + l, toks - 1), min(blk, blocks - 1)));
         }
@@ -420,7 +447,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     while (issued < M::DEPTH && issued < total) issue_next();
   }
   if (!LONG && !staged) {
-    load_x(0);
+    load_x();
     // x has landed here, by a vmcnt(0) that the compiler sees: a wait of its own at the
     // first use, in the loop, would drain the ring there in every round
     __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -433,7 +460,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   // of the tile's pairs are there and as many entries remain to be issued.
   auto wait_entry = [&](bool full) {
     if (full || issued < total)
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W4_OPS * (M::DEPTH - 1)) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(M::OPS * (M::DEPTH - 1)) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   };
   auto next_entry = [&](bool full) {
@@ -452,6 +479,18 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
       // a row's own bytes only: those past its end may be another row's NaN
       sc[h] = *(const uint8_t*)(e + W4_SCALES + l * 12 + ((l * blocks) & 2) +
                                 min(4 * h + g, blocks - 1 - q * 8));
+      if (LONG) {
+        const int blk = q * 8 + 4 * h + g;
+        uint4 v[XB / 16];
+#pragma unroll
+        for (int k = 0; k < XB / 16; ++k) v[k] = x_piece(e + W4_ENTRY, h, k);
+        float xsc = 1.f;
+        if (X8)
+          xsc = __int_as_float(
+              (int)*(const uint8_t*)(e + W4_ENTRY + M::X_PAIR + l * 12 +
+                                     ((min(l, toks - 1) * blocks + xs_low) & 3) + 4 * h + g) << 23);
+        put_x(0, 0, h, blk < blocks, v, xsc);
+      }
     }
     next_entry(full);
 #pragma unroll
@@ -461,7 +500,7 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
         const uint32_t c[4] = {cw[h].x, cw[h].y, cw[h].z, cw[h].w};
         const bf16x8 wf = w4_widen(c[k], __int_as_float(sc[h] << 23));
 #pragma unroll
-        for (int t = 0; t < T; ++t) acc[t][h] = mfma16(wf, xf[t][i][h][k], acc[t][h]);
+        for (int t = 0; t < T; ++t) acc[t][h] = mfma16(wf, xf[t][LONG ? 0 : i][h][k], acc[t][h]);
       }
   };
   for (int tile = 0; tile < n_tiles; ++tile) {
@@ -471,14 +510,13 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     if (!LONG && mine == P && issued + per_tile <= total) {
 #pragma unroll
       for (int i = 0; i < P; ++i) take_pair(i, w * P + i, true);
+    } else if (LONG) {
+      for (int i = 0; i < mine; ++i) take_pair(0, i * WT + w, false);
     } else {
-      for (int ph = 0; ph < phases; ++ph) {
-        if (LONG) load_x(ph);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          if (ph * P + i >= mine) break;
-          take_pair(i, (ph * WT + w) * P + i, false);
-        }
+      for (int i = 0; i < P; ++i) {
+        if (i >= mine) break;
+        take_pair(i, w * P + i, false);
       }
     }
     if (DELTA) {
@@ -639,12 +677,12 @@ static lora_status product_for(const W4Args& a, hipStream_t s) {
     if (streams && pairs <= 32) return product<16, 1, 2, 1, X8, false, false, true>(a, s);
   }
   if (pairs <= 16)
-    return a.n > 16 ? product<16, 1, 1, 2, X8, false, DELTA>(a, s)
+    return a.n > 80 ? product<16, 1, 1, 2, X8, false, DELTA>(a, s)
                     : product<16, 1, 1, 1, X8, false, DELTA>(a, s);
   if (pairs <= 32) return product<16, 1, 2, 1, X8, false, DELTA>(a, s);
   if (pairs <= 40) return product<8, 1, 5, 1, X8, false, DELTA>(a, s);
   if (pairs <= 48) return product<8, 1, 6, 1, X8, false, DELTA>(a, s);
-  return product<8, 1, 4, 1, X8, true, DELTA>(a, s);
+  return product<4, 1, 1, 1, X8, true, DELTA>(a, s);
 }
 
 static lora_status launch_product(int64_t n, int64_t d_in, int64_t d_out, const void* x,

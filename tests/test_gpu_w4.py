@@ -132,6 +132,33 @@ def test_lora_forward(n, d_in, d_out, x8):
     assert np.array_equal(bits_of(y)[out], bits_of(base)[out])
 
 
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 12416, 4224), (6, 14336, 8256), (18, 12352, 4224), (16, 20480, 64)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_long_rows(n, d_in, d_out, x8):
+    """Rows whose x does not fit the registers, several tiles a block; scales of x that
+    begin at an odd multiple of two bytes; sampled rows."""
+    rng = np.random.default_rng(n + d_in + d_out)
+    codes, scales = _weights(rng, d_out, d_in)
+    x, xs, xv = _x(rng, n + 1, d_in, x8)
+    x, xs, xv = x[1:], xs[1:] if x8 else None, xv[1:]
+    ranks = [16, 64, 8]
+    pack, a_off, b_off, A, Bm, s = _adapters(rng, ranks, d_in, d_out)
+    ids = rng.integers(0, 3, n).astype(np.int32)
+    rows = np.unique(np.concatenate((rng.integers(0, d_out, 100), [0, d_out - 1])))
+    W = OQ.values(codes[rows], scales[rows])
+    y = torch.empty(n, d_out, dtype=torch.bfloat16, device="cuda")
+    L.w4_linear(x, _dev(codes), _dev(scales), y, x_scales=xs)
+    _check(y[:, _dev(rows)], xv @ W.T, np.abs(xv) @ np.abs(W).T, d_in)
+    shape = L.make_shape(n, d_in, d_out, len(pack), len(pack), 3, 64, L.IDS_INTERLEAVED)
+    ws, desc = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape)), L.make_desc(a_off, b_off, ranks, s)
+    dp = dev_bf16(pack)
+    L.lora_forward_w4(shape, x, _dev(codes), _dev(scales), dp, dp, desc, _dev(ids), y, ws, x_scales=xs)
+    Br = [b[rows] for b in Bm]
+    want = xv @ W.T + np.stack([float(s[a]) * (Br[a] @ (A[a] @ xv[t])) for t, a in enumerate(ids)])
+    _check(y[:, _dev(rows)], want, _magnitude(xv, W, A, Br, s, ids), d_in)
+    assert L.lora_device_status(ws) == 0
+
+
 def test_bad_descriptors_and_order():
     rng = np.random.default_rng(3)
     d_in, d_out, ranks = 128, 64, [16, 16, 16, 16, 16]
