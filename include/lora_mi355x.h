@@ -539,6 +539,7 @@ lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t*
  *   x  bf16 [n][d_in] with x_scales NULL; or e4m3 codes uint8 [n][d_in] with
  *      x_scales uint8 [n][d_in/32] (E8M0), as rmsnorm_forward_q8 writes them
  *   y  bf16 [n][d_out] out
+ * A token's y (here and in lora_forward_w4) has the same bits in every batch.
  * d_in, d_out multiples of 64, <= 2^20; x, codes, scales, y 16-byte aligned. */
 lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
                       const uint8_t* x_scales, const uint8_t* codes, const uint8_t* scales,

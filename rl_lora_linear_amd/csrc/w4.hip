@@ -16,9 +16,9 @@
 // lies ~2^-14 below.
 // Bound by the codes' bytes where there are many (one token's 151936 x 4096, 331 MB:
 // 54 to 57 us, 5.8 to 6.1 TB/s of the 7.1 that plain reads reach), by launch, first
-// access and the join where there are few (4096 x 4096 4.4 us, a launch alone 3.9;
-// 12288 x 4096 8.8), by LDS traffic and conversions in large batches of long rows (64
-// tokens 12288 -> 4096 17.2 us).  The adapters' shrink is a launch of its own, 3 us
+// access and the join where there are few (4096 x 4096 4.2 us, a launch alone 3.9;
+// 12288 x 4096 8.6), by LDS traffic and conversions in large batches of long rows (64
+// tokens 12288 -> 4096 16.9 us).  The adapters' shrink is a launch of its own, 3 us
 // with one token; times in a captured graph.
 #include "common.hpp"
 #include "sgmv.hpp"
@@ -139,21 +139,25 @@ __global__ __launch_bounds__(64 * W4S_WAVES) void w4_shrink_kernel(
 // them.  The waves split k in pieces of 256 columns ("pairs": two steps of four
 // scale blocks): wave w keeps its pairs' x as MFMA fragments in registers for all
 // of its tiles and moves its own pairs of codes through a ring of its own in LDS,
-// so the loop has no barrier.  LDS-DMA fills the ring two pairs ahead (64 KB and
-// more in flight per CU).  Loading the fragments straight into registers would
+// so the pairs need no barrier.  LDS-DMA fills the ring two pairs ahead, five with
+// eight waves (73 KB and more in flight per CU).  Loading the fragments straight into registers would
 // touch 16 rows per quarter wave: the texture path then serves 16 bytes a clock,
 // a quarter of what it does for the whole 128-byte lines that the DMA asks for.
 // At the end of a tile the waves' sums are joined through LDS (one barrier); a
 // wave owns one token's LoRA delta (two where a team has 8 waves or T is 2), whose
 // factor rows are one more ring entry.
 constexpr int W4_PAIR = 256;                     // columns of one ring entry
-constexpr int W4_DIRECT_TOKENS = 4;              // tokens whose x is read without LDS
+// Up to four tokens read x's fragments straight from memory (bf16 4096 -> 12288: one
+// token 8.7 us, through LDS 9.5; 8 -> 9.4 and 9.6, 16 -> 10.7 and 10.0; in 8 bits four
+// tokens 9.3 and 9.1).
+constexpr int W4_DIRECT_TOKENS = 4;
 constexpr int W4_SCALES = 2048;                  // entry: 16 rows x 128 B of codes, then
 constexpr int W4_ENTRY = 2048 + 256;             // 16 rows x 12 B holding 8 B of scales
 // LDS of a block of NW waves in TEAMS teams and T token tiles: the rings ([slot][wave]),
 // the waves' sums (of two rounds in turn where T is 1), the deltas likewise and the
 // tokens' u.  Before the rings start, x passes through all of it but the first EARLY
-// slots, which fill meanwhile: as many as leave the number of x's rounds as it is.
+// slots, which fill meanwhile: as many as leave the number of x's rounds as it is (16
+// tokens in 8 bits 4096 -> 12288 9.4 us, 10.0 with the rings begun after x).
 // LONG: an entry holds its pair's x too.
 template <int NW, int TEAMS, int P, int T, bool X8, bool LONG>
 struct W4Lds {
@@ -224,10 +228,10 @@ struct W4Args {
 };
 
 // NW waves, each holding the x of P pairs of 16 T tokens.  The waves form TEAMS teams
-// that take a row tile each at a time and split k among themselves.  LONG: d_in beyond what
-// the waves can hold of x; they then take it in phases and read their x again for
-// every tile.  DELTA: with adapters.  STREAM: the codes are read non-temporally, see
-// product_for.
+// that take a row tile each at a time and split k among themselves.  LONG: d_in beyond
+// what the waves can hold of x; a pair's x then comes through the ring with its codes,
+// for every tile again.  DELTA: with adapters.  STREAM: the codes are read
+// non-temporally, see product_for.
 template <int NW, int TEAMS, int P, int T, bool X8, bool LONG, bool DELTA, bool STREAM = false>
 __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   using M = W4Lds<NW, TEAMS, P, T, X8, LONG>;
@@ -468,7 +472,9 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     e = e == ring + (M::DEPTH - 1) * M::SLOT ? ring : e + M::SLOT;
     if (full || issued < total) issue_next();
   };
-  f32x4 acc[T][2];
+  // teams: a pair's sum by itself, see the join
+  constexpr int SUMS = TEAMS > 1 ? P : 1;
+  f32x4 acc[SUMS][T][2];
   auto take_pair = [&](int i, int q, bool full) {
     wait_entry(full);
     uint4 cw[2];
@@ -497,16 +503,19 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t c[4] = {cw[h].x, cw[h].y, cw[h].z, cw[h].w};
-        const bf16x8 wf = w4_widen(c[k], __int_as_float(sc[h] << 23));
+        const uint32_t code[4] = {cw[h].x, cw[h].y, cw[h].z, cw[h].w};
+        const bf16x8 wf = w4_widen(code[k], __int_as_float(sc[h] << 23));
 #pragma unroll
-        for (int t = 0; t < T; ++t) acc[t][h] = mfma16(wf, xf[t][LONG ? 0 : i][h][k], acc[t][h]);
+        for (int t = 0; t < T; ++t) {
+          f32x4& c = acc[SUMS > 1 ? i : 0][t][h];
+          c = mfma16(wf, xf[t][LONG ? 0 : i][h][k], c);
+        }
       }
   };
   for (int tile = 0; tile < n_tiles; ++tile) {
     const int turn = M::TURNS == 2 ? tile & 1 : 0;
 #pragma unroll
-    for (int t = 0; t < T; ++t) acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < SUMS * T * 2; ++i) acc[i / (2 * T)][i / 2 % T][i % 2] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (!LONG && mine == P && issued + per_tile <= total) {
 #pragma unroll
       for (int i = 0; i < P; ++i) take_pair(i, w * P + i, true);
@@ -545,8 +554,12 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
       }
     }
 #pragma unroll
-    for (int t = 0; t < T; ++t)
-      ((f32x4*)join)[((turn * NW + wave) * T + t) * 64 + lane] = acc[t][0] + acc[t][1];
+    for (int t = 0; t < T; ++t) {
+      f32x4 sum = acc[0][t][0] + acc[0][t][1];
+#pragma unroll
+      for (int i = 1; i < SUMS; ++i) sum += acc[i][t][0] + acc[i][t][1];
+      ((f32x4*)join)[((turn * NW + wave) * T + t) * 64 + lane] = sum;
+    }
     // writes of this tile visible to all; the other buffer is free again after it.
     // The DMA in flight is not waited for.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -555,9 +568,12 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     if (w < 4 * T) {
       const int t = w / 4, i = (w % 4) * 64 + lane, al = i >> 2;
       const float* p = join + ((turn * NW + team * WT) * T + t) * 256 + i;
-      float s = p[0];
-#pragma unroll 5
-      for (int v = 1; v < WT; ++v) s += p[v * T * 256];
+      // Waves of one pair are added two and two, as a wave of two teams adds its two pairs:
+      // a token's sum has one order for a given d_in, whatever the batch.
+      constexpr int STEP = P == 1 && !LONG ? 2 : 1;
+      float s = 0.f;
+#pragma unroll 4
+      for (int v = 0; v < WT; v += STEP) s += STEP == 2 ? p[v * T * 256] + p[(v + 1) * T * 256] : p[v * T * 256];
       const int tk = 16 * t + (al & 15), row = 4 * (al >> 4) + (i & 3);
       if (DELTA) s += delta[((turn * TEAMS + team) * 16 * T + tk) * 16 + row];
       const float s1 = __shfl_xor(s, 1, kWave);
@@ -649,8 +665,16 @@ static lora_status product(W4Args a, hipStream_t s) {
   return launch_check("w4_product");
 }
 
-// The fewest registers of x that hold d_in: 16 waves with one or two pairs each,
-// 8 with five or six.  Two token tiles a block where one pair leaves room.
+// The fewest registers of x that hold d_in: 16 waves with one or two pairs each, 8 with
+// five or six (64 tokens 10240 -> 5120: five 17.9 us, six 19.0).  Where one pair leaves
+// room, a block takes two token tiles from 81 tokens on: half the blocks would read and
+// convert the codes twice (256 tokens 4096 -> 12288 39.1 us against 47.9; 96 19.9
+// against 22.6), but fewer tokens leave them too few row tiles (48 tokens 14.6 against
+// 14.1, with 64 adapters 27.5 against 24.5).  Longer rows stream x (one token 14336 ->
+// 4096 10.2 us, 64 tokens 32; kept in registers phase by phase 11.5 and 66), which reads
+// x again for every tile: at 12288 -> 4096 1, 16 and 64 tokens take 9.3, 10.0 and 28.2 us
+// so and 10.0, 12.1 and 17.2 from registers.  The choice has to follow from d_in alone: it
+// sets the order of a token's sum.
 template <bool X8, bool DELTA>
 static lora_status product_for(const W4Args& a, hipStream_t s) {
   const int64_t pairs = cdiv(a.d_in, W4_PAIR);

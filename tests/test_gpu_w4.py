@@ -159,6 +159,37 @@ def test_long_rows(n, d_in, d_out, x8):
     assert L.lora_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("d_in,d_out", [(64, 4224), (1024, 8256), (2048, 4288), (4032, 50048), (4096, 64), (8192, 128), (8192, 24640),
+                                        (9216, 64), (12288, 64), (12352, 4224)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_batch_invariance(d_in, d_out, x8):
+    """A token's bits are the same alone and in every larger batch, with adapters and without."""
+    rng = np.random.default_rng(d_in + d_out)
+    dev = torch.Generator("cuda").manual_seed(d_in)
+    codes = torch.randint(0, 256, (d_out, d_in // 2), dtype=torch.uint8, device="cuda", generator=dev)
+    scales = torch.randint(115, 125, (d_out, d_in // 32), dtype=torch.uint8, device="cuda", generator=dev)
+    n = 256
+    x, xs, _ = _x(rng, n, d_in, x8)
+    ranks = [16, 64, 8, 32]
+    pack, a_off, b_off, _, _, s = _adapters(rng, ranks, d_in, d_out)
+    ids, desc, p = dev_i32(rng.integers(0, 4, n).astype(np.int32)), L.make_desc(a_off, b_off, ranks, s), dev_bf16(pack)
+
+    def run(n, adapters):
+        y = torch.empty(n, d_out, dtype=torch.bfloat16, device="cuda")
+        if not adapters:
+            L.w4_linear(x[:n], codes, scales, y, x_scales=xs[:n] if x8 else None)
+            return bits_of(y)
+        shape = L.make_shape(n, d_in, d_out, len(pack), len(pack), 4, 64, L.IDS_INTERLEAVED)
+        ws = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape))
+        L.lora_forward_w4(shape, x[:n], codes, scales, p, p, desc, ids[:n], y, ws, x_scales=xs[:n] if x8 else None)
+        return bits_of(y)
+
+    for adapters in (False, True):
+        whole = run(n, adapters)
+        for k in (1, 4, 5, 16, 17, 80, 81):
+            assert np.array_equal(run(k, adapters), whole[:k]), (adapters, k)
+
+
 def test_bad_descriptors_and_order():
     rng = np.random.default_rng(3)
     d_in, d_out, ranks = 128, 64, [16, 16, 16, 16, 16]
