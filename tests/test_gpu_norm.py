@@ -173,6 +173,28 @@ def test_gradient_against_differences():
         assert abs((got * d).sum() - want) <= U16 * np.abs(got * d).sum() + 1e-5
 
 
+def test_weight_gradient_against_differences():
+    """dweight against central differences of the oracle in float64 (y is linear in the weight)."""
+    n, H = 37, 200
+    rng = np.random.default_rng(8)
+    h = B.round_bf16(rng.standard_normal((n, H)))
+    w, dv = B.round_bf16(1 + 0.2 * rng.standard_normal(H)), B.round_bf16(rng.standard_normal((n, H)))
+    f = lambda a: float((ON.rmsnorm_forward(h, a, EPS)[0] * dv).sum())  # noqa: E731
+    x, wd, y, rstd = dev_bf16(B.to_bf16_bits(h)), dev_bf16(B.to_bf16_bits(w)), _empty(n, H), torch.empty(n, device="cuda")
+    L.rmsnorm_forward(x, wd, EPS, y, rstd=rstd)
+    dx, dw = _empty(n, H), torch.empty(H, device="cuda")
+    ws = torch.empty(L.rmsnorm_backward_workspace_bytes(n, H), dtype=torch.uint8, device="cuda")
+    L.rmsnorm_backward(dev_bf16(B.to_bf16_bits(dv)), x, wd, rstd, dx, dweight=dw, ws=ws)
+    got = f64_of(dw)
+    mag = np.abs(dv * h / np.sqrt((h * h).mean(1, keepdims=True) + EPS)).sum(0)
+    for _ in range(5):
+        d = rng.standard_normal(H)
+        want = (f(w + 1e-3 * d) - f(w - 1e-3 * d)) / 2e-3
+        # rstd to 2^-19, two more roundings a term and n - 1 additions of 2^-24 each: below
+        # 2^-17 of the terms; the difference is exact but for float64's ~1e-10
+        assert abs((got * d).sum() - want) <= 2.0 ** -17 * (mag * np.abs(d)).sum() + 1e-8
+
+
 def test_no_rows_and_zero_gradient():
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
