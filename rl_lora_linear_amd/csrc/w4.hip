@@ -26,6 +26,7 @@
 namespace lora {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
@@ -154,9 +155,9 @@ constexpr int W4_DIRECT_TOKENS = 4;
 constexpr int W4_SCALES = 2048;                  // entry: 16 rows x 128 B of codes, then
 constexpr int W4_ENTRY = 2048 + 256;             // 16 rows x 12 B holding 8 B of scales
 // LDS of a block of NW waves in TEAMS teams and T token tiles: the rings ([slot][wave]),
-// the waves' sums (of two rounds in turn where T is 1), the deltas likewise and the
-// tokens' u.  Before the rings start, x passes through all of it but the first EARLY
-// slots, which fill meanwhile: as many as leave the number of x's rounds as it is (16
+// the waves' sums (of two rounds in turn where T is 1), the deltas likewise; at the end
+// the tokens' u.  Before the rings start, x passes through all before u but the first
+// EARLY slots, which fill meanwhile: as many as leave the number of x's rounds as it is (16
 // tokens in 8 bits 4096 -> 12288 9.4 us, 10.0 with the rings begun after x).
 // LONG: an entry holds its pair's x too.
 template <int NW, int TEAMS, int P, int T, bool X8, bool LONG>
@@ -170,10 +171,10 @@ struct W4Lds {
   static constexpr int JOIN = DEPTH * SLOT;                    // [TURNS][NW][T][64] f32x4
   static constexpr int DELTA = JOIN + TURNS * NW * T * 64 * 16;
                                                                // [TURNS][TEAMS][16 T tokens][16 rows] f32
-  static constexpr int U = DELTA + TURNS * TEAMS * T * 16 * 16 * 4;   // [16 T tokens][64] f32
-  static constexpr int END = U + T * 16 * 64 * 4;
-  static constexpr int MOST = 160 * 1024;                      // one block a CU
-  static constexpr int x_pairs(int early) { return std::min((MOST - early * SLOT) / NW / X_PAIR, T * P); }
+  static constexpr int END = DELTA + TURNS * TEAMS * T * 16 * 16 * 4;
+  static constexpr int BYTES = 160 * 1024;                     // one block a CU
+  static constexpr int U = BYTES - T * 16 * 64 * 4;            // [16 T tokens][64] f32
+  static constexpr int x_pairs(int early) { return std::min((U - early * SLOT) / NW / X_PAIR, T * P); }
   static constexpr int x_rounds(int early) {
     return x_pairs(early) > 0 ? (T * P + x_pairs(early) - 1) / x_pairs(early) : 1 << 20;
   }
@@ -184,8 +185,7 @@ struct W4Lds {
   }
   static constexpr int EARLY = early();
   static constexpr int X_PAIRS = x_pairs(EARLY);
-  static constexpr int BYTES = LONG ? END : std::max(END, EARLY * SLOT + NW * X_PAIRS * X_PAIR);
-  static_assert((LONG || X_PAIRS > 0) && BYTES <= MOST);
+  static_assert(END <= U && (LONG || (X_PAIRS > 0 && EARLY * SLOT + NW * X_PAIRS * X_PAIR <= U)));
 };
 
 struct W4Delta {
@@ -251,6 +251,21 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
   const int pairs = (a.d_in + W4_PAIR - 1) / W4_PAIR;
   // this wave's pairs: w P .. w P + P - 1; LONG: w, w + WT, ...
   const int mine = LONG ? (pairs - w + WT - 1) / WT : min(max(pairs - w * P, 0), P);
+
+  // The adapters of the delta's tokens, w + i WT, and their u are asked for before all
+  // else: nothing waits for them until the first delta.
+  float* u = (float*)(lds + M::U);
+  i32x4 tm[TOKS];   // W4Token, by scalar loads
+#pragma unroll
+  for (int i = 0; i < TOKS; ++i) {
+    const int t = w + i * WT;
+    tm[i] = i32x4{0, 0, 0, 0};
+    if (DELTA && t < toks) {
+      tm[i] = ((const __attribute__((address_space(4))) i32x4*)(uintptr_t)a.dl.tok)[tok0 + t];
+      dma4(min(lane, a.dl.max_rank - 1) * 4, a.dl.u + (int64_t)(tok0 + t) * a.dl.max_rank,
+           lds_at(u + t * 64));
+    }
+  }
 
   // x fragments: lane (l, g) of chunk h of a pair holds scale block 8 q + 4 h + g of
   // token l of a token tile.  Lanes past the last token take the last one's (their
@@ -420,21 +435,13 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
     });
   while (issued < M::DEPTH && issued < total) issue_next();
 
-  // the delta's tokens of this wave: w + i WT
   int deltas = 0;
-  float* u = (float*)(lds + M::U);
   float* delta = (float*)(lds + M::DELTA);
 #pragma unroll
   for (int i = 0; i < TOKS; ++i) {
     const int t = w + i * WT;
-    rank[i] = 0;
-    B[i] = nullptr;
-    if (DELTA && t < toks) {
-      const W4Token tm = a.dl.tok[tok0 + t];
-      rank[i] = __builtin_amdgcn_readfirstlane(tm.rank);
-      B[i] = a.dl.B_pack + uniform64(tm.b_off);
-      u[t * 64 + lane] = lane < rank[i] ? a.dl.u[(int64_t)(tok0 + t) * a.dl.max_rank + lane] : 0.f;
-    }
+    rank[i] = __builtin_amdgcn_readfirstlane(tm[i][2]);
+    B[i] = a.dl.B_pack + uniform64((int64_t)(uint32_t)tm[i][0] | (int64_t)tm[i][1] << 32);
     deltas += rank[i] > 0 ? 1 : 0;
     if (DELTA && t < 16 * T && lane < 16 * M::TURNS)   // zeros stay where a token has no delta
       delta[(((lane >> 4) * TEAMS + team) * 16 * T + t) * 16 + (lane & 15)] = 0.f;
