@@ -145,8 +145,8 @@ __global__ __launch_bounds__(64 * W4S_WAVES) void w4_shrink_kernel(
 // touch 16 rows per quarter wave: the texture path then serves 16 bytes a clock,
 // a quarter of what it does for the whole 128-byte lines that the DMA asks for.
 // At the end of a tile the waves' sums are joined through LDS (one barrier); a
-// wave owns one token's LoRA delta (two where a team has 8 waves or T is 2), whose
-// factor rows are one more ring entry.
+// wave owns one token's LoRA delta (two where a block has 8 waves or T is 2, four where
+// it has 4), whose factor rows are one more ring entry.
 constexpr int W4_PAIR = 256;                     // columns of one ring entry
 // Up to four tokens read x's fragments straight from memory (bf16 4096 -> 12288: one
 // token 8.7 us, through LDS 9.5; 8 -> 9.4 and 9.6, 16 -> 10.7 and 10.0; in 8 bits four

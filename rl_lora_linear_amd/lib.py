@@ -638,7 +638,8 @@ def adam_step_clipped(shape, table, steps, p, g, m, v, max_norm, lr, beta1=0.9, 
     pt, pp, pg, pm, pv, pn = _grad_args(shape, table, (("p", p), ("g", g), ("m", m), ("v", v)), norms)
     dev = p.get_device()
     if ws is None:
-        ws = empty_workspace(grad_workspace_bytes(shape), device=p.device)
+        with torch.cuda.stream(stream):   # cleared, and later reused, in the call's own order
+            ws = empty_workspace(grad_workspace_bytes(shape), device=p.device)
     _check(LIB.adam_step_clipped(ctypes.byref(shape), pt, _dense(steps, _I64T, (shape.n_groups,), "steps", dev),
                                  pp, pg, pm, pv, max_norm, lr, beta1, beta2, eps, weight_decay,
                                  _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16", dev), pn, _device_ptr(ws, "ws", dev),

@@ -189,6 +189,23 @@ def test_non_finite_group_is_left_alone(bad, where):
     assert np.array_equal(dm.cpu().numpy()[other] != 0, g[other] != 0) and np.any(got[other] != p[other])
 
 
+def test_fresh_workspace_on_another_stream():
+    """A workspace that the call makes itself is cleared on the call's stream, not on a busy current one."""
+    n = 5000
+    g = torch.ones(n, device="cuda")
+    g[7] = float("nan")
+    shape, table = L.make_grad_table([(0, n, 0)], 1, n)
+    p, m, v = (torch.zeros(n, device="cuda") for _ in range(3))
+    steps, side = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = torch.ones(4096, 4096, device="cuda")
+    for _ in range(50):      # some milliseconds of work on the current stream
+        a = a @ a * 2.0 ** -12
+    ws = L.adam_step_clipped(shape, table, steps, p, g, m, v, 1.0, LR, stream=side)
+    torch.cuda.synchronize()
+    assert L.lora_device_status(ws) == L.FLAG_NONFINITE_GRAD and int(steps) == 0 and not bool(m.any())
+
+
 def test_large_finite_gradients_do_not_overflow():
     n = 5000
     g = np.full(n, 3e38, np.float32)
