@@ -18,7 +18,7 @@
 // 54 to 57 us, 5.8 to 6.1 TB/s of the 7.1 that plain reads reach), by launch, first
 // access and the join where there are few (4096 x 4096 4.2 us, a launch alone 3.9;
 // 12288 x 4096 8.6), by LDS traffic and conversions in large batches of long rows (64
-// tokens 12288 -> 4096 16.9 us).  The adapters' shrink is a launch of its own, 3 us
+// tokens 12288 -> 4096 17.1 us).  The adapters' shrink is a launch of its own, 3 us
 // with one token; times in a captured graph.
 #include "common.hpp"
 #include "sgmv.hpp"

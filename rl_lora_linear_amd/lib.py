@@ -91,9 +91,9 @@ class GradShape(ctypes.Structure):
 W4_MAX_TOKENS = 256
 GRAD_CHUNK = 8192
 GRAD_DTYPE = np.dtype([("offset", "<i8"), ("count", "<i8"), ("group", "<i4"), ("first_chunk", "<i4")])
-assert GRAD_DTYPE.itemsize == 24
 DESC_DTYPE = np.dtype([("a_off", "<i8"), ("b_off", "<i8"), ("rank", "<i4"), ("scale", "<f4")])
-assert DESC_DTYPE.itemsize == 24
+DESC_BYTES = GRAD_TENSOR_BYTES = 24
+assert DESC_DTYPE.itemsize == DESC_BYTES and GRAD_DTYPE.itemsize == GRAD_TENSOR_BYTES
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -476,7 +476,7 @@ def _device_ptr(t: torch.Tensor, name: str, dev: int):
 def _stream_for(t: torch.Tensor, stream=None):
     """The stream to enqueue on (the current one if None); t must lie on the current device,
     which is where the library launches."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     if t.get_device() != dev or (stream is not None and stream.device_index != dev):
         raise LoraError(LORA_E_INVALID_ARG, f"the tensors are on {t.device}, the stream on "
                         f"{dev if stream is None else stream.device}, the current device is {dev}")
@@ -529,7 +529,7 @@ def rmsnorm_backward(dy, h, weight, rstd, dx, dh=None, dweight=None, accumulate=
                                 _dense(weight, _BF16, (hidden,), "weight", dev),
                                 _dense(rstd, _F32, (n,), "rstd", dev), _dense(dx, _BF16, dy.shape, "dx", dev),
                                 _dense(dweight, _F32, (hidden,), "dweight", dev), int(accumulate),
-                                None if ws is None else _device_ptr(ws, "ws", dev), 0 if ws is None else _nbytes(ws),
+                                None if ws is None else _device_ptr(ws, "ws", dev), 0 if ws is None else ws.nbytes,
                                 _stream_for(dy, stream)))
 
 
@@ -571,14 +571,16 @@ def lora_forward_w4(shape, x, codes, scales, A_pack, B_pack, desc, ids, y, ws, x
                     stream=None):
     """lora_forward on a 4-bit base (see w4_linear for x, codes and the scales)."""
     px, pxs, pc, ps, py = _w4_args(shape.n_tokens, shape.d_in, shape.d_out, x, x_scales, codes, scales, y)
-    for pack, elems, name in ((A_pack, shape.a_pack_elems, "A_pack"), (B_pack, shape.b_pack_elems, "B_pack")):
-        _arg(pack.dtype == torch.bfloat16 and pack.numel() >= elems, f"{name}: needs {elems} bfloat16 elements")
+    if A_pack.dtype != torch.bfloat16 or A_pack.numel() < shape.a_pack_elems:
+        raise LoraError(LORA_E_INVALID_ARG, f"A_pack: needs {shape.a_pack_elems} bfloat16 elements")
+    if B_pack.dtype != torch.bfloat16 or B_pack.numel() < shape.b_pack_elems:
+        raise LoraError(LORA_E_INVALID_ARG, f"B_pack: needs {shape.b_pack_elems} bfloat16 elements")
     dev = codes.get_device()
-    _arg(_nbytes(desc) >= shape.n_adapters * DESC_DTYPE.itemsize, "desc is shorter than n_adapters entries")
+    _arg(desc.nbytes >= shape.n_adapters * DESC_BYTES, "desc is shorter than n_adapters entries")
     _check(LIB.lora_forward_w4(ctypes.byref(shape), px, pxs, pc, ps, _device_ptr(A_pack, "A_pack", dev),
                                _device_ptr(B_pack, "B_pack", dev), _device_ptr(desc, "desc", dev),
                                _dense(ids, (torch.int32,), (shape.n_tokens,), "ids", dev), py,
-                               _device_ptr(ws, "ws", dev), _nbytes(ws), _stream_for(codes, stream)))
+                               _device_ptr(ws, "ws", dev), ws.nbytes, _stream_for(codes, stream)))
 
 
 def make_grad_table(tensors, n_groups, n_elems, device="cuda"):
@@ -608,8 +610,7 @@ def grad_workspace_bytes(shape: GradShape) -> int:
 
 
 def _grad_args(shape, table, flat, norms):
-    _arg(table.numel() * table.element_size() >= shape.n_tensors * GRAD_DTYPE.itemsize,
-         "table is shorter than n_tensors entries")
+    _arg(table.nbytes >= shape.n_tensors * GRAD_TENSOR_BYTES, "table is shorter than n_tensors entries")
     dev = flat[0][1].get_device()
     ptrs = [_dense(t, _F32, (shape.n_elems,), name, dev) for name, t in flat]
     return (_device_ptr(table, "table", dev), *ptrs, _dense(norms, _F32, (shape.n_groups,), "norms", dev))
@@ -619,14 +620,14 @@ def grad_norm(shape, table, g, norms, ws, stream=None):
     """norms[a] = the norm of group a's gradient (shape, table: make_grad_table)."""
     pt, pg, pn = _grad_args(shape, table, (("g", g),), norms)
     dev = g.get_device()
-    _check(LIB.grad_norm(ctypes.byref(shape), pt, pg, pn, _device_ptr(ws, "ws", dev), _nbytes(ws), _stream_for(g, stream)))
+    _check(LIB.grad_norm(ctypes.byref(shape), pt, pg, pn, _device_ptr(ws, "ws", dev), ws.nbytes, _stream_for(g, stream)))
 
 
 def grad_clip(shape, table, g, max_norm, out, norms, ws, stream=None):
     """out = g scaled to at most max_norm per group; out may be g, norms may be None."""
     pt, pg, po, pn = _grad_args(shape, table, (("g", g), ("out", out)), norms)
     dev = g.get_device()
-    _check(LIB.grad_clip(ctypes.byref(shape), pt, pg, max_norm, po, pn, _device_ptr(ws, "ws", dev), _nbytes(ws),
+    _check(LIB.grad_clip(ctypes.byref(shape), pt, pg, max_norm, po, pn, _device_ptr(ws, "ws", dev), ws.nbytes,
                          _stream_for(g, stream)))
 
 
@@ -643,7 +644,7 @@ def adam_step_clipped(shape, table, steps, p, g, m, v, max_norm, lr, beta1=0.9, 
     _check(LIB.adam_step_clipped(ctypes.byref(shape), pt, _dense(steps, _I64T, (shape.n_groups,), "steps", dev),
                                  pp, pg, pm, pv, max_norm, lr, beta1, beta2, eps, weight_decay,
                                  _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16", dev), pn, _device_ptr(ws, "ws", dev),
-                                 _nbytes(ws), _stream_for(p, stream)))
+                                 ws.nbytes, _stream_for(p, stream)))
     return ws
 
 

@@ -168,6 +168,7 @@ def test_operands_of_two_devices(L):
     class On:
         def __init__(self, dev, dtype, *shape):
             self.dev, self.dtype, self.shape = dev, dtype, torch.Size(shape)
+            self.nbytes = self.shape.numel() * dtype.itemsize
 
         def get_device(self):
             return self.dev
@@ -180,9 +181,6 @@ def test_operands_of_two_devices(L):
 
         def numel(self):
             return self.shape.numel()
-
-        def element_size(self):
-            return self.dtype.itemsize
 
         def data_ptr(self):
             assert self.dev == 0
