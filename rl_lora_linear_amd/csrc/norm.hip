@@ -383,12 +383,15 @@ static unsigned norm_free_grid(int64_t n, const NormPlan& p) {
   return norm_grid(n, p, std::max<int64_t>(1, (1 << 20) / p.block));
 }
 
-// Blocks that keep dw partials: at least one a CU, and 2^17 threads in all (8 waves a
-// CU): the partials, written and read again, are then 8 MB at most columns (at 8192 x
-// 4096 51.6 us; with twice the blocks 56.5, with half of them 69.7).
+// Blocks that keep dw partials: 2^17 threads in all (8 waves a CU), so that the partials,
+// written and read again, are 8 MB at most columns (at 8192 x 4096 51.6 us; with twice the
+// blocks 56.5, with half of them 69.7), and as many on every CU: rounded up to whole
+// multiples of 256, or down where that would leave blocks without a row (2790 x 7168: 512
+// blocks 35.6 us, 256 43.0, 292 40.3; 500 x 7168: 256 blocks 13.6, 500 15.3).
 int64_t rmsnorm_bwd_blocks(int64_t n, int64_t hidden) {
   const NormPlan p = norm_plan(hidden);
-  return norm_grid(n, p, std::max<int64_t>(256, (1 << 17) / p.block));
+  const int64_t most = (1 << 17) / p.block, up = align_up(most, 256);
+  return norm_grid(n, p, n >= up * (p.block / p.team) ? up : std::max<int64_t>(256, most / 256 * 256));
 }
 
 // Calls that move more than 96 MB, three eighths of the last-level cache, make
