@@ -685,20 +685,25 @@ static lora_status product(W4Args a, hipStream_t s) {
 template <bool X8, bool DELTA>
 static lora_status product_for(const W4Args& a, hipStream_t s) {
   const int64_t pairs = cdiv(a.d_in, W4_PAIR);
+  // Codes of more than 96 MB, three eighths of the last-level cache, are read
+  // non-temporally where one token tile reads them once: 151936 x 4096 54.2 us against
+  // 60.8, 32768 x 8192 28.3 against 30.6; 12288 x 4096 (25 MB, found in that cache) 9.2
+  // against 8.8.
+  const bool streams = !DELTA && a.n <= 16 && (int64_t)a.d_out * a.d_in / 2 > (int64_t)96 << 20;
+  // Up to 2048 columns one row tile would leave half of the waves without a pair: two
+  // teams take two tiles, where there are more tiles than CUs (one token 1024 -> 49152
+  // 9.5 us against 13.0, 2048 -> 49152 12.3 against 13.9; 64 tokens 2048 -> 25600 16.9
+  // against 21.1; 2048 -> 4096, 256 tiles, 4.2 against 4.0), and up to 1024 columns four
+  // (64 tokens 1024 -> 25600 11.7 against 13.5 with two; two token tiles as well serve
+  // more than 80 tokens better: 256 28.2 against 29.3).  With adapters a wave of two teams
+  // has two tokens' deltas, which sixteen tokens do not gain from (2048 -> 12288 14.7 us
+  // against 13.7; 64 tokens 1024 -> 25600 35.2 against 39.0), and with two token tiles four,
+  // for which the registers do not suffice.
+  const int64_t tiles = a.d_out / 16 * cdiv(a.n, 16);
   if constexpr (!DELTA) {
-    // Codes of more than 96 MB, three eighths of the last-level cache, are read
-    // non-temporally where one token tile reads them once: 151936 x 4096 54.2 us against
-    // 60.8, 32768 x 8192 28.3 against 30.6; 12288 x 4096 (25 MB, found in that cache) 9.2
-    // against 8.8.
-    const bool streams = a.n <= 16 && (int64_t)a.d_out * a.d_in / 2 > (int64_t)96 << 20;
-    // Up to 2048 columns one row tile would leave half of the waves without a pair: two
-    // teams take two tiles, where there are more tiles than CUs (one token 1024 -> 49152
-    // 9.5 us against 13.0, 2048 -> 49152 12.3 against 13.9; 2048 -> 4096, 256 tiles, 4.2
-    // against 4.0).  With adapters a wave of two teams would have two tokens' deltas
-    // (sixteen tokens 2048 -> 12288 14.7 us against 13.7).
-    if (a.n <= 16 && pairs <= 8 && a.d_out / 16 > device_cus())
-      return streams ? product<16, 2, 1, 1, X8, false, false, true>(a, s)
-                     : product<16, 2, 1, 1, X8, false, false>(a, s);
+    if (pairs <= 4 && !streams && a.n <= 80 && tiles > 2 * device_cus())
+      return product<16, 4, 1, 1, X8, false, false>(a, s);
+    if (streams && pairs <= 8) return product<16, 2, 1, 1, X8, false, false, true>(a, s);
     if (streams && pairs <= 16) {
       // up to 4096 columns two teams halve the rounds (one token's 151936 x 4096 57.0 us
       // against 60.3), but read x twice (sixteen tokens 67.0 against 63.0)
@@ -706,6 +711,11 @@ static lora_status product_for(const W4Args& a, hipStream_t s) {
                                      : product<16, 1, 1, 1, X8, false, false, true>(a, s);
     }
     if (streams && pairs <= 32) return product<16, 1, 2, 1, X8, false, false, true>(a, s);
+  }
+  if (pairs <= 8 && tiles > device_cus()) {
+    if (a.n <= 80 && (!DELTA || a.n > 16)) return product<16, 2, 1, 1, X8, false, DELTA>(a, s);
+    if constexpr (!DELTA)
+      if (a.n > 80) return product<16, 2, 1, 2, X8, false, false>(a, s);
   }
   if (pairs <= 16)
     return a.n > 80 ? product<16, 1, 1, 2, X8, false, DELTA>(a, s)

@@ -61,7 +61,9 @@ SIZES = [(1, 64, 64), (1, 4096, 64), (2, 192, 128), (7, 320, 192), (15, 1024, 32
          (3, 4352, 64), (20, 4416, 128), (2, 8192, 64), (33, 8192, 64), (5, 8256, 64), (17, 10240, 64), (4, 10304, 128), (40, 12288, 64),
          (40, 13056, 64), (256, 12352, 64),
          # more row tiles than CUs, of few columns: two teams of waves a block
-         (1, 64, 4224), (16, 320, 4160), (3, 2048, 4288), (5, 1984, 8256)]
+         (1, 64, 4224), (16, 320, 4160), (3, 2048, 4288), (5, 1984, 8256),
+         # four teams, and two with two token tiles
+         (3, 1024, 8256), (40, 320, 4160), (90, 1984, 4160)]
 
 
 @pytest.mark.parametrize("x8", [False, True])
