@@ -78,10 +78,7 @@ struct W4Adapters {
 
 __device__ __forceinline__ bool w4_desc_ok(const lora_adapter_desc& d, const W4Adapters& a, int d_in,
                                            int d_out) {
-  const int64_t r = d.rank;
-  return r >= 8 && r <= 64 && (r % 8) == 0 && r <= a.max_rank && d.a_off >= 0 && d.b_off >= 0 &&
-         (d.a_off % 8) == 0 && (d.b_off % 8) == 0 && d.a_off + r * d_in <= a.a_elems &&
-         d.b_off + r * d_out <= a.b_elems;
+  return desc_ok(d, a.max_rank, d_in, d_out, a.a_elems, a.b_elems);
 }
 
 template <bool X8>

@@ -369,3 +369,25 @@ def test_codes_past_four_gigabytes():
     rest = torch.ones(d_out, dtype=torch.bool, device="cuda")
     rest[torch.from_numpy(rows).to("cuda")] = False
     assert bool((y[:, rest] == 0).all())
+
+
+@pytest.mark.parametrize("which", ["A", "B"])
+@pytest.mark.parametrize("offset", [(1 << 63) - 8, (1 << 63) - 16 * 128 - 8, 1 << 62])
+def test_offsets_near_the_largest_integer(which, offset):
+    """A descriptor whose end lies past 64 bits: flagged, its token gets the base output, the others their own."""
+    rng = np.random.default_rng(12)
+    d_in, d_out, ranks, n = 128, 64, [16, 8, 16], 3
+    codes, scales = _weights(rng, d_out, d_in)
+    pack, a_off, b_off, _, _, s = _adapters(rng, ranks, d_in, d_out)
+    x, _, _ = _x(rng, n, d_in, False)
+    p, ids = dev_bf16(pack), dev_i32(np.arange(n))
+    shape = L.make_shape(n, d_in, d_out, len(pack), len(pack), 3, 16, L.IDS_INTERLEAVED)
+    ws = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape))
+    good, y, base = (torch.empty(n, d_out, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    L.w4_linear(x, _dev(codes), _dev(scales), base)
+    L.lora_forward_w4(shape, x, _dev(codes), _dev(scales), p, p, L.make_desc(a_off, b_off, ranks, s), ids, good, ws)
+    assert L.lora_device_status(ws) == 0
+    (a_off if which == "A" else b_off)[1] = offset
+    L.lora_forward_w4(shape, x, _dev(codes), _dev(scales), p, p, L.make_desc(a_off, b_off, ranks, s), ids, y, ws)
+    assert L.lora_device_status(ws) == L.FLAG_BAD_DESC
+    assert np.array_equal(bits_of(y)[[0, 2]], bits_of(good)[[0, 2]]) and np.array_equal(bits_of(y)[1], bits_of(base)[1])
