@@ -67,14 +67,11 @@ __global__ __launch_bounds__(KEYSCAN_WAVES * kWave) void seg_keyscan_kernel(
     for (int i = 0; i < tabs.n_tabs; ++i) {
       const lora_host::SegDescs& t = tabs.tab[i];
       const lora_adapter_desc d = t.desc[k];
-      const int64_t r = d.rank;
-      if (r == 0) {
+      if (d.rank == 0) {
         on = false;
         continue;
       }
-      const bool ok = r >= 8 && r <= 64 && (r % 8) == 0 && r <= max_rank && d.a_off >= 0 &&
-                      d.b_off >= 0 && (d.a_off % 8) == 0 && (d.b_off % 8) == 0 &&
-                      d.a_off + r * t.d_in <= t.a_elems && d.b_off + t.d_out * r <= t.b_elems;
+      const bool ok = desc_ok(d, max_rank, t.d_in, t.d_out, t.a_elems, t.b_elems);
       if (!ok) set_flag(status, LORA_FLAG_BAD_DESC);
       on = on && ok;
     }
@@ -266,15 +263,11 @@ __global__ __launch_bounds__(1024) void seg_small_kernel(
         for (int i = 0; i < 3; ++i) {
           if (i >= tabs.n_tabs) break;
           const lora_host::SegDescs& tb = tabs.tab[i];
-          const int64_t rk = d[i].rank;
-          if (rk == 0) {
+          if (d[i].rank == 0) {
             on = false;
             continue;
           }
-          const bool ok = rk >= 8 && rk <= 64 && (rk % 8) == 0 && rk <= max_rank &&
-                          d[i].a_off >= 0 && d[i].b_off >= 0 && (d[i].a_off % 8) == 0 &&
-                          (d[i].b_off % 8) == 0 && d[i].a_off + rk * tb.d_in <= tb.a_elems &&
-                          d[i].b_off + tb.d_out * rk <= tb.b_elems;
+          const bool ok = desc_ok(d[i], max_rank, tb.d_in, tb.d_out, tb.a_elems, tb.b_elems);
           if (!ok) set_flag(status, LORA_FLAG_BAD_DESC);
           on = on && ok;
         }

@@ -272,3 +272,26 @@ def test_host_validation_errors():
     with pytest.raises(L.LoraError) as e:
         L.lora_forward(dl.shape, dl.x, dl.W, dl.pack, dl.pack, dl.desc, dl.ids, y, u, small)
     assert e.value.status == L.LORA_E_WORKSPACE
+
+
+@pytest.mark.parametrize("kind", ["ragged", "tall"])     # one block builds the segments, or several launches do
+@pytest.mark.parametrize("which", ["A", "B"])
+def test_offsets_near_the_largest_integer(kind, which):
+    """A descriptor whose end lies past 64 bits is flagged and its adapter inactive: the bits of an unused slot."""
+    c = _case(kind)
+    off = {"A": c.a_off.astype(np.int64).copy(), "B": c.b_off.astype(np.int64).copy()}
+    results = []
+    for rank0, offset in ((True, None), (False, (1 << 63) - 8), (False, 1 << 62)):
+        a = {k: v.copy() for k, v in off.items()}
+        if offset:
+            a[which][2] = offset
+        dl = DevLayer(c)
+        dl.desc = L.make_desc(a["A"], a["B"], np.where((np.arange(c.n_adapters) == 2) & rank0, 0, c.ranks), dl.scales32)
+        y, u = dl.forward()
+        assert dl.status() == (0 if rank0 else L.FLAG_BAD_DESC)
+        grad = torch.zeros(c.pack_elems, device="cuda")
+        dx, g = dl.backward(u, grad=grad)
+        assert dl.status() == (0 if rank0 else L.FLAG_BAD_DESC)
+        results.append((bits_of(y), bits_of(u), bits_of(dx), g.cpu().numpy()))
+    for other in results[1:]:
+        assert all(np.array_equal(p, q) for p, q in zip(results[0], other))
