@@ -506,7 +506,7 @@ lora_status rmsnorm_forward_q8(int64_t n, int64_t hidden, const uint16_t* x,
  *   dweight_j = sum_t dy_tj xh_tj  (fp32 [hidden], nullable: a frozen weight;
  *   accumulate != 0 adds into it, 0 overwrites it, with zeros for n = 0).
  *   dy, dh, h bf16 [n][hidden]; rstd fp32 [n] from the forward
- *   dx bf16 [n][hidden] out, may be dy or dh
+ *   dx bf16 [n][hidden] out, may be dy or dh, must not overlap h
  * dweight is summed in a fixed order: results are bitwise repeatable.
  * Workspace: needed only with dweight (else ws may be NULL). */
 size_t rmsnorm_backward_workspace_bytes(int64_t n, int64_t hidden);

@@ -1101,6 +1101,12 @@ lora_status bf16_add(int64_t n, const uint16_t* a, const uint16_t* b, uint16_t* 
 }
 
 // ------------------------------------------------------------------ RMS norm
+// Whether two buffers share a byte (a NULL one shares none).
+static bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+  return a && b && (p <= q ? q - p < (uintptr_t)a_bytes : p - q < (uintptr_t)b_bytes);
+}
+
 static lora_status norm_checks(int64_t n, int64_t hidden, const char* what) {
   LORA_ARG_CHECK(n >= 0 && n <= INT32_MAX / 2, "%s: n %lld outside [0, 2^30)", what, (long long)n);
   LORA_ARG_CHECK(hidden > 0, "%s: hidden must be positive", what);
@@ -1171,6 +1177,7 @@ lora_status rmsnorm_backward(int64_t n, int64_t hidden, const uint16_t* dy, cons
     return LORA_E_WORKSPACE;
   }
   LORA_ARG_CHECK(!dweight || aligned16(ws), "rmsnorm_backward: the workspace must be 16-byte aligned");
+  LORA_ARG_CHECK(!overlap(dx, n * hidden * 2, h, n * hidden * 2), "rmsnorm_backward: dx overlaps h");
   if (n == 0 && !dweight) return LORA_OK;
   return launch_rmsnorm_bwd(n, hidden, dy, dh, h, weight, rstd, dx, dweight, accumulate,
                             dweight ? (float*)((char*)ws + 256) : nullptr, S(stream));

@@ -195,3 +195,14 @@ def test_operands_of_two_devices(L):
                  lambda: L.grad_norm(L.GradShape(4, 1, 1, 1), On(1, u, 24), On(0, f, 4), On(0, f, 1), On(0, u, 512))):
         with pytest.raises(L.LoraError, match="on device"):
             call()
+
+
+def test_norm_gradient_in_the_place_of_h(L):
+    """dx may be dy or dh; h is read only, also where only a part of it lies under dx."""
+    n, H, E = 4, 64, L.LORA_E_INVALID_ARG
+    at = lambda byte: ctypes.c_void_p((1 << 20) + byte)  # noqa: E731
+    bwd = lambda h, dx: L.LIB.rmsnorm_backward(n, H, P, None, h, P, P, dx, None, 0, None, 0, None)  # noqa: E731
+    size = n * H * 2
+    for byte in (0, 16, size - 16):
+        _is(L, bwd(at(0), at(byte)), E, b"dx overlaps h")
+        _is(L, bwd(at(byte), at(0)), E, b"dx overlaps h")
