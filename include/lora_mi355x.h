@@ -492,8 +492,9 @@ lora_status rmsnorm_forward(int64_t n, int64_t hidden, const uint16_t* x, const 
  *   NaN code.
  *   q        uint8 [n][hidden] out     OCP e4m3 codes
  *   q_scales uint8 [n][hidden/32] out  e + 127 (E8M0)
- * This is the x that w4_linear and lora_forward_w4 take with x_scales.
- * hidden a multiple of 32; the rest as rmsnorm_forward. */
+ * This is the x that w4_linear and lora_forward_w4 take with x_scales (at most
+ * LORA_W4_MAX_TOKENS rows a call).  q and q_scales must not overlap x, residual
+ * or h.  hidden a multiple of 32; the rest as rmsnorm_forward. */
 lora_status rmsnorm_forward_q8(int64_t n, int64_t hidden, const uint16_t* x,
                                const uint16_t* residual, const uint16_t* weight, float eps,
                                uint16_t* h, uint8_t* q, uint8_t* q_scales, float* rstd,

@@ -1152,6 +1152,13 @@ lora_status rmsnorm_forward_q8(int64_t n, int64_t hidden, const uint16_t* x,
     set_error("rmsnorm_forward_q8: hidden %lld must be a multiple of 32", (long long)hidden);
     return LORA_E_UNSUPPORTED;
   }
+  // rows of q are half as long as rows of x: one row's codes would lie in another's x
+  const int64_t row_bytes[2] = {n * hidden, n * (hidden / 32)};
+  const void* const out[2] = {q, q_scales};
+  for (int i = 0; i < 2; ++i)
+    for (const void* in : {(const void*)x, (const void*)residual, (const void*)h})
+      LORA_ARG_CHECK(!overlap(out[i], row_bytes[i], in, n * hidden * 2),
+                     "rmsnorm_forward_q8: q or q_scales overlaps x, residual or h");
   if (n == 0) return LORA_OK;
   return launch_rmsnorm_fwd(n, hidden, x, residual, weight, eps, h, nullptr, q, q_scales, rstd,
                             S(stream));

@@ -206,3 +206,20 @@ def test_norm_gradient_in_the_place_of_h(L):
     for byte in (0, 16, size - 16):
         _is(L, bwd(at(0), at(byte)), E, b"dx overlaps h")
         _is(L, bwd(at(byte), at(0)), E, b"dx overlaps h")
+
+
+def test_eight_bit_norm_in_the_place_of_its_input(L):
+    """q's rows are shorter than x's: no place inside x, residual or h suits them."""
+    n, H, E = 4, 64, L.LORA_E_INVALID_ARG
+    at = lambda byte: ctypes.c_void_p((1 << 20) + byte)  # noqa: E731
+    far = {"x": at(1 << 14), "r": at(2 << 14), "h": at(3 << 14), "q": at(4 << 14), "s": at(5 << 14)}
+
+    def call(**kw):
+        a = {**far, **kw}
+        return L.LIB.rmsnorm_forward_q8(n, H, a["x"], a["r"], P, 1e-6, a["h"], a["q"], a["s"], None, None)
+
+    for name in ("x", "r", "h"):
+        for byte in (0, n * H, 2 * n * H - 16):
+            place = ctypes.c_void_p(far[name].value + byte)
+            _is(L, call(q=place), E, b"overlaps")
+            _is(L, call(s=place), E, b"overlaps")
