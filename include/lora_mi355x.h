@@ -551,7 +551,7 @@ lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
  * the base product, s_a A_a x_t and the delta in fp32, rounded once.  Shape,
  * packs, descriptors, ids (sorted or not), their device checks and flags as for
  * lora_forward: a token with an invalid id or an inactive adapter gets the base
- * output.  x and x_scales, codes and scales as for w4_linear;
+ * output.  x and x_scales, codes and scales as for w4_linear; desc 8-byte aligned;
  * n_tokens <= LORA_W4_MAX_TOKENS.  Workspace:
  * lora_forward_w4_workspace_bytes(shape); word 0 is the status word. */
 size_t lora_forward_w4_workspace_bytes(const lora_shape* shape);
@@ -569,6 +569,7 @@ lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_
  *   device array of n_tensors entries, sorted by group; tensors must not
  *   overlap; first_chunk_0 = 0 and first_chunk_{i+1} = first_chunk_i +
  *   ceil(count_i / LORA_GRAD_CHUNK); n_chunks is the sum over all entries.
+ * The table is 8-byte aligned.
  * Elements outside every tensor are never touched.  The device checks every entry
  * (but for overlaps): one that breaks these rules sets LORA_FLAG_BAD_DESC and is
  * never used as an address beyond n_elems.  What the groups of such a table give is

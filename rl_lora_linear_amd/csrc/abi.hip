@@ -174,6 +174,8 @@ lora_status check_shape(const lora_shape* sh) {
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+// A table read by scalar loads, which drop an address's low bits.
+bool aligned8(const void* p) { return ((uintptr_t)p & 7) == 0; }
 
 lora_status layer_segments(const lora_shape& sh, const lora_adapter_desc* desc,
                            const int32_t* ids, const LayerWs& w, hipStream_t s) {
@@ -1249,6 +1251,7 @@ lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_
                  "codes, scales, A_pack, B_pack and desc must be non-NULL");
   LORA_ARG_CHECK(aligned16(codes) && aligned16(scales) && aligned16(A_pack) && aligned16(B_pack),
                  "codes, scales and the packs must be 16-byte aligned");
+  LORA_ARG_CHECK(aligned8(desc), "lora_forward_w4: desc must be 8-byte aligned");
   LORA_ARG_CHECK(sh.n_tokens == 0 || (x && adapter_ids && y), "x, adapter_ids and y must be non-NULL");
   LORA_ARG_CHECK(sh.n_tokens == 0 || (aligned16(x) && aligned16(y)), "x and y must be 16-byte aligned");
   if (!ws || ws_bytes < w4_ws_bytes(sh.n_tokens, sh.max_rank)) {
@@ -1283,6 +1286,7 @@ static lora_status grad_checks(const grad_shape* shape, const grad_tensor* table
                                float max_norm, void* ws, size_t ws_bytes, const char* what) {
   TRY(check_grad_shape(shape));
   LORA_ARG_CHECK(shape->n_tensors == 0 || table, "%s: table is NULL", what);
+  LORA_ARG_CHECK(aligned8(table), "%s: table must be 8-byte aligned", what);
   LORA_ARG_CHECK(shape->n_chunks == 0 || g, "%s: g is NULL", what);
   LORA_ARG_CHECK(max_norm >= 0.f, "%s: max_norm must be >= 0 (and not NaN)", what);
   if (!ws || ws_bytes < grad_ws_bytes(*shape)) {

@@ -223,3 +223,15 @@ def test_eight_bit_norm_in_the_place_of_its_input(L):
             place = ctypes.c_void_p(far[name].value + byte)
             _is(L, call(q=place), E, b"overlaps")
             _is(L, call(s=place), E, b"overlaps")
+
+
+@pytest.mark.parametrize("byte", [65, 66, 68])
+def test_tables_that_are_not_aligned(L, byte):
+    """Descriptors and gradient tables cut out of a byte buffer at any place but a multiple of 8."""
+    lib, E, at = L.LIB, L.LORA_E_INVALID_ARG, ctypes.c_void_p(byte)
+    sh = L.make_shape(2, 128, 64, 4096, 4096, 4, 16, L.IDS_INTERLEAVED)
+    _is(L, lib.lora_forward_w4(ctypes.byref(sh), P, None, P, P, P, P, at, P, P, P, BIG, None), E, b"desc must be 8-byte aligned")
+    good = L.GradShape(1000, 2, 2, 1)
+    _is(L, lib.grad_norm(ctypes.byref(good), at, P, P, P, BIG, None), E, b"table must be 8-byte aligned")
+    _is(L, lib.grad_clip(ctypes.byref(good), at, P, 1.0, P, P, P, BIG, None), E, b"table must be 8-byte aligned")
+    _is(L, lib.adam_step_clipped(ctypes.byref(good), at, P, P, P, P, P, 1.0, 1e-3, 0.9, 0.99, 1e-8, 0.0, None, P, P, BIG, None), E, b"table must be 8-byte")
