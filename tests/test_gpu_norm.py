@@ -246,3 +246,117 @@ def test_on_another_stream():
     L.rmsnorm_forward(x, w, EPS, y, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert np.array_equal(bits_of(y), bits_of(ref))
+
+
+def _device_rows(seed, n, H):
+    """_rows' kind of rows, made on the device (for batches of hundreds of megabytes)."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    size = torch.randint(-8, 8, (n, 1), generator=g, device="cuda").float().exp2()
+    wide = torch.where(torch.rand(H, generator=g, device="cuda") < 0.02, 30.0, 1.0)
+    return (torch.randn(n, H, generator=g, device="cuda") * size * wide).to(torch.bfloat16)
+
+
+# calls of more than 96 MB (non-temporal accesses), several rounds of every block: rows of one wave's team, of
+# several waves, past 16384 columns, and element by element
+LARGE = [(8193, 4096), (131075, 128), (2051, 20480), (5003, 4099)]
+
+
+def _sample(n):
+    return np.unique(np.concatenate(([0, 1, n // 2, n - 2, n - 1], np.random.default_rng(n).integers(0, n, 60))))
+
+
+@pytest.mark.parametrize("n,H", LARGE)
+def test_forward_large(n, H):
+    x, r, w = _device_rows(1, n, H), _device_rows(2, n, H), dev_bf16(B.to_bf16_bits(1 + 0.3 * np.random.default_rng(H).standard_normal(H)))
+    h, y, rstd = _empty(n, H), _empty(n, H), torch.full((n,), float("nan"), device="cuda")
+    L.rmsnorm_forward(x, w, EPS, y, rstd=rstd, residual=r, h=h)
+    assert bool((h == (x.float() + r.float()).to(torch.bfloat16)).all()) and bool(torch.isfinite(rstd).all()) and bool(torch.isfinite(y).all())
+    at = torch.from_numpy(_sample(n)).to("cuda")
+    v, rs = ON.rmsnorm_forward(f64_of(h[at]), f64_of(w), EPS)
+    _close(f64_of(rstd[at]), rs, U32)
+    _close(f64_of(y[at]), v, U16 + 2 * U32)
+    # the same rows in a small batch: the same bits
+    h2, y2, rstd2 = _empty(len(at), H), _empty(len(at), H), torch.empty(len(at), device="cuda")
+    L.rmsnorm_forward(x[at], w, EPS, y2, rstd=rstd2, residual=r[at], h=h2)
+    assert np.array_equal(bits_of(y2), bits_of(y[at])) and np.array_equal(bits_of(h2), bits_of(h[at])) and torch.equal(rstd2, rstd[at])
+    if H % 32 == 0:
+        q, s = torch.full((n, H), 0x7F, dtype=torch.uint8, device="cuda"), torch.full((n, H // 32), 255, dtype=torch.uint8, device="cuda")
+        L.rmsnorm_forward_q8(x, w, EPS, q, s, rstd=rstd, residual=r, h=h)
+        q2, s2 = torch.empty(len(at), H, dtype=torch.uint8, device="cuda"), torch.empty(len(at), H // 32, dtype=torch.uint8, device="cuda")
+        L.rmsnorm_forward_q8(x[at], w, EPS, q2, s2, residual=r[at], h=h2)
+        assert torch.equal(q2, q[at]) and torch.equal(s2, s[at]) and torch.equal(rstd[at], rstd2)
+        e = s[at].cpu().numpy().astype(int) - 127
+        scale = np.repeat(np.exp2(e.astype(float)), 32, axis=1)
+        val = q[at].view(torch.float8_e4m3fn).float().cpu().numpy().astype(np.float64) * scale
+        bad = ~(np.abs(val - v) <= np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10 * scale) * (1 + U32) + 2 * U32 * np.abs(v))
+        assert not bad.any()
+        # no value saturates, and none could do with half the scale
+        top = np.abs(v).reshape(len(at), -1, 32).max(axis=2) / np.exp2(e.astype(float))
+        assert np.all(top <= 448 * (1 + 2 * U32)) and np.all((top >= 224 * (1 - 2 * U32)) | (e == -126))
+        assert bool((q & 127 != 127).all()) and bool((s != 255).all())
+
+
+@pytest.mark.parametrize("dh,dw", [(True, True), (False, False)])
+@pytest.mark.parametrize("n,H", LARGE)
+def test_backward_large(n, H, dh, dw):
+    h, dy, u = _device_rows(3, n, H), _device_rows(4, n, H), _device_rows(5, n, H) if dh else None
+    w = dev_bf16(B.to_bf16_bits(1 + 0.3 * np.random.default_rng(H).standard_normal(H)))
+    rstd = torch.cat([1 / (p.double().square().mean(1) + EPS).sqrt() for p in h.split(1024)]).float()
+    g_w, ws = None, None
+    if dw:
+        g_w, ws = torch.full((H,), float("nan"), device="cuda"), L.empty_workspace(L.rmsnorm_backward_workspace_bytes(n, H))
+    dx = _empty(n, H)
+    L.rmsnorm_backward(dy, h, w, rstd, dx, dh=u, dweight=g_w, ws=ws)
+    assert bool(torch.isfinite(dx).all())
+    at = torch.from_numpy(_sample(n)).to("cuda")
+    d64, h64, w64, r64 = (f64_of(t) for t in (dy[at], h[at], w, rstd[at]))
+    want, _ = ON.rmsnorm_backward(d64, h64, w64, r64, f64_of(u[at]) if dh else None)
+    # as in test_backward: the mean of g xh, the other terms
+    r = r64[:, None]
+    g, xh = d64 * w64, h64 * r
+    slack = r * np.abs(xh) * np.mean(np.abs(g * xh), axis=1, keepdims=True) * 2.0 ** -18 + r * np.abs(g) * 2.0 ** -21
+    if dh:
+        slack += np.abs(f64_of(u[at])) * 2.0 ** -23
+    _close(f64_of(dx[at]), want, U16, extra=slack * (1 + U16))
+    small = _empty(len(at), H)
+    L.rmsnorm_backward(dy[at], h[at], w, rstd[at], small, dh=u[at] if dh else None)
+    assert np.array_equal(bits_of(small), bits_of(dx[at]))
+    if dw:
+        term = [(p.double() * q.double() * s.double()[:, None]) for p, q, s in zip(dy.split(1024), h.split(1024), rstd.split(1024))]
+        want_w, mag = sum(t.sum(0) for t in term), sum(t.abs().sum(0) for t in term)
+        # additions behind one another: a team's rows, the block's teams, every 128th of its blocks, then 4 and 32 sums of
+        # these; each off by 2^-24 of the magnitudes, and two products before them
+        blocks = (L.rmsnorm_backward_workspace_bytes(n, H) - 256) // (4 * H)
+        teams = 16 if H == 128 else 1
+        steps = -(-n // (blocks * teams)) + teams + -(-blocks // 128) + 4 + 32 + 2
+        _close(f64_of(g_w), f64_of(want_w), 2.0 ** -24, extra=steps * 2.0 ** -24 * f64_of(mag))
+        again = torch.zeros(H, device="cuda")
+        L.rmsnorm_backward(dy, h, w, rstd, dx, dh=u, dweight=again, accumulate=True, ws=ws)
+        assert torch.equal(again, g_w)
+
+
+@pytest.mark.parametrize("n,H", [(5, 64), (9, 33), (300, 2048), (3, 4099), (2, 20480)])
+def test_outputs_in_the_place_of_inputs(n, H):
+    """h in the place of x or of residual, y then in the other's; dx in the place of dh."""
+    rng = np.random.default_rng(n + H)
+    x, r, w = dev_bf16(_rows(rng, n, H)), dev_bf16(_rows(rng, n, H)), dev_bf16(B.to_bf16_bits(1 + 0.3 * rng.standard_normal(H)))
+    h, y = _empty(n, H), _empty(n, H)
+    L.rmsnorm_forward(x, w, EPS, y, residual=r, h=h)
+    for place in ("x", "residual"):
+        a, b, out = x.clone(), r.clone(), _empty(n, H)
+        L.rmsnorm_forward(a, w, EPS, out, residual=b, h=a if place == "x" else b)
+        assert np.array_equal(bits_of(out), bits_of(y)) and np.array_equal(bits_of(a if place == "x" else b), bits_of(h))
+    a, b = x.clone(), r.clone()
+    L.rmsnorm_forward(a, w, EPS, a, residual=b, h=b)
+    assert np.array_equal(bits_of(a), bits_of(y)) and np.array_equal(bits_of(b), bits_of(h))
+    if H % 32 == 0:
+        q, s = torch.empty(n, H, dtype=torch.uint8, device="cuda"), torch.empty(n, H // 32, dtype=torch.uint8, device="cuda")
+        q2, s2 = torch.empty_like(q), torch.empty_like(s)
+        L.rmsnorm_forward_q8(x, w, EPS, q, s, residual=r, h=h)
+        a = x.clone()
+        L.rmsnorm_forward_q8(a, w, EPS, q2, s2, residual=r, h=a)
+        assert torch.equal(q, q2) and torch.equal(s, s2) and np.array_equal(bits_of(a), bits_of(h))
+    rstd, dx, u = torch.rand(n, device="cuda"), _empty(n, H), dev_bf16(_rows(rng, n, H))
+    L.rmsnorm_backward(y, h, w, rstd, dx, dh=u)
+    L.rmsnorm_backward(y, h, w, rstd, u, dh=u)
+    assert np.array_equal(bits_of(u), bits_of(dx))
