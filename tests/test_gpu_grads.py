@@ -294,3 +294,71 @@ def test_elements_past_32_bits():
     assert list(f64_of(norms)) == [60.0, 0.0]
     _close(f64_of(g[n - 900:]), np.full(900, 0.2), 2.0 ** -21)
     assert not bool(g[:n - 900].any())
+
+
+def _crowd(blocks_over):
+    """20000 tensors of a few elements over 300 uneven groups, empty ones between them, and one group that spans many
+    blocks: more chunks than blocks in every launch, groups that begin and end inside a block."""
+    rng = np.random.default_rng(blocks_over)
+    owner = np.sort((300 * rng.random(20000) ** 2).astype(int))
+    counts = rng.integers(0, 6, 20000)
+    counts[rng.integers(0, 20000, 40)] = rng.integers(8000, 9000, 40)
+    counts[np.searchsorted(owner, 150)] = blocks_over * L.GRAD_CHUNK + 77
+    gaps = rng.integers(0, 3, 20000)
+    ends = np.cumsum(counts + gaps)
+    tensors = [(int(e - g - c), int(c), int(a)) for e, g, c, a in zip(ends, gaps, counts, owner)]
+    return tensors, 301, int(ends[-1]) + 3
+
+
+@pytest.mark.parametrize("bad", [False, True])
+def test_more_chunks_than_blocks(bad):
+    tensors, G, n = _crowd(60)
+    rng = np.random.default_rng(7)
+    g = (rng.standard_normal(n) * np.exp2(rng.integers(-20, 4, n))).astype(np.float32)
+    shape, table = L.make_grad_table(tensors, G, n)
+    assert shape.n_chunks > 16384      # the most blocks of any launch
+    ws = L.empty_workspace(L.grad_workspace_bytes(shape))
+    owner = np.full(n, -1)
+    for o, c, a in tensors:
+        owner[o:o + c] = a
+    inside = owner >= 0
+    sick = 149 if bad else G     # (no group)
+    if bad:
+        g[np.flatnonzero(owner == sick)[-1]] = np.inf
+    dg, norms = dev_f32(g), torch.full((G,), -1.0, device="cuda")
+    flag = L.FLAG_NONFINITE_GRAD if bad else 0
+    L.grad_norm(shape, table, dg, norms, ws)
+    assert L.lora_device_status(ws) == flag
+    want = OC.norms(tensors, G, g)
+    _close(np.delete(f64_of(norms), sick) if bad else f64_of(norms), np.delete(want, sick) if bad else want, 2.0 ** -23)
+    assert f64_of(norms)[G - 1] == 0 and (not bad or np.isinf(f64_of(norms)[sick]))
+    max_norm = float(np.median(want[want > 0]))
+    out, norms2 = torch.full((n,), 7.0, device="cuda"), torch.empty(G, device="cuda")
+    L.grad_clip(shape, table, dg, max_norm, out, norms2, ws)
+    assert L.lora_device_status(ws) == flag and torch.equal(norms, norms2)
+    res, _ = OC.clip(tensors, G, g, max_norm, out=np.full(n, 7.0))
+    fine = owner != sick
+    _close(f64_of(out)[fine], res[fine], 2.0 ** -22, extra=2.0 ** -149)
+    assert np.array_equal(f64_of(out)[~inside], np.full((~inside).sum(), 7.0))
+    assert np.array_equal(out.cpu().numpy()[~fine], g[~fine])
+    p, m = rng.standard_normal(n).astype(np.float32), (rng.standard_normal(n) * 0.1).astype(np.float32)
+    v = (rng.random(n) * 0.01 + 1e-4).astype(np.float32)
+    steps = rng.integers(0, 50, G)
+    dp, dm, dv, st, pb = dev_f32(p), dev_f32(m), dev_f32(v), torch.from_numpy(steps).to("cuda"), dev_bf16(np.zeros(n, np.uint16))
+    L.adam_step_clipped(shape, table, st, dp, dg, dm, dv, max_norm, LR, B1, B2, EPS, 0.1, p_bf16=pb, norms=norms2, ws=ws)
+    assert L.lora_device_status(ws) == flag and torch.equal(norms, norms2)
+    want_p, want_m, want_v, want_steps, _ = OC.adam_clipped(tensors, G, steps, p, g, m, v, max_norm, LR, B1, B2, EPS, 0.1)
+    assert np.array_equal(st.cpu().numpy(), want_steps)
+    cg = np.where(fine, OC.clip(tensors, G, g, max_norm)[0], 0.0)
+    gp, gm, gv = (f64_of(a) for a in (dp, dm, dv))
+    slack = 2.0 ** -21 * (np.abs(B1 * m.astype(np.float64)) + np.abs((1 - B1) * cg))
+    _close(gm, want_m, 0, extra=slack)
+    _close(gv, want_v, 2.0 ** -21)
+    t = np.where(inside, want_steps[owner], 1)
+    t = np.where(fine, t, 1)
+    per_m = LR / (1 - B1 ** t) / (np.sqrt(want_v / (1 - B2 ** t)) + EPS)
+    _close(gp, want_p, 0, extra=2.0 ** -22 * np.abs(p) + per_m * (slack + 2.0 ** -20 * np.abs(want_m)))
+    still = ~inside | ~fine
+    for got, old in ((gp, p), (gm, m), (gv, v)):
+        assert np.array_equal(got[still], old[still])
+    assert np.array_equal(bits_of(pb)[~still], B.to_bf16_bits_f32(dp.cpu().numpy())[~still]) and not bits_of(pb)[still].any()
