@@ -391,3 +391,65 @@ def test_offsets_near_the_largest_integer(which, offset):
     L.lora_forward_w4(shape, x, _dev(codes), _dev(scales), p, p, L.make_desc(a_off, b_off, ranks, s), ids, y, ws)
     assert L.lora_device_status(ws) == L.FLAG_BAD_DESC
     assert np.array_equal(bits_of(y)[[0, 2]], bits_of(good)[[0, 2]]) and np.array_equal(bits_of(y)[1], bits_of(base)[1])
+
+
+# every size class of x in registers with several row tiles a block: one pair of columns a wave (two token
+# tiles and one), two, five and six
+@pytest.mark.parametrize("n,d_in,d_out", [(256, 4096, 4224), (33, 4032, 8256), (5, 4352, 8256), (20, 8192, 4224), (33, 8256, 4224),
+                                          (40, 10240, 4160), (256, 9216, 1088), (1, 12288, 8256), (64, 12288, 4096)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_several_tiles_a_block(n, d_in, d_out, x8):
+    """Rings that stay full from tile to tile, the join's buffers in turn, deltas of several
+    tokens a wave, tokens without an adapter between them; sampled rows of every block's tiles."""
+    rng = np.random.default_rng(n + d_in + d_out)
+    codes, scales = _weights(rng, d_out, d_in)
+    scales = np.minimum(scales, 122).astype(np.uint8)
+    x, xs, xv = _x(rng, n, d_in, x8)
+    ranks = [16, 64, 8, 40]
+    pack, a_off, b_off, A, Bm, s = _adapters(rng, ranks, d_in, d_out)
+    ids = rng.integers(-1, 4, n).astype(np.int32)
+    ids[0] = 1
+    rows = np.unique(np.concatenate((rng.integers(0, d_out, 150), [0, d_out - 1], np.arange(7, d_out, 1031))))
+    W = OQ.values(codes[rows], scales[rows])
+    dc, ds, at = _dev(codes), _dev(scales), _dev(rows)
+    want, mag = xv @ W.T, np.abs(xv) @ np.abs(W).T
+    y = torch.full((n, d_out), float("nan"), dtype=torch.bfloat16, device="cuda")
+    L.w4_linear(x, dc, ds, y, x_scales=xs)
+    _check(y[:, at], want, mag, d_in)
+    assert bool(torch.isfinite(y).all())
+    shape = L.make_shape(n, d_in, d_out, len(pack), len(pack), 4, 64, L.IDS_INTERLEAVED)
+    ws, desc, p = L.empty_workspace(L.lora_forward_w4_workspace_bytes(shape)), L.make_desc(a_off, b_off, ranks, s), dev_bf16(pack)
+    z = torch.full((n, d_out), float("nan"), dtype=torch.bfloat16, device="cuda")
+    L.lora_forward_w4(shape, x, dc, ds, p, p, desc, _dev(ids), z, ws, x_scales=xs)
+    Br = [b[rows] for b in Bm]
+    want = want + np.stack([float(s[a]) * (Br[a] @ (A[a] @ xv[t])) if a >= 0 else np.zeros(len(rows)) for t, a in enumerate(ids)])
+    _check(z[:, at], want, _magnitude(xv, W, A, Br, s, ids), d_in)
+    assert bool(torch.isfinite(z).all()) and np.array_equal(bits_of(z)[ids < 0], bits_of(y)[ids < 0])
+    assert L.lora_device_status(ws) == (L.FLAG_ID_RANGE if (ids < 0).any() else 0)
+
+
+@pytest.mark.parametrize("d_in,d_out", [(9216, 4224), (12288, 4160)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_batch_invariance_over_several_tiles(d_in, d_out, x8):
+    test_batch_invariance(d_in, d_out, x8)
+
+
+def test_quantize_non_finite_weights():
+    """NaN becomes 0, +-Inf the largest code of the finite weights' scale; blocks without a finite weight too."""
+    rng = np.random.default_rng(13)
+    W = B.round_bf16(rng.standard_normal((64, 128)))
+    clean = W.copy()
+    W[0, [3, 40, 41]], clean[0, [3, 40, 41]] = [np.nan, np.inf, -np.inf], 0
+    W[1, 32:64], clean[1, 32:64] = np.nan, 0
+    W[2, 0:32], clean[2, 0:32] = np.inf, 0
+    W[3, 64:96], clean[3, 64:96] = -np.inf, 0
+    with np.errstate(invalid="ignore"):
+        bits = B.to_bf16_bits(W)
+    codes, scales = torch.empty(64, 64, dtype=torch.uint8, device="cuda"), torch.empty(64, 4, dtype=torch.uint8, device="cuda")
+    L.w4_quantize(dev_bf16(bits), codes, scales)
+    want_c, want_s = OQ.quantize(clean)
+    assert np.array_equal(scales.cpu().numpy(), want_s)
+    want = OQ.values(want_c, want_s)
+    top = 6 * np.repeat(np.exp2(want_s.astype(float) - 127), 32, axis=1)
+    want = np.where(np.isinf(W), np.sign(W) * top, want)
+    assert np.array_equal(OQ.values(codes.cpu().numpy(), want_s), want)
