@@ -527,8 +527,8 @@ lora_status rmsnorm_backward(int64_t n, int64_t hidden, const uint16_t* dy, cons
  * w4_quantize lays a bf16 W [d_out][d_in] out so, once per frozen matrix: per
  * 32 weights the least power of two (2^-126 or more) with max |w| <= 6 scale,
  * codes to nearest, ties to the even code.  W must be finite (NaN becomes 0 and
- * +-Inf +-6 scale).  d_in, d_out multiples of 64, <= 2^20; W, codes 16-byte
- * aligned. */
+ * +-Inf +-6 scale) and below 3.5 2^126, which would round to 2^128.  d_in, d_out
+ * multiples of 64, <= 2^20; W, codes 16-byte aligned. */
 lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t* codes,
                         uint8_t* scales, void* stream);
 
@@ -540,6 +540,10 @@ lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t*
  *   x  bf16 [n][d_in] with x_scales NULL; or e4m3 codes uint8 [n][d_in] with
  *      x_scales uint8 [n][d_in/32] (E8M0), as rmsnorm_forward_q8 writes them
  *   y  bf16 [n][d_out] out
+ * Weights and 8-bit x enter the sum as bf16, subnormals included: exactly, but that x
+ * under scale byte 3 is rounded to a multiple of 2^-133 (half a step at most), and a
+ * magnitude of 2^128 or more counts as infinite (weights of scale bytes 253 and 254,
+ * x from byte 247 on, where code and scale reach it): its y is not finite.
  * A token's y (here and in lora_forward_w4) has the same bits in every batch.
  * d_in, d_out multiples of 64, <= 2^20; x, codes, scales, y 16-byte aligned. */
 lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,

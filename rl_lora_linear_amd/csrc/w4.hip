@@ -6,12 +6,13 @@
 // One persistent block per CU keeps its tokens' x in registers as MFMA fragments and
 // streams 16-row tiles of codes past it; the block's waves split k and are joined
 // through LDS in wave order.  A lane turns 16 bytes of codes -- one scale's 32 weights
-// -- into bf16 pairs with the conversion unit (exact: a 2-bit significand times a power
-// of two) and feeds v_mfma_f32_16x16x32_bf16 four times.  k may be met in any order as
+// -- into bf16 pairs with the conversion unit (exact for scale bytes up to 252: a 2-bit
+// significand times a power of two, where that is below bf16's normal numbers a subnormal,
+// which the matrix unit keeps) and feeds v_mfma_f32_16x16x32_bf16 four times.  k may be met in any order as
 // long as weights and x agree, so lane group g of the MFMA simply takes scale block
 // 4 c + g and both operands are read as whole 16-byte pieces in memory order, without
-// shuffles.  8-bit x is widened to bf16 in registers (exact as well).  Sums are fp32
-// throughout, y is rounded once.  The scaled 4-bit MFMA would take the codes as they
+// shuffles.  8-bit x is widened to bf16 in registers (exact for scale bytes 3 to 246; below,
+// multiples of 2^-133).  Sums are fp32 throughout, y is rounded once.  The scaled 4-bit MFMA would take the codes as they
 // are, but it aligns the 128 products of a step to the largest of them and drops what
 // lies ~2^-14 below.
 // Bound by the codes' bytes where there are many (one token's 151936 x 4096, 331 MB:
@@ -33,7 +34,8 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
                                          __builtin_bit_cast(bf16x2, b), c, false);
 }
 // Codes 2i, 2i + 1 of four bytes as a bf16 pair, times 2^(byte - 127); `scale` has the
-// scale byte as its exponent field (the unit takes that field alone: 0 is 2^-127, 255 NaN).
+// scale byte as its exponent field (the unit takes that field alone: 0 is 2^-127, 255 NaN);
+// a value of 2^128 or more becomes infinite.
 template <int I>
 __device__ __forceinline__ uint32_t w4_pair(uint32_t codes, float scale) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));

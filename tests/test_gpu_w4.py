@@ -453,3 +453,56 @@ def test_quantize_non_finite_weights():
     top = 6 * np.repeat(np.exp2(want_s.astype(float) - 127), 32, axis=1)
     want = np.where(np.isinf(W), np.sign(W) * top, want)
     assert np.array_equal(OQ.values(codes.cpu().numpy(), want_s), want)
+
+
+def test_every_scale_byte():
+    """Weights of scale bytes 0 to 252 are exact bf16, below the normal numbers too; 8-bit x from byte 3 to 246.  Under
+    byte 3 x is rounded to a multiple of 2^-133; 255 is NaN.  One row of weights a byte, one code a column; the
+    other operand brings the product back to the middle of fp32's range."""
+    mag = np.array([0.5, 1, 1.5, 2, 3, 4, 6])
+    codes = np.zeros((256, 32), np.uint8)       # 64 columns: 7 codes and zeros
+    for c in range(1, 8):
+        codes[:, c // 2] |= c << 4 * (c % 2)
+    for bytes_, k in ((range(0, 120), 100), (range(120, 253), -90)):
+        scales = np.full((256, 2), 127, np.uint8)
+        scales[list(bytes_), 0] = list(bytes_)
+        x = np.zeros((7, 64))
+        x[np.arange(7), np.arange(1, 8)] = 2.0 ** k
+        y = torch.empty(7, 256, dtype=torch.bfloat16, device="cuda")
+        L.w4_linear(dev_bf16(B.to_bf16_bits(x)), _dev(codes), _dev(scales), y)
+        got = f64_of(y)
+        for b in bytes_:
+            assert np.array_equal(got[:, b], mag * 2.0 ** (b - 127 + k)), b
+    every = np.concatenate((np.arange(0, 127), np.arange(128, 255))).astype(np.uint8)    # e4m3 without its NaNs
+    val = torch.from_numpy(every).view(torch.float8_e4m3fn).double().numpy()
+    eye = np.zeros((256, 128), np.uint8)        # row i takes column i: 256 columns, code 1.0
+    eye[np.arange(256), np.arange(256) // 2] = np.where(np.arange(256) % 2, 0x20, 0x02)
+    q = np.full((1, 256), 0x00, np.uint8)
+    q[0, :254] = every
+    for b in (0, 1, 2, 3, 4, 9, 10, 60, 126, 127, 190, 240, 245, 246):
+        k = 100 if b < 120 else -100
+        y = torch.empty(1, 256, dtype=torch.bfloat16, device="cuda")
+        L.w4_linear(_dev(q), _dev(eye), _dev(np.full((256, 8), 127 + k, np.uint8)), y, x_scales=_dev(np.full((1, 8), b, np.uint8)))
+        want, got = val * 2.0 ** (b - 127), f64_of(y)[0, :254] / 2.0 ** k
+        if b >= 3:
+            assert np.array_equal(got, want), b
+        else:
+            assert np.all(np.abs(got - want) <= 2.0 ** -134), b
+    L.w4_linear(_dev(q), _dev(eye), _dev(np.full((256, 8), 127, np.uint8)), y, x_scales=_dev(np.full((1, 8), 255, np.uint8)))
+    assert bool(torch.isnan(y).all())
+
+
+def test_values_beyond_bf16():
+    """A code times its scale of 2^128 or more is infinite: y of that row (or token) is not finite, the others' are."""
+    for d_in in (64, 256, 12352):
+        codes, scales = np.full((64, d_in // 2), 0x22, np.uint8), np.full((64, d_in // 32), 127, np.uint8)
+        codes[[3, 5], 0], scales[[3, 5], 0], codes[9, 0], scales[9, 0] = 0x26, (253, 254), 0x25, 253       # 4.0; 3.0
+        x = torch.ones(2, d_in, dtype=torch.bfloat16, device="cuda") * 2.0 ** -20
+        y = torch.empty(2, 64, dtype=torch.bfloat16, device="cuda")
+        L.w4_linear(x, _dev(codes), _dev(scales), y)
+        finite = np.isfinite(f64_of(y))
+        assert not finite[:, [3, 5]].any() and np.delete(finite, [3, 5], axis=1).all()
+        q, qs = np.full((2, d_in), 0x38, np.uint8), np.full((2, d_in // 32), 127, np.uint8)
+        q[1, 0], qs[1, 0] = 0x7E, 247                                                                      # 448 2^120
+        L.w4_linear(_dev(q), _dev(np.full((64, d_in // 2), 0x22, np.uint8)), _dev(np.full((64, d_in // 32), 107, np.uint8)), y, x_scales=_dev(qs))
+        assert not np.isfinite(f64_of(y)[1]).any() and np.isfinite(f64_of(y)[0]).all()
