@@ -84,7 +84,8 @@ typedef enum {
 #define LORA_FLAG_ID_RANGE     0x1  /* an adapter/segment id outside [0, n_keys) */
 #define LORA_FLAG_UNSORTED     0x2  /* ids decrease although LORA_IDS_SORTED was promised */
 #define LORA_FLAG_TARGET_RANGE 0x4  /* a target token id outside [0, vocab) */
-#define LORA_FLAG_BAD_DESC     0x8  /* an adapter descriptor with bad rank, offset or alignment */
+#define LORA_FLAG_BAD_DESC     0x8  /* an adapter descriptor with bad rank, offset or alignment; a gradient
+                                       table's entry or a step counter that breaks its rules */
 #define LORA_FLAG_NONFINITE_GRAD 0x10 /* AdamW skipped an adapter whose gradient held NaN or Inf */
 #define LORA_FLAG_NONFINITE_LOSS 0x20 /* loss_grad removed kept rows whose inputs held NaN or Inf */
 
@@ -616,9 +617,11 @@ lora_status grad_clip(const grad_shape* shape, const grad_tensor* table, const f
 /* grad_clip and one AdamW step per group in one call, without writing the
  * clipped gradient: each element as in adam_step on min(1, max_norm / (norm +
  * 1e-6)) g, the constants taken from the 64-bit lr, betas, eps and decay.
- * steps: DEVICE int64 [n_groups], the steps each group has made; the call makes
- * step steps[a] + 1 and stores it, so a captured graph counts on with every replay.  A group with a non-finite gradient keeps p, m, v, its bf16 copy
- * and its counter, and LORA_FLAG_NONFINITE_GRAD is set.  p, m, v updated in
+ * steps: DEVICE int64 [n_groups], the steps each group has made (0 or more); the call
+ * makes step steps[a] + 1 and stores it, so a captured graph counts on with every
+ * replay.  A group with a non-finite gradient keeps p, m, v, its bf16 copy and its
+ * counter, and LORA_FLAG_NONFINITE_GRAD is set; so does a group whose counter is
+ * negative or 2^63 - 1, and LORA_FLAG_BAD_DESC is set.  p, m, v updated in
  * place, g read only, p_bf16 (nullable) receives bf16(p); norms (nullable) as
  * for grad_clip. */
 lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table, int64_t* steps,

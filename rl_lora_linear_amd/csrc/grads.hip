@@ -10,9 +10,9 @@
 // again, in block order -- at most 4096 of them, read from L2 while its own first
 // elements are on their way -- instead of a launch between the two that would
 // only add its latency, and then scales or steps its chunks.  A group is skipped
-// exactly when its sum is not finite, that is when any of its elements is NaN or
-// +-Inf, so the norm's pass over g is also the scan that decides the skip.  Both
-// passes are bound by HBM.
+// when its sum is not finite, that is when any of its elements is NaN or +-Inf, so the
+// norm's pass over g is also the scan that decides the skip (AdamW skips a group with a
+// counter that counts no steps as well).  Both passes are bound by HBM.
 #include "common.hpp"
 #include "sgmv.hpp"
 
@@ -27,11 +27,11 @@ static_assert(GRAD_CHUNK % (GRAD_THREADS * 4) == 0, "whole 16-byte rounds per ch
 // c_a (gradients near the fp32 range) keeps its bits in coef, and ldexp rounds only
 // where the result is subnormal.
 struct GradFactors {
-  float coef;          // 1 for a skipped group
+  float coef;          // 1 for a group whose gradient is not finite
   int32_t exp2;
   float step_size;     // lr / (1 - beta1^step)
   float inv_sqrt_bc2;  // 1 / sqrt(1 - beta2^step)
-  int32_t skip;
+  int32_t skip;        // a gradient that is not finite, or a counter that counts no steps
 };
 
 __device__ __forceinline__ float clipped(float g, const GradFactors& f) {
@@ -135,6 +135,10 @@ __device__ __forceinline__ double grad_squares(const GradPieces& r, const float*
   return s;
 }
 
+// Whether a counter of steps made has a next one, at least 1: others would divide by
+// 1 - beta^0 or count past 64 bits.
+__device__ __forceinline__ bool grad_counts(int64_t made) { return made >= 0 && made < INT64_MAX; }
+
 // First launch.  Block b takes chunks b per .. (b + 1) per - 1, the next chunk's
 // elements in flight while one is summed.
 __global__ __launch_bounds__(GRAD_THREADS) void grad_partial_kernel(
@@ -153,7 +157,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_partial_kernel(
       for (int a = max(here + 1, 0); a <= sh.n_groups; ++a) ws.start[a] = sh.n_chunks;
   }
   if (steps)
-    for (int a = id; a < sh.n_groups; a += threads) ws.steps[a] = steps[a];
+    for (int a = id; a < sh.n_groups; a += threads) {
+      ws.steps[a] = steps[a];
+      if (!grad_counts(steps[a])) set_flag(ws.status, LORA_FLAG_BAD_DESC);
+    }
 
   const int c0 = blockIdx.x * ws.per, c1 = min(sh.n_chunks, c0 + ws.per);
   if (c0 >= c1) return;
@@ -217,7 +224,8 @@ __device__ __forceinline__ GradFactors grad_factors(const grad_shape& sh, const 
   f.coef = (float)c;
   if (c < 0x1p-126) f.coef = (float)frexp(c, &f.exp2);
   if (ad.steps) {
-    const int64_t step = ws.steps[a] + 1;
+    f.skip = !grad_counts(ws.steps[a]);
+    const int64_t step = f.skip ? 1 : ws.steps[a] + 1;
     f.step_size = (float)(ad.lr / (1.0 - power(ad.beta1, step)));
     f.inv_sqrt_bc2 = (float)(1.0 / sqrt(1.0 - power(ad.beta2, step)));
   }
@@ -230,8 +238,8 @@ __device__ __forceinline__ void grad_report(const GradWs& ws, int a, double norm
                                             float* norms) {
   if (threadIdx.x != 0) return;
   if (norms) norms[a] = (float)norm;
-  if (f.skip) set_flag(ws.status, LORA_FLAG_NONFINITE_GRAD);
-  else if (ad.steps) ad.steps[a] = ws.steps[a] + 1;
+  if (!__builtin_isfinite(norm)) set_flag(ws.status, LORA_FLAG_NONFINITE_GRAD);
+  if (ad.steps && !f.skip) ad.steps[a] = ws.steps[a] + 1;
 }
 
 // grad_norm's second launch: one block a group.
@@ -387,7 +395,7 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_apply_kernel(grad_shape sh,
        a += gridDim.x * GRAD_THREADS)
     if (ws.start[a] >= ws.start[a + 1]) {
       if (norms) norms[a] = 0.f;
-      if (ad.steps) ad.steps[a] = ws.steps[a] + 1;
+      if (ad.steps && grad_counts(ws.steps[a])) ad.steps[a] = ws.steps[a] + 1;
     }
 }
 

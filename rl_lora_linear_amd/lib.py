@@ -634,7 +634,7 @@ def grad_clip(shape, table, g, max_norm, out, norms, ws, stream=None):
 def adam_step_clipped(shape, table, steps, p, g, m, v, max_norm, lr, beta1=0.9, beta2=0.999,
                       eps=1e-8, weight_decay=0.0, p_bf16=None, norms=None, ws=None, stream=None):
     """One AdamW step per group on its clipped gradient; steps: device int64 [n_groups], the
-    steps made so far, counted up by the call.  ws: workspace of grad_workspace_bytes(shape)
+    steps made so far (>= 0), counted up by the call.  ws: workspace of grad_workspace_bytes(shape)
     (a fresh zeroed one if None)."""
     pt, pp, pg, pm, pv, pn = _grad_args(shape, table, (("p", p), ("g", g), ("m", m), ("v", v)), norms)
     dev = p.get_device()

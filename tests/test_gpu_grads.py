@@ -362,3 +362,24 @@ def test_more_chunks_than_blocks(bad):
     for got, old in ((gp, p), (gm, m), (gv, v)):
         assert np.array_equal(got[still], old[still])
     assert np.array_equal(bits_of(pb)[~still], B.to_bf16_bits_f32(dp.cpu().numpy())[~still]) and not bits_of(pb)[still].any()
+
+
+def test_counters_that_count_no_steps():
+    """A negative step counter (or one that cannot be counted up) has no step 1 or later: the group keeps its values
+    and its counter and is flagged, as adam_step refuses steps below 1; the others step."""
+    n, top = 5000, (1 << 63) - 1
+    tensors = [(0, 1000, 0), (1000, 9, 1), (1009, 1500, 2), (2509, 500, 3)]      # group 4 has no tensor
+    shape, table = L.make_grad_table(tensors, 6, n)
+    ws = L.empty_workspace(L.grad_workspace_bytes(shape))
+    rng = np.random.default_rng(3)
+    p, g = rng.standard_normal(n).astype(np.float32), rng.standard_normal(n).astype(np.float32)
+    steps = np.array([-1, 0, -7, top, -2, 4])
+    dp, dm, dv, st, norms = dev_f32(p), dev_f32(np.zeros(n)), dev_f32(np.zeros(n)), torch.from_numpy(steps).to("cuda"), torch.empty(6, device="cuda")
+    L.adam_step_clipped(shape, table, st, dp, dev_f32(g), dm, dv, 1.0, LR, norms=norms, ws=ws)
+    assert L.lora_device_status(ws) == L.FLAG_BAD_DESC
+    assert list(st.cpu().numpy()) == [-1, 1, -7, top, -2, 5]
+    moved = np.zeros(n, bool)
+    moved[1000:1009] = True
+    assert np.array_equal(dp.cpu().numpy()[~moved], p[~moved]) and not dm.cpu().numpy()[~moved].any() and not dv.cpu().numpy()[~moved].any()
+    assert np.all(dp.cpu().numpy()[moved] != p[moved]) and np.all(np.isfinite(dp.cpu().numpy()))
+    _close(f64_of(norms), OC.norms(tensors, 6, g), 2.0 ** -23)
