@@ -587,7 +587,7 @@ def make_grad_table(tensors, n_groups, n_elems, device="cuda"):
     """tensors: (offset, count, group) triples of one flat buffer of n_elems, in any order.
     Returns the GradShape and the device table (sorted by group) of the calls below."""
     t = np.array([tuple(map(int, e)) for e in tensors], np.int64).reshape(-1, 3)
-    _arg(np.all(t[:, :2] >= 0) and np.all(t[:, 0] + t[:, 1] <= n_elems),
+    _arg(np.all(t[:, :2] >= 0) and np.all(t[:, 0] <= n_elems - t[:, 1]),   # (a sum could wrap)
          f"a tensor lies outside a buffer of {n_elems}")
     _arg(np.all((t[:, 2] >= 0) & (t[:, 2] < n_groups)), f"a group outside [0, {n_groups})")
     by_place = t[np.argsort(t[:, 0], kind="stable")]

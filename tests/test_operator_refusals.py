@@ -235,3 +235,12 @@ def test_tables_that_are_not_aligned(L, byte):
     _is(L, lib.grad_norm(ctypes.byref(good), at, P, P, P, BIG, None), E, b"table must be 8-byte aligned")
     _is(L, lib.grad_clip(ctypes.byref(good), at, P, 1.0, P, P, P, BIG, None), E, b"table must be 8-byte aligned")
     _is(L, lib.adam_step_clipped(ctypes.byref(good), at, P, P, P, P, P, 1.0, 1e-3, 0.9, 0.99, 1e-8, 0.0, None, P, P, BIG, None), E, b"table must be 8-byte")
+
+
+@pytest.mark.parametrize("bad", [(1 << 63) - 8, (1 << 62) + (1 << 61)])
+def test_table_builder_offsets_near_the_largest_integer(L, bad):
+    for entry in ((bad, 100, 0), (100, bad, 0), (bad, bad, 0)):
+        with pytest.raises(L.LoraError, match="outside a buffer"):
+            L.make_grad_table([entry], 1, 1000, device="cpu")
+    with pytest.raises(L.LoraError, match="outside a buffer"):
+        L.make_grad_table([(0, 10, 0), (bad, 8, 0)], 1, (1 << 42), device="cpu")
