@@ -529,7 +529,8 @@ lora_status rmsnorm_backward(int64_t n, int64_t hidden, const uint16_t* dy, cons
  * 32 weights the least power of two (2^-126 or more) with max |w| <= 6 scale,
  * codes to nearest, ties to the even code.  W must be finite (NaN becomes 0 and
  * +-Inf +-6 scale) and below 3.5 2^126, which would round to 2^128.  d_in, d_out
- * multiples of 64, <= 2^20; W, codes 16-byte aligned. */
+ * multiples of 64, <= 2^20; W, codes 16-byte aligned; codes and scales must not
+ * overlap W. */
 lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t* codes,
                         uint8_t* scales, void* stream);
 
@@ -546,7 +547,8 @@ lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t*
  * magnitude of 2^128 or more counts as infinite (weights of scale bytes 253 and 254,
  * x from byte 247 on, where code and scale reach it): its y is not finite.
  * A token's y (here and in lora_forward_w4) has the same bits in every batch.
- * d_in, d_out multiples of 64, <= 2^20; x, codes, scales, y 16-byte aligned. */
+ * d_in, d_out multiples of 64, <= 2^20; x, codes, scales, y 16-byte aligned; y must
+ * not overlap x or x_scales (nor in lora_forward_w4). */
 lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
                       const uint8_t* x_scales, const uint8_t* codes, const uint8_t* scales,
                       uint16_t* y, void* stream);

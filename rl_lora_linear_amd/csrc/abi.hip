@@ -1212,11 +1212,21 @@ static lora_status w4_tokens(int64_t n, const char* what) {
   return LORA_OK;
 }
 
+// y of some rows is written while other blocks have yet to read x.
+static bool w4_y_on_x(int64_t n, int64_t d_in, int64_t d_out, const void* x, const void* x_scales,
+                      const void* y) {
+  return overlap(y, n * d_out * 2, x, n * d_in * (x_scales ? 1 : 2)) ||
+         overlap(y, n * d_out * 2, x_scales, n * (d_in / 32));
+}
+
 lora_status w4_quantize(const uint16_t* W, int64_t d_out, int64_t d_in, uint8_t* codes,
                         uint8_t* scales, void* stream) {
   TRY(w4_dims(d_in, d_out, "w4_quantize"));
   LORA_ARG_CHECK(W && codes && scales, "w4_quantize: W, codes and scales must be non-NULL");
   LORA_ARG_CHECK(aligned16(W) && aligned16(codes), "w4_quantize: W and codes must be 16-byte aligned");
+  LORA_ARG_CHECK(!overlap(codes, d_out * d_in / 2, W, d_out * d_in * 2) &&
+                     !overlap(scales, d_out * d_in / 32, W, d_out * d_in * 2),
+                 "w4_quantize: codes or scales overlap W");
   return launch_w4_quantize(W, d_out, d_in, codes, scales, S(stream));
 }
 
@@ -1229,6 +1239,7 @@ lora_status w4_linear(int64_t n, int64_t d_in, int64_t d_out, const void* x,
                  "w4_linear: codes or scales NULL or not 16-byte aligned");
   LORA_ARG_CHECK(n == 0 || (x && y && aligned16(x) && aligned16(y)),
                  "w4_linear: x or y NULL or not 16-byte aligned");
+  LORA_ARG_CHECK(!w4_y_on_x(n, d_in, d_out, x, x_scales, y), "w4_linear: y overlaps x or x_scales");
   if (n == 0) return LORA_OK;
   return launch_w4_linear(n, d_in, d_out, x, x_scales, codes, scales, y, S(stream));
 }
@@ -1260,6 +1271,8 @@ lora_status lora_forward_w4(const lora_shape* shape, const void* x, const uint8_
     return LORA_E_WORKSPACE;
   }
   LORA_ARG_CHECK(aligned16(ws), "lora_forward_w4: the workspace must be 16-byte aligned");
+  LORA_ARG_CHECK(!w4_y_on_x(sh.n_tokens, sh.d_in, sh.d_out, x, x_scales, y),
+                 "lora_forward_w4: y overlaps x or x_scales");
   if (sh.n_tokens == 0) return LORA_OK;
   return launch_lora_w4(sh, x, x_scales, codes, scales, A_pack, B_pack, desc, adapter_ids, y, ws,
                         S(stream));

@@ -244,3 +244,21 @@ def test_table_builder_offsets_near_the_largest_integer(L, bad):
             L.make_grad_table([entry], 1, 1000, device="cpu")
     with pytest.raises(L.LoraError, match="outside a buffer"):
         L.make_grad_table([(0, 10, 0), (bad, 8, 0)], 1, (1 << 42), device="cpu")
+
+
+def test_four_bit_outputs_in_the_place_of_inputs(L):
+    """Blocks read all of x, or of W, while others write: no output may lie there."""
+    lib, E, n, d = L.LIB, L.LORA_E_INVALID_ARG, 2, 128
+    at = lambda byte: ctypes.c_void_p((1 << 20) + byte)  # noqa: E731
+    sh = L.make_shape(n, d, d, 4096, 4096, 4, 16, L.IDS_INTERLEAVED)
+    layer = lambda x, xs, y: lib.lora_forward_w4(ctypes.byref(sh), x, xs, P, P, P, P, P, P, y, P, BIG, None)  # noqa: E731
+    linear = lambda x, xs, y: lib.w4_linear(n, d, d, x, xs, P, P, y, None)  # noqa: E731
+    far = at(1 << 16)
+    for call in (layer, linear):
+        for byte in (0, 16, n * d * 2 - 16):
+            _is(L, call(at(0), None, at(byte)), E, b"overlaps x")
+            _is(L, call(at(byte), None, at(0)), E, b"overlaps x")
+        _is(L, call(at(0), far, at(n * d - 16)), E, b"overlaps x")
+        _is(L, call(far, at(0), at(0)), E, b"overlaps x")
+    for codes, scales in ((at(0), far), (at(d * d * 2 - 16), far), (far, at(d * d * 2 - 1))):
+        _is(L, lib.w4_quantize(at(0), d, d, codes, scales, None), E, b"overlap W")
