@@ -8,7 +8,8 @@
 //   dx = bf16(dh + rstd (g - xh mean_j(g xh))),   dw_j = sum_t dy_tj xh_tj.
 //
 // Everything is bound by HBM: a row is read once, kept in registers across its
-// reduction and written once.  In a captured graph, launches included, 8192 x 4096
+// reduction and written once (but for the backward of rows past 16384 columns, which
+// does not fit them: see there).  In a captured graph, launches included, 8192 x 4096
 // with the residual takes 46.4 us (5.8 TB/s), its backward 44.6 us (6.0 TB/s) and 51.6
 // with the weight's gradient; 4097 x 2048 in 8 bits 11.7 us (5.0 TB/s).  A team of lanes owns a row and lane l of it
 // holds the 8-column vectors l, l + team, ...: rows of up to 512 columns take
@@ -192,7 +193,8 @@ __global__ __launch_bounds__(VPL == 1 ? NORM_SMALL_BLOCK : 1024) void rmsnorm_fw
 // rows its team visits; the block's teams are joined through LDS in team order
 // and the block writes one row of partial [gridDim.x][H].  A row of more than
 // 16384 columns does not fit the registers beside dw: it is read again, from the
-// caches, once its sum is known.
+// caches, once its sum is known, and 42 registers a lane still spill to scratch, with a
+// frozen weight too (2048 x 20480: 203 us without dw, 185 with it, 1.7 to 1.8 TB/s).
 template <int VPL, bool VEC, bool NT>
 __global__ __launch_bounds__(VPL == 1 ? NORM_SMALL_BLOCK : 1024) void rmsnorm_bwd_kernel(
     int64_t n, int H, int team, const uint16_t* dy, const uint16_t* dh,
@@ -383,11 +385,13 @@ static unsigned norm_free_grid(int64_t n, const NormPlan& p) {
   return norm_grid(n, p, std::max<int64_t>(1, (1 << 20) / p.block));
 }
 
-// Blocks that keep dw partials: 2^17 threads in all (8 waves a CU), so that the partials,
-// written and read again, are 8 MB at most columns (at 8192 x 4096 51.6 us; with twice the
-// blocks 56.5, with half of them 69.7), and as many on every CU: rounded up to whole
-// multiples of 256, or down where that would leave blocks without a row (2790 x 7168: 512
-// blocks 35.6 us, 256 43.0, 292 40.3; 500 x 7168: 256 blocks 13.6, 500 15.3).
+// Blocks that keep dw partials: 2^17 threads in all (8 waves a CU), which the whole
+// multiples of the CUs below raise to as many as 2^18.  The partials, written and read
+// again, are 8 MB at 1024, 2048, 4096 and 8192 columns, 14 MB at 7168, 16 at 16384 and 32
+// at 32768 (at 8192 x 4096 51.6 us; with twice the blocks 56.5, with half of them 69.7).  As
+// many on every CU: rounded up to whole multiples of 256, or down where that would leave
+// blocks without a row (2790 x 7168: 512 blocks 35.6 us, 256 43.0, 292 40.3; 500 x 7168:
+// 256 blocks 13.6, 500 15.3).
 int64_t rmsnorm_bwd_blocks(int64_t n, int64_t hidden) {
   const NormPlan p = norm_plan(hidden);
   const int64_t most = (1 << 17) / p.block, up = align_up(most, 256);

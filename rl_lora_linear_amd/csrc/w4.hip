@@ -594,7 +594,8 @@ __global__ __launch_bounds__(64 * NW) void w4_product_kernel(W4Args a) {
 // ------------------------------------------------------------------ quantiser
 // 32 weights per four lanes: the least power of two with max|w| <= 6 scale (no
 // finite weight saturates), then the nearest e2m1 magnitude, ties to the even
-// code.  NaN and +-Inf do not take part in the scale; NaN becomes 0.
+// code.  NaN and +-Inf do not take part in the scale; NaN becomes 0.  Run once per
+// frozen matrix: 151936 x 4096 392 us (4.0 TB/s read and written), 12288 x 4096 34.5.
 __global__ __launch_bounds__(256) void w4_quantize_kernel(int64_t n8, const uint16_t* __restrict__ W,
                                                           uint8_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
