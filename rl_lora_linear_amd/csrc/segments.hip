@@ -13,6 +13,7 @@
 //                prefix[key][chunk] + (earlier tokens of the chunk with that
 //                key), so the order inside a key is the token order.
 #include "common.hpp"
+#include "desc.hpp"
 #include "segments.hpp"
 
 namespace lora {

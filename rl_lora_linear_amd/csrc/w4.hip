@@ -22,6 +22,7 @@
 // tokens 12288 -> 4096 17.1 us).  The adapters' shrink is a launch of its own, 3 us
 // with one token; times in a captured graph.
 #include "common.hpp"
+#include "desc.hpp"
 #include "sgmv.hpp"
 
 namespace lora {

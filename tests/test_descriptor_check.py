@@ -10,7 +10,7 @@ import pytest
 I64_MAX = (1 << 63) - 1
 
 SOURCE = r'''
-#include "common.hpp"
+#include "desc.hpp"
 extern "C" bool check(int64_t a_off, int64_t b_off, int32_t rank, int32_t max_rank, int64_t d_in,
                       int64_t d_out, int64_t a_elems, int64_t b_elems) {
   return lora::desc_ok(lora_adapter_desc{a_off, b_off, rank, 1.f}, max_rank, d_in, d_out, a_elems, b_elems);
