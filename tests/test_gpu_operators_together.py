@@ -270,3 +270,31 @@ def test_grad_clip_graph():
 
     _replay_check(run, got, lambda: scratch.normal_())
     assert L.lora_device_status(ws) == 0
+
+
+def test_neighbouring_parts_of_one_buffer():
+    """Operands that lie one behind the other in one allocation share no byte and are taken."""
+    n, H = 4, 64
+    rng = np.random.default_rng(14)
+    part = torch.empty(5, n, H, dtype=torch.bfloat16, device="cuda")
+    part[:] = torch.randn(5, n, H, device="cuda").to(torch.bfloat16)
+    w, rstd = dev_bf16(B.to_bf16_bits(rng.standard_normal(H))), torch.rand(n, device="cuda")
+    apart = [t.clone() for t in part]
+    out = [_bf(n, H) for _ in range(3)]
+    L.rmsnorm_backward(apart[0], apart[2], w, rstd, out[0])
+    L.rmsnorm_backward(part[0], part[2], w, rstd, part[1])     # dx in front of h
+    L.rmsnorm_backward(part[0], part[2], w, rstd, part[3])     # and behind it
+    assert np.array_equal(bits_of(part[1]), bits_of(out[0])) and np.array_equal(bits_of(part[3]), bits_of(out[0]))
+    codes = torch.randint(0, 256, (H, H // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((H, H // 32), 127, dtype=torch.uint8, device="cuda")
+    L.w4_linear(apart[2], codes, scales, out[1])
+    L.w4_linear(part[2], codes, scales, part[1])
+    L.w4_linear(part[2], codes, scales, part[3])
+    assert np.array_equal(bits_of(part[1]), bits_of(out[1])) and np.array_equal(bits_of(part[3]), bits_of(out[1]))
+    raw = torch.empty(3 * n * H + n * H // 32, dtype=torch.uint8, device="cuda")     # q, x, q_scales
+    x = raw[n * H:3 * n * H].view(torch.bfloat16).view(n, H)
+    x.copy_(apart[0])
+    q, s = torch.empty(n, H, dtype=torch.uint8, device="cuda"), torch.empty(n, H // 32, dtype=torch.uint8, device="cuda")
+    L.rmsnorm_forward_q8(apart[0], w, EPS, q, s)
+    L.rmsnorm_forward_q8(x, w, EPS, raw[:n * H].view(n, H), raw[3 * n * H:].view(n, H // 32))
+    assert torch.equal(raw[:n * H].view(n, H), q) and torch.equal(raw[3 * n * H:].view(n, H // 32), s)
