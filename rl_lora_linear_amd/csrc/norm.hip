@@ -11,11 +11,11 @@
 // reduction and written once (but for the backward of rows past 16384 columns, which
 // does not fit them: see there).  In a captured graph, launches included, 8192 x 4096
 // with the residual takes 46.4 us (5.8 TB/s), its backward 44.6 us (6.0 TB/s) and 51.6
-// with the weight's gradient; 4097 x 2048 in 8 bits 11.7 us (5.0 TB/s).  A team of lanes owns a row and lane l of it
-// holds the 8-column vectors l, l + team, ...: rows of up to 512 columns take
-// part of a wave (several rows a wave, shuffles only), longer ones whole waves
-// of one block that join their sums through LDS.  Teams step over the rows
-// with the grid's stride, so a block reads the weight once.  The team of a row
+// with the weight's gradient; 4097 x 2048 in 8 bits 11.7 us (5.0 TB/s).
+// A team of lanes owns a row and lane l of it holds the 8-column vectors l, l + team, ...:
+// rows of up to 512 columns take part of a wave (several rows a wave, shuffles only),
+// longer ones whole waves of one block that join their sums through LDS.  Teams step over
+// the rows with the grid's stride, so a block reads the weight once.  The team of a row
 // depends on `hidden` alone: a row's bits do not change with the batch.
 #include <type_traits>
 

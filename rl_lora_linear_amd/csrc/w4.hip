@@ -7,14 +7,14 @@
 // streams 16-row tiles of codes past it; the block's waves split k and are joined
 // through LDS in wave order.  A lane turns 16 bytes of codes -- one scale's 32 weights
 // -- into bf16 pairs with the conversion unit (exact for scale bytes up to 252: a 2-bit
-// significand times a power of two, where that is below bf16's normal numbers a subnormal,
-// which the matrix unit keeps) and feeds v_mfma_f32_16x16x32_bf16 four times.  k may be met in any order as
-// long as weights and x agree, so lane group g of the MFMA simply takes scale block
-// 4 c + g and both operands are read as whole 16-byte pieces in memory order, without
-// shuffles.  8-bit x is widened to bf16 in registers (exact for scale bytes 3 to 246; below,
-// multiples of 2^-133).  Sums are fp32 throughout, y is rounded once.  The scaled 4-bit MFMA would take the codes as they
-// are, but it aligns the 128 products of a step to the largest of them and drops what
-// lies ~2^-14 below.
+// significand times a power of two, where that is below bf16's normal numbers a
+// subnormal, which the matrix unit keeps) and feeds v_mfma_f32_16x16x32_bf16 four times.
+// k may be met in any order as long as weights and x agree, so lane group g of the MFMA
+// simply takes scale block 4 c + g and both operands are read as whole 16-byte pieces in
+// memory order, without shuffles.  8-bit x is widened to bf16 in registers (exact for
+// scale bytes 3 to 246; below, multiples of 2^-133).  Sums are fp32 throughout, y is
+// rounded once.  The scaled 4-bit MFMA would take the codes as they are, but it aligns
+// the 128 products of a step to the largest of them and drops what lies ~2^-14 below.
 // Bound by the codes' bytes where there are many (one token's 151936 x 4096, 331 MB:
 // 54 to 57 us, 5.8 to 6.1 TB/s of the 7.1 that plain reads reach), by launch, first
 // access and the join where there are few (4096 x 4096 4.2 us, a launch alone 3.9;
