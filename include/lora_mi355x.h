@@ -88,6 +88,9 @@ typedef enum {
                                        table's entry or a step counter that breaks its rules */
 #define LORA_FLAG_NONFINITE_GRAD 0x10 /* AdamW skipped an adapter whose gradient held NaN or Inf */
 #define LORA_FLAG_NONFINITE_LOSS 0x20 /* loss_grad removed kept rows whose inputs held NaN or Inf */
+#define LORA_FLAG_BAD_LENGTH   0x40 /* a sequence's offsets or length that break their rules */
+#define LORA_FLAG_BAD_PAGE     0x80 /* a cache page, slot or page counter out of range */
+#define LORA_FLAG_NO_PAGES     0x100 /* kv_tables left a request out: too few free pages */
 
 typedef enum { LORA_IDS_SORTED = 0, LORA_IDS_INTERLEAVED = 1 } lora_id_order;
 
@@ -631,6 +634,172 @@ lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table,
                               double lr, double beta1, double beta2, double eps,
                               double weight_decay, uint16_t* p_bf16, float* norms, void* ws, size_t ws_bytes,
                               void* stream);
+
+/* ---- attention over packed prompts ------------------------------------ */
+
+/* Attention of the prompts of one batch, packed one behind the other: sequence b has
+ * the query rows cu_q[b] .. cu_q[b+1] - 1 of q and the key rows cu_k[b] .. cu_k[b+1] - 1
+ * of k and v.  Head h reads key head h / (n_heads / n_kv_heads).  With Lq and Lk rows,
+ * query i sees the keys j with
+ *   causal: j <= i + Lk - Lq  (the ends lie on each other; Lq = Lk in training),
+ *   else:   every j;
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),
+ *   o_i = bf16(sum_j exp(s_ij - lse_i) v_j).
+ * A query that sees no key (Lk < Lq, Lk = 0) has o = 0 and lse = -inf.  Products and
+ * sums are fp32; the weights exp(.) enter the second product as bf16.  A sequence's
+ * results have the same bits whatever else the batch holds, and depend on nothing
+ * outside its rows; with causal, o_i and lse_i depend on keys that query i sees only,
+ * also where others hold NaN or Inf. */
+typedef struct {        /* host struct */
+  int64_t n_q;          /* rows of q, o; 0 .. 2^30 - 1 */
+  int64_t n_k;          /* rows of k, v; 0 .. 2^30 - 1 */
+  int64_t q_stride;     /* elements from a row of q (and dq) to the next, >= n_heads * head_dim */
+  int64_t k_stride;     /* of k, dk; >= n_kv_heads * head_dim */
+  int64_t v_stride;     /* of v, dv; likewise */
+  int64_t o_stride;     /* of o, dout; >= n_heads * head_dim.  Strides: multiples of 8, < 2^31 */
+  int32_t n_seqs;       /* 0 .. 65536 */
+  int32_t n_heads;      /* a multiple of n_kv_heads; <= 1024 */
+  int32_t n_kv_heads;   /* >= 1 */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t causal;       /* 0 or 1 */
+  float scale;          /* finite */
+} attn_shape;
+
+/* Workspace of the two calls below; word 0 is the status word.  0 on an invalid shape. */
+size_t attention_workspace_bytes(const attn_shape* shape);
+
+/*   q bf16 [n_q] rows of [n_heads][head_dim]; k, v bf16 [n_k] rows of
+ *   [n_kv_heads][head_dim], each row at its stride: slices of one fused
+ *   projection's output are taken as they are.  All 16-byte aligned.
+ *   cu_q, cu_k int32 [n_seqs+1], not decreasing, within [0, n_q] and [0, n_k]; may be
+ *              one array.  A sequence that breaks this sets LORA_FLAG_BAD_LENGTH and is
+ *              left out.
+ *   o   bf16 [n_q] rows of [n_heads][head_dim] out, must not overlap q, k or v
+ *   lse fp32 [n_heads][n_q] out
+ * Rows of o and lse that belong to no sequence are left as they were. */
+lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const uint16_t* k,
+                              const uint16_t* v, const int32_t* cu_q, const int32_t* cu_k,
+                              uint16_t* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward for dout = dL/do, with o and lse from the forward on the same inputs:
+ *   p_ij = exp(s_ij - lse_i),  ds_ij = p_ij (dout_i . v_j - dout_i . o_i)
+ *   dq_i = scale sum_j ds_ij k_j
+ *   dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
+ * over the heads of j's group too; each sum in fp32, in a fixed order (bitwise
+ * repeatable), p and ds entering the products as bf16, rounded to bf16 once at the end.
+ *   dout as o; dq, dk, dv bf16 out with the strides of q, k, v (so they may be slices of
+ *   one buffer); none may overlap an input.  Rows that belong to no sequence are left as
+ *   they were.  A NaN or Inf of a sequence may reach all gradients of that sequence, and
+ *   none of another's. */
+lora_status attention_backward(const attn_shape* shape, const uint16_t* dout, const uint16_t* q,
+                               const uint16_t* k, const uint16_t* v, const uint16_t* o,
+                               const float* lse, const int32_t* cu_q, const int32_t* cu_k,
+                               uint16_t* dq, uint16_t* dk, uint16_t* dv, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* ---- paged key-value cache --------------------------------------------- */
+
+/* A layer's cache is n_pages pages of page_size rows for each key head:
+ *   k_cache, v_cache  bf16 [n_pages][n_kv_heads][page_size][head_dim], or in 8 bits
+ *                     (k_scales, v_scales given) uint8 e4m3 codes of that shape with
+ *   k_scales, v_scales uint8 [n_pages][n_kv_heads][page_size][head_dim/32] (E8M0): the
+ *                     8-bit form of rmsnorm_forward_q8, 32 columns to a scale.
+ * Row p of a request lies in page block_table[request][p / page_size], row
+ * p % page_size; the two make its slot, page * page_size + p % page_size. */
+typedef struct {        /* host struct */
+  int32_t n_seqs;       /* 0 .. 4096 */
+  int32_t n_kv_heads;   /* 1 .. 1024 */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t page_size;    /* 16, 32, 64, 128 or 256 */
+  int32_t n_pages;      /* >= 1; n_pages * page_size < 2^31 */
+  int32_t max_pages;    /* columns of a block table, >= 1; max_pages * page_size < 2^31 */
+} kv_shape;
+
+/* Block tables and slot maps of one step from its requests' lengths:
+ *   cached_lens int32 [n_seqs]  rows that each request has in the cache
+ *   new_lens    int32 [n_seqs]  rows that come in this step; < 0: the request has ended
+ *   seq_lens    int32 [n_seqs] out  cached + new rows; 0 for an ended request.  May be
+ *                               cached_lens.
+ *   block_table int32 [n_seqs][max_pages] in/out  entries of the pages that a request has
+ *                               are read; those of its new pages are written
+ *   ring        int32 [n_pages] in/out  the free pages, a queue: new pages are taken, in
+ *                               the requests' order, from ring[head % n_pages] on, an
+ *                               ended request's pages are put, in order, at
+ *                               ring[tail % n_pages] on (for later calls)
+ *   ring_state  int64 [2]  head and tail, counted on for ever: tail - head pages are free
+ *   ring_state_out int64 [2] out, may be ring_state (a captured graph then steps on)
+ *   cu_new      int32 [n_seqs+1] out, nullable  where each request's new rows begin in
+ *                               the packed batch (the cu_q of attention_forward)
+ *   slots       int32 [n_slots] out  each new row's slot, in the packed order; -1 behind
+ *                               the last one
+ *   positions, token_seqs int32 [n_slots] out, nullable  each new row's position and
+ *                               request (an adapter id's index); -1 behind the last one
+ * A request is served, or left out whole: its seq_len then stays the cached one, its
+ * slots are -1, it takes no page, and a bit of the status word says why:
+ *   LORA_FLAG_NO_PAGES    it needs pages, and the pages that it and the requests before
+ *                         it need are more than are free;
+ *   LORA_FLAG_BAD_LENGTH  cached_len is negative, its rows do not fit max_pages, or the
+ *                         batch's rows up to its last one do not fit n_slots (cu_new
+ *                         stops at n_slots);
+ *   LORA_FLAG_BAD_PAGE    ring_state's head and tail do not fit each other or n_pages
+ *                         (nothing is taken or put then); also set where a page id out
+ *                         of range is met: its rows' slots are -1, and it is put into
+ *                         the ring as it is.
+ * Pages that do not fit the ring (the same page put twice) are dropped whole, with
+ * LORA_FLAG_BAD_PAGE.  0 <= n_slots < 2^30.
+ * Workspace: kv_tables_workspace_bytes(shape); word 0 is the status word. */
+size_t kv_tables_workspace_bytes(const kv_shape* shape);
+lora_status kv_tables(const kv_shape* shape, const int32_t* cached_lens, const int32_t* new_lens,
+                      int32_t* seq_lens, int32_t* block_table, int32_t* ring,
+                      const int64_t* ring_state, int64_t* ring_state_out, int32_t* cu_new,
+                      int64_t n_slots, int32_t* slots, int32_t* positions, int32_t* token_seqs,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* New keys and values into the cache: row t of k and v to slot slots[t], rows with slot
+ * -1 nowhere.  In 8 bits each 32 columns are quantised as in rmsnorm_forward_q8.
+ *   k, v bf16 [n] rows of [n_kv_heads][head_dim] at k_stride, v_stride (elements; multiples
+ *        of 8, >= n_kv_heads * head_dim, < 2^31), 16-byte aligned; 0 <= n < 2^30
+ *   slots int32 [n]; another slot outside [-1, n_pages * page_size) sets
+ *        LORA_FLAG_BAD_PAGE and its row goes nowhere.  Slots must differ: of rows with
+ *        one slot, pieces of any may stay.
+ *   caches 16-byte, scales 4-byte aligned; scales both or none.  The caches must not
+ *        overlap k or v.
+ *   ws: at least 256 bytes; word 0 is the status word.
+ * Of the shape, n_seqs and max_pages are not used. */
+lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_t k_stride,
+                     const uint16_t* v, int64_t v_stride, const int32_t* slots, void* k_cache,
+                     void* v_cache, uint8_t* k_scales, uint8_t* v_scales, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* Attention of one new token of each request over its rows in the cache (its own row
+ * written before, by kv_write):
+ *   s_j = scale q . k_j for j < seq_lens[b],  lse = log sum_j exp(s_j),
+ *   o = bf16(sum_j exp(s_j - lse) v_j)
+ *   q    bf16 [n_seqs] rows of [n_heads][head_dim] at q_stride (elements; a multiple of
+ *        8, >= n_heads * head_dim, < 2^31)
+ *   block_table int32 [n_seqs][max_pages], seq_lens int32 [n_seqs] as kv_tables leaves
+ *        them.  seq_len 0: o = 0 and lse = -inf.
+ *   max_len  an upper bound of the lengths (0 .. max_pages * page_size), which sizes the
+ *        launch: a step captured with the longest length to come serves every step.  A
+ *        length outside [0, max_len] counts as 0 and sets LORA_FLAG_BAD_LENGTH; rows of
+ *        a page out of range are left out, with LORA_FLAG_BAD_PAGE.
+ *   o    bf16 [n_seqs][n_heads][head_dim] out, must not overlap q
+ *   lse  fp32 [n_seqs][n_heads] out, nullable
+ * Products and sums are fp32, the weights exp(.) enter the second product as bf16; keys
+ * and values in 8 bits enter as bf16, as the 8-bit x of w4_linear does: exactly, but for
+ * scale bytes under 3 and magnitudes of 2^128 or more.  What a page holds behind a
+ * request's last row is never used.  The
+ * length is split and joined by rules on the request's own length: its results have the
+ * same bits in every batch.  n_heads a multiple of n_kv_heads, <= 1024.
+ * Workspace: attention_decode_workspace_bytes(shape, n_heads, max_len); word 0 is the
+ * status word. */
+size_t attention_decode_workspace_bytes(const kv_shape* shape, int32_t n_heads, int64_t max_len);
+lora_status attention_decode(const kv_shape* shape, int32_t n_heads, const uint16_t* q,
+                             int64_t q_stride, const void* k_cache, const void* v_cache,
+                             const uint8_t* k_scales, const uint8_t* v_scales,
+                             const int32_t* block_table, const int32_t* seq_lens,
+                             int64_t max_len, float scale, uint16_t* o, float* lse, void* ws,
+                             size_t ws_bytes, void* stream);
 
 /* ---- forward without allocation ------------------------------------- */
 

@@ -23,6 +23,7 @@ Modules
   norm      -- RMS norm with the residual's addition, its 8-bit output, its backward
   w4        -- 4-bit weights with a scale per 32: rounding, values, the product
   clip      -- per-adapter gradient norms over many tensors, clipping, AdamW on top
+  attention -- attention over packed prompts and a paged cache, the cache's page tables
   moe       -- top-k routed expert layer with per-(expert, adapter) LoRA
 """
-from . import adam, clip, logprob, lora, loss, mlp, moe, norm, segments, w4  # noqa: F401
+from . import adam, attention, clip, logprob, lora, loss, mlp, moe, norm, segments, w4  # noqa: F401

@@ -24,6 +24,7 @@ LIB_PATH = os.environ.get("LORA_MI355X_LIB") or os.path.join(_HERE, "liblora_mi3
 LORA_OK, LORA_E_INVALID_ARG, LORA_E_UNSUPPORTED, LORA_E_WORKSPACE, LORA_E_HIP, LORA_E_DEVICE_CHECK = range(6)
 FLAG_ID_RANGE, FLAG_UNSORTED, FLAG_TARGET_RANGE, FLAG_BAD_DESC = 0x1, 0x2, 0x4, 0x8
 FLAG_NONFINITE_GRAD, FLAG_NONFINITE_LOSS = 0x10, 0x20
+FLAG_BAD_LENGTH, FLAG_BAD_PAGE, FLAG_NO_PAGES = 0x40, 0x80, 0x100
 IDS_SORTED, IDS_INTERLEAVED = 0, 1
 LOSS_CROSS_ENTROPY, LOSS_IMPORTANCE_SAMPLING, LOSS_PPO, LOSS_CUSTOM = range(4)
 TIMER_BASE_GEMM, TIMER_LOGPROB_FWD, TIMER_LOGPROB_BWD, TIMER_SHRINK, TIMER_EXPAND, TIMER_GRAD, TIMER_ADAM = range(7)
@@ -42,6 +43,8 @@ EXPORTS = [
     "rmsnorm_forward", "rmsnorm_forward_q8", "rmsnorm_backward_workspace_bytes", "rmsnorm_backward",
     "w4_quantize", "w4_linear", "lora_forward_w4_workspace_bytes", "lora_forward_w4",
     "grad_workspace_bytes", "grad_norm", "grad_clip", "adam_step_clipped",
+    "attention_workspace_bytes", "attention_forward", "attention_backward", "kv_tables_workspace_bytes",
+    "kv_tables", "kv_write", "attention_decode_workspace_bytes", "attention_decode",
     "lora_probe_mfma_flops_per_iter", "lora_probe_mfma", "lora_probe_copy", "lora_probe_read",
 ]
 
@@ -86,6 +89,18 @@ class GradShape(ctypes.Structure):
     _fields_ = [("n_elems", ctypes.c_int64), ("n_chunks", ctypes.c_int32),
                 ("n_tensors", ctypes.c_int32), ("n_groups", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class AttnShape(ctypes.Structure):
+    _fields_ = [("n_q", ctypes.c_int64), ("n_k", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64),
+                ("n_seqs", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class KvShape(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 W4_MAX_TOKENS = 256
@@ -157,6 +172,15 @@ def _load() -> ctypes.CDLL:
         "grad_clip": (_I32, [ctypes.POINTER(GradShape), _P, _P, _F, _P, _P, _P, _SZ, _P]),
         "adam_step_clipped": (_I32, [ctypes.POINTER(GradShape), _P, _P, _P, _P, _P, _P, _F] + [_D] * 5 +
                               [_P, _P, _P, _SZ, _P]),
+        "attention_workspace_bytes": (_SZ, [ctypes.POINTER(AttnShape)]),
+        "attention_forward": (_I32, [ctypes.POINTER(AttnShape)] + [_P] * 8 + [_SZ, _P]),
+        "attention_backward": (_I32, [ctypes.POINTER(AttnShape)] + [_P] * 12 + [_SZ, _P]),
+        "kv_tables_workspace_bytes": (_SZ, [ctypes.POINTER(KvShape)]),
+        "kv_tables": (_I32, [ctypes.POINTER(KvShape)] + [_P] * 8 + [_I64] + [_P] * 4 + [_SZ, _P]),
+        "kv_write": (_I32, [ctypes.POINTER(KvShape), _I64, _P, _I64, _P, _I64] + [_P] * 6 + [_SZ, _P]),
+        "attention_decode_workspace_bytes": (_SZ, [ctypes.POINTER(KvShape), _I32, _I64]),
+        "attention_decode": (_I32, [ctypes.POINTER(KvShape), _I32, _P, _I64] + [_P] * 6 + [_I64, _F] + [_P] * 3 +
+                             [_SZ, _P]),
         "lora_probe_mfma_flops_per_iter": (_I64, [_I32]),
         "lora_probe_mfma": (_I32, [_I64, _I32, _P, _P]),
         "lora_probe_copy": (_I32, [_P, _P, _I64, _P]),
@@ -485,6 +509,7 @@ def _stream_for(t: torch.Tensor, stream=None):
 
 
 _BF16, _F32, _I64T, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int64,), (torch.uint8,)
+_I32T = (torch.int32,)
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _E8M0 = (torch.uint8, torch.float8_e8m0fnu)
 
@@ -646,6 +671,133 @@ def adam_step_clipped(shape, table, steps, p, g, m, v, max_norm, lr, beta1=0.9, 
                                  _dense(p_bf16, _BF16, (shape.n_elems,), "p_bf16", dev), pn, _device_ptr(ws, "ws", dev),
                                  ws.nbytes, _stream_for(p, stream)))
     return ws
+
+
+def make_attention_shape(n_q, n_k, n_seqs, n_heads, n_kv_heads, head_dim, scale, causal=True, q_stride=None,
+                         k_stride=None, v_stride=None, o_stride=None) -> AttnShape:
+    """Strides in elements from a token's row to the next; None: rows lie one behind the other."""
+    q, k = n_heads * head_dim, n_kv_heads * head_dim
+    return AttnShape(n_q, n_k, q if q_stride is None else q_stride, k if k_stride is None else k_stride,
+                     k if v_stride is None else v_stride, q if o_stride is None else o_stride, n_seqs, n_heads,
+                     n_kv_heads, head_dim, int(causal), scale)
+
+
+def attention_workspace_bytes(shape: AttnShape) -> int:
+    n = LIB.attention_workspace_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise LoraError(LORA_E_INVALID_ARG, LIB.lora_last_error().decode())
+    return n
+
+
+def _rows(t, n, heads, d, stride, name: str, dev: int):
+    """The pointer of rows of [heads][d] in bf16 whose tokens lie stride elements apart."""
+    if t.dtype != torch.bfloat16 or t.shape != (n, heads, d) or \
+            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or (n > 1 and t.stride(0) != stride))):
+        raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs torch.bfloat16 {(n, heads, d)} with strides {(stride, d, 1)}, "
+                        f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    if t.get_device() != dev or dev < 0:
+        _on_device(t, name, dev)
+    return t.data_ptr()
+
+
+def _attn_args(s, q, k, v, cu_q, cu_k, o, lse, dev):
+    return (_rows(q, s.n_q, s.n_heads, s.head_dim, s.q_stride, "q", dev),
+            _rows(k, s.n_k, s.n_kv_heads, s.head_dim, s.k_stride, "k", dev),
+            _rows(v, s.n_k, s.n_kv_heads, s.head_dim, s.v_stride, "v", dev),
+            _dense(cu_q, _I32T, (s.n_seqs + 1,), "cu_q", dev), _dense(cu_k, _I32T, (s.n_seqs + 1,), "cu_k", dev),
+            _rows(o, s.n_q, s.n_heads, s.head_dim, s.o_stride, "o", dev),
+            _dense(lse, _F32, (s.n_heads, s.n_q), "lse", dev))
+
+
+def attention_forward(shape: AttnShape, q, k, v, cu_q, cu_k, o, lse, ws, stream=None):
+    """q [n_q][n_heads][head_dim], k, v [n_k][n_kv_heads][head_dim] of packed sequences at the
+    offsets cu_q, cu_k (int32 [n_seqs+1]); o like q, lse fp32 [n_heads][n_q]."""
+    dev = q.get_device()
+    pq, pk, pv, cq, ck, po, pl = _attn_args(shape, q, k, v, cu_q, cu_k, o, lse, dev)
+    _check(LIB.attention_forward(ctypes.byref(shape), pq, pk, pv, cq, ck, po, pl, _device_ptr(ws, "ws", dev), ws.nbytes,
+                                 _stream_for(q, stream)))
+
+
+def attention_backward(shape: AttnShape, dout, q, k, v, o, lse, cu_q, cu_k, dq, dk, dv, ws, stream=None):
+    """dq, dk, dv with the shapes and strides of q, k, v; o and lse from the forward."""
+    s, dev = shape, q.get_device()
+    pq, pk, pv, cq, ck, po, pl = _attn_args(s, q, k, v, cu_q, cu_k, o, lse, dev)
+    _check(LIB.attention_backward(ctypes.byref(s), _rows(dout, s.n_q, s.n_heads, s.head_dim, s.o_stride, "dout", dev),
+                                  pq, pk, pv, po, pl, cq, ck, _rows(dq, s.n_q, s.n_heads, s.head_dim, s.q_stride, "dq", dev),
+                                  _rows(dk, s.n_k, s.n_kv_heads, s.head_dim, s.k_stride, "dk", dev),
+                                  _rows(dv, s.n_k, s.n_kv_heads, s.head_dim, s.v_stride, "dv", dev),
+                                  _device_ptr(ws, "ws", dev), ws.nbytes, _stream_for(q, stream)))
+
+
+def make_kv_shape(n_seqs, n_kv_heads, head_dim, page_size, n_pages, max_pages) -> KvShape:
+    return KvShape(n_seqs, n_kv_heads, head_dim, page_size, n_pages, max_pages)
+
+
+def kv_tables_workspace_bytes(shape: KvShape) -> int:
+    n = LIB.kv_tables_workspace_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise LoraError(LORA_E_INVALID_ARG, LIB.lora_last_error().decode())
+    return n
+
+
+def kv_tables(shape: KvShape, cached_lens, new_lens, seq_lens, block_table, ring, ring_state, ring_state_out, cu_new,
+              slots, ws, positions=None, token_seqs=None, stream=None):
+    """Pages for the new rows of each request, and where each row goes; slots, positions and
+    token_seqs int32 [n_slots].  seq_lens may be cached_lens, ring_state_out may be ring_state."""
+    s, dev = shape, block_table.get_device()
+    _arg(slots.dim() == 1, "slots must be [n_slots]")
+    per_seq = lambda t, name: _dense(t, _I32T, (s.n_seqs,), name, dev)  # noqa: E731
+    per_slot = lambda t, name: _dense(t, _I32T, slots.shape, name, dev)  # noqa: E731
+    _check(LIB.kv_tables(ctypes.byref(s), per_seq(cached_lens, "cached_lens"), per_seq(new_lens, "new_lens"),
+                         per_seq(seq_lens, "seq_lens"), _dense(block_table, _I32T, (s.n_seqs, s.max_pages), "block_table", dev),
+                         _dense(ring, _I32T, (s.n_pages,), "ring", dev), _dense(ring_state, _I64T, (2,), "ring_state", dev),
+                         _dense(ring_state_out, _I64T, (2,), "ring_state_out", dev),
+                         _dense(cu_new, _I32T, (s.n_seqs + 1,), "cu_new", dev), slots.numel(), per_slot(slots, "slots"),
+                         per_slot(positions, "positions"), per_slot(token_seqs, "token_seqs"), _device_ptr(ws, "ws", dev),
+                         ws.nbytes, _stream_for(block_table, stream)))
+
+
+def _cache_args(s, k_cache, v_cache, k_scales, v_scales, dev):
+    rows = (s.n_pages, s.n_kv_heads, s.page_size)
+    types = _BF16 if k_scales is None else _E4M3
+    blocks = (*rows, s.head_dim // 32)
+    return (_dense(k_cache, types, (*rows, s.head_dim), "k_cache", dev), _dense(v_cache, types, (*rows, s.head_dim), "v_cache", dev),
+            _dense(k_scales, _E8M0, blocks, "k_scales", dev), _dense(v_scales, _E8M0, blocks, "v_scales", dev))
+
+
+def kv_write(shape: KvShape, k, v, slots, k_cache, v_cache, ws, k_scales=None, v_scales=None, stream=None):
+    """Rows t of k and v [n][n_kv_heads][head_dim] to slot slots[t] of the caches
+    [n_pages][n_kv_heads][page_size][head_dim]: bf16, or e4m3 codes with E8M0 scales [..][head_dim/32]."""
+    s, n, dev = shape, slots.numel(), k.get_device()
+    ks, vs = (t.stride(0) if n > 1 else s.n_kv_heads * s.head_dim for t in (k, v))
+    kc, vc, sk, sv = _cache_args(s, k_cache, v_cache, k_scales, v_scales, dev)
+    _check(LIB.kv_write(ctypes.byref(s), n, _rows(k, n, s.n_kv_heads, s.head_dim, ks, "k", dev), ks,
+                        _rows(v, n, s.n_kv_heads, s.head_dim, vs, "v", dev), vs, _dense(slots, _I32T, (n,), "slots", dev),
+                        kc, vc, sk, sv, _device_ptr(ws, "ws", dev), ws.nbytes, _stream_for(k, stream)))
+
+
+def attention_decode_workspace_bytes(shape: KvShape, n_heads, max_len) -> int:
+    n = LIB.attention_decode_workspace_bytes(ctypes.byref(shape), n_heads, max_len)
+    if n == 0:
+        raise LoraError(LORA_E_INVALID_ARG, LIB.lora_last_error().decode())
+    return n
+
+
+def attention_decode(shape: KvShape, q, k_cache, v_cache, block_table, seq_lens, max_len, scale, o, ws, k_scales=None,
+                     v_scales=None, lse=None, stream=None):
+    """q [n_seqs][n_heads][head_dim], the new token of each request, against its seq_lens rows in
+    the cache (kv_write, kv_tables), none longer than max_len; o like q, lse fp32 [n_seqs][n_heads]."""
+    s, dev = shape, q.get_device()
+    _arg(q.dim() == 3, "q must be [n_seqs][n_heads][head_dim]")
+    heads = q.shape[1]
+    stride = q.stride(0) if s.n_seqs > 1 else heads * s.head_dim
+    kc, vc, sk, sv = _cache_args(s, k_cache, v_cache, k_scales, v_scales, dev)
+    _check(LIB.attention_decode(ctypes.byref(s), heads, _rows(q, s.n_seqs, heads, s.head_dim, stride, "q", dev), stride, kc, vc,
+                                sk, sv, _dense(block_table, _I32T, (s.n_seqs, s.max_pages), "block_table", dev),
+                                _dense(seq_lens, _I32T, (s.n_seqs,), "seq_lens", dev), max_len, scale,
+                                _dense(o, _BF16, (s.n_seqs, heads, s.head_dim), "o", dev),
+                                _dense(lse, _F32, (s.n_seqs, heads), "lse", dev), _device_ptr(ws, "ws", dev), ws.nbytes,
+                                _stream_for(q, stream)))
 
 
 def lora_probe_mfma(iters, blocks, sink, stream=None):

@@ -1,0 +1,176 @@
+"""Host-side refusals of the attention and key-value cache calls (CPU only: every call here
+fails before anything is enqueued, or has nothing to do, whatever its pointers hold)."""
+import ctypes
+
+import pytest
+
+from test_operator_refusals import BIG, L, ODD, P, _is  # noqa: F401
+
+
+def at(n):
+    return ctypes.c_void_p(n << 20)     # buffers 1 MiB apart, never dereferenced
+
+
+def test_attention(L):  # noqa: F811
+    lib, E = L.LIB, L.LORA_E_INVALID_ARG
+    good = dict(n_q=100, n_k=120, n_seqs=3, n_heads=4, n_kv_heads=2, head_dim=64, scale=0.1)
+    mk = lambda **kw: L.make_attention_shape(**{**good, **kw})  # noqa: E731
+    need = L.attention_workspace_bytes(mk())
+    assert 256 + 4 * 4 * 100 <= need
+
+    def fwd(s=None, q=at(1), k=at(2), v=at(3), cq=P, ck=P, o=at(4), lse=P, ws=P, nb=BIG):
+        return lib.attention_forward(ctypes.byref(s or mk()), q, k, v, cq, ck, o, lse, ws, nb, None)
+
+    def bwd(s=None, do=at(1), q=at(2), k=at(3), v=at(4), o=at(5), lse=P, cq=P, ck=P, dq=at(6), dk=at(7), dv=at(8), ws=P, nb=BIG):
+        return lib.attention_backward(ctypes.byref(s or mk()), do, q, k, v, o, lse, cq, ck, dq, dk, dv, ws, nb, None)
+
+    shapes = [(dict(n_q=-1), E, b"n_q"), (dict(n_k=1 << 30), E, b"n_k"), (dict(n_seqs=-1), E, b"n_seqs"), (dict(n_seqs=65537), E, b"n_seqs"),
+              (dict(n_heads=3), E, b"multiple"), (dict(n_heads=0), E, b"multiple"), (dict(n_kv_heads=0), E, b"multiple"),
+              (dict(n_heads=1026), E, b"1024"), (dict(head_dim=80), L.LORA_E_UNSUPPORTED, b"64 or 128"), (dict(head_dim=256), L.LORA_E_UNSUPPORTED, b"64 or 128"),
+              (dict(scale=float("nan")), E, b"scale"), (dict(scale=float("inf")), E, b"scale"), (dict(causal=2), E, b"causal"),
+              (dict(q_stride=255), E, b"multiple of 8"), (dict(q_stride=248), E, b"shorter"), (dict(k_stride=120), E, b"shorter"),
+              (dict(v_stride=-8), E, b"shorter"), (dict(o_stride=1 << 31), E, b"2^31"),
+              (dict(n_q=(1 << 30) - 1, n_heads=1024, n_kv_heads=2), L.LORA_E_UNSUPPORTED, b"one launch")]
+    for kw, kind, word in shapes:
+        s = mk(**kw)
+        assert lib.attention_workspace_bytes(ctypes.byref(s)) == 0
+        _is(L, fwd(s=s), kind, word)
+        _is(L, bwd(s=s), kind, word)
+    _is(L, lib.attention_forward(None, P, P, P, P, P, P, P, P, BIG, None), E, b"NULL")
+    for k in ("q", "k", "v", "cq", "ck", "o", "lse"):
+        _is(L, fwd(**{k: None}), E, b"non-NULL")
+    for k in ("do", "q", "k", "v", "o", "lse", "cq", "ck", "dq", "dk", "dv"):
+        _is(L, bwd(**{k: None}), E, b"non-NULL")
+    for k in ("q", "k", "v", "o", "ws"):
+        _is(L, fwd(**{k: ODD}), E, b"aligned")
+    for k in ("do", "q", "k", "v", "o", "dq", "dk", "dv", "ws"):
+        _is(L, bwd(**{k: ODD}), E, b"aligned")
+    for f in (fwd, bwd):
+        _is(L, f(ws=None), L.LORA_E_WORKSPACE)
+        _is(L, f(nb=need - 1), L.LORA_E_WORKSPACE)
+    for k in ("q", "k", "v"):
+        _is(L, fwd(**{k: at(4)}), E, b"overlaps")
+    for own, out in ((6, "dq"), (7, "dk"), (8, "dv")):
+        for n in range(1, 9):
+            if n != own:
+                _is(L, bwd(**{out: at(n)}), E, b"overlap")
+    # slices of one buffer lie between one another: taken; a slice too far: refused
+    row = 8 * 64
+    s = mk(n_k=100, q_stride=row, k_stride=row, v_stride=row)
+    sl = lambda base, head: ctypes.c_void_p((base << 20) + 2 * 64 * head)  # noqa: E731
+    ok = dict(q=sl(1, 0), k=sl(1, 4), v=sl(1, 6), dq=sl(3, 0), dk=sl(3, 4), dv=sl(3, 6))
+    none = mk(n_k=100, q_stride=row, k_stride=row, v_stride=row, n_seqs=0)     # past every check, nothing to do
+    assert bwd(s=none, do=at(8), o=at(9), **ok) == L.LORA_OK
+    _is(L, bwd(s=s, do=at(8), o=at(9), **{**ok, "dk": sl(3, 3)}), E, b"overlap")
+    _is(L, bwd(s=s, do=at(8), o=at(9), **{**ok, "dv": sl(3, 7)}), E, b"overlap")
+    _is(L, bwd(s=s, do=at(8), o=at(9), **{**ok, "dv": sl(1, 6)}), E, b"overlaps an input")
+    s = mk(n_q=0, n_k=0)
+    assert fwd(s=s, q=None, k=None, v=None, o=None, lse=None) == L.LORA_OK
+    assert bwd(s=s, do=None, q=None, k=None, v=None, o=None, lse=None, dq=None, dk=None, dv=None) == L.LORA_OK
+    assert fwd(s=mk(n_seqs=0), cq=None, ck=None) == L.LORA_OK
+
+
+def _kv(L, **kw):
+    return L.make_kv_shape(**{**dict(n_seqs=3, n_kv_heads=2, head_dim=64, page_size=16, n_pages=20, max_pages=4), **kw})
+
+
+def _bad_kv(L):
+    E, U = L.LORA_E_INVALID_ARG, L.LORA_E_UNSUPPORTED
+    return [(dict(n_seqs=-1), E), (dict(n_seqs=4097), E), (dict(n_kv_heads=0), E), (dict(n_kv_heads=1025), E), (dict(n_pages=0), E),
+            (dict(max_pages=0), E), (dict(head_dim=96), U), (dict(page_size=8), U), (dict(page_size=24), U), (dict(page_size=512), U),
+            (dict(n_pages=1 << 27), U), (dict(max_pages=1 << 27), U)]
+
+
+def test_tables(L):  # noqa: F811
+    lib, E = L.LIB, L.LORA_E_INVALID_ARG
+
+    def call(s=None, c=P, n=P, sl=at(1), t=P, r=P, st=P, so=P, cu=P, ns=10, slots=P, pos=P, seq=P, ws=P, nb=BIG):
+        return lib.kv_tables(ctypes.byref(s or _kv(L)), c, n, sl, t, r, st, so, cu, ns, slots, pos, seq, ws, nb, None)
+
+    for kw, kind in _bad_kv(L):
+        assert lib.kv_tables_workspace_bytes(ctypes.byref(_kv(L, **kw))) == 0
+        _is(L, call(s=_kv(L, **kw)), kind)
+    for k in ("c", "n", "sl", "t", "r", "st", "so", "slots"):
+        _is(L, call(**{k: None}), E, b"non-NULL")
+    odd4 = ctypes.c_void_p(66)
+    for k in ("c", "n", "sl", "t", "r", "cu", "slots", "pos", "seq"):
+        _is(L, call(**{k: odd4}), E, b"aligned")
+    for k in ("st", "so"):
+        _is(L, call(**{k: ctypes.c_void_p(68)}), E, b"aligned")
+    _is(L, call(ns=-1), E, b"n_slots")
+    _is(L, call(ns=1 << 30), E, b"n_slots")
+    _is(L, call(sl=P), E, b"same buffer")
+    _is(L, call(ws=None), L.LORA_E_WORKSPACE)
+    _is(L, call(nb=255), L.LORA_E_WORKSPACE)
+    _is(L, call(ws=ODD), E, b"aligned")
+
+
+def test_write(L):  # noqa: F811
+    lib, E = L.LIB, L.LORA_E_INVALID_ARG
+
+    def call(s=None, n=5, k=at(1), ks=128, v=at(2), vs=128, sl=P, kc=at(3), vc=at(4), sk=None, sv=None, ws=P, nb=256):
+        return lib.kv_write(ctypes.byref(s or _kv(L)), n, k, ks, v, vs, sl, kc, vc, sk, sv, ws, nb, None)
+
+    for kw, kind in _bad_kv(L):
+        _is(L, call(s=_kv(L, **kw)), kind)
+    for k in ("k", "v", "sl", "kc", "vc"):
+        _is(L, call(**{k: None}), E)
+    for k in ("k", "v", "kc", "vc", "ws"):
+        _is(L, call(**{k: ODD}), E, b"aligned")
+    for st in (120, 132, 1 << 31, -128):
+        _is(L, call(ks=st), E, b"stride")
+        _is(L, call(vs=st), E, b"stride")
+    _is(L, call(n=-1), E, b"n ")
+    _is(L, call(n=1 << 30), E, b"n ")
+    _is(L, call(sk=at(5)), E, b"go together")
+    _is(L, call(sk=at(5), sv=ctypes.c_void_p(66)), E, b"4-byte")
+    _is(L, call(ws=None), L.LORA_E_WORKSPACE)
+    _is(L, call(nb=255), L.LORA_E_WORKSPACE)
+    for a, b in (("k", 3), ("k", 4), ("v", 3), ("v", 4)):
+        _is(L, call(**{a: at(b)}), E, b"overlaps")
+    _is(L, call(vc=at(3)), E, b"caches overlap")
+    assert call(n=0, k=None, v=None, sl=None) == L.LORA_OK
+
+
+def test_decode(L):  # noqa: F811
+    lib, E = L.LIB, L.LORA_E_INVALID_ARG
+
+    def call(s=None, h=4, q=at(1), qs=256, kc=at(2), vc=at(3), sk=None, sv=None, t=P, ln=P, m=50, sc=0.1, o=at(4), lse=None, ws=P, nb=BIG):
+        return lib.attention_decode(ctypes.byref(s or _kv(L)), h, q, qs, kc, vc, sk, sv, t, ln, m, sc, o, lse, ws, nb, None)
+
+    size = lambda s=None, h=4, m=50: lib.attention_decode_workspace_bytes(ctypes.byref(s or _kv(L)), h, m)  # noqa: E731
+    for kw, kind in _bad_kv(L):
+        assert size(s=_kv(L, **kw)) == 0
+        _is(L, call(s=_kv(L, **kw)), kind)
+    for h in (0, 3, 1026, -2):
+        assert size(h=h) == 0
+        _is(L, call(h=h), E, b"n_heads")
+    for m in (-1, 65):
+        assert size(m=m) == 0
+        _is(L, call(m=m), E, b"max_len")
+    assert size(s=_kv(L, n_seqs=4096, n_kv_heads=1024), h=1024) == 0 and b"one launch" in lib.lora_last_error()
+    for k in ("q", "kc", "vc", "t", "ln", "o"):
+        _is(L, call(**{k: None}), E)
+    for k in ("q", "kc", "vc", "o", "ws"):
+        _is(L, call(**{k: ODD}), E, b"aligned")
+    for k in ("t", "ln", "lse"):
+        _is(L, call(**{k: ctypes.c_void_p(66)}), E, b"aligned")
+    for st in (248, 260, 1 << 31):
+        _is(L, call(qs=st), E, b"q_stride")
+    _is(L, call(sc=float("inf")), E, b"scale")
+    _is(L, call(sk=at(6)), E, b"go together")
+    long = _kv(L, max_pages=400)
+    need = size(s=long, m=6400)
+    assert need >= 256 + 3 * 4 * 32 * (8 + 4 * 64) and size() == 256
+    _is(L, call(s=long, m=6400, nb=need - 1), L.LORA_E_WORKSPACE)
+    _is(L, call(ws=None), L.LORA_E_WORKSPACE)
+    _is(L, call(o=at(1)), E, b"overlaps q")
+    assert call(s=_kv(L, n_seqs=0), q=None, o=None, t=None, ln=None) == L.LORA_OK
+
+
+@pytest.mark.parametrize("bound", [0, 1, 128, 129, 1000, 4096, 4097, 100000])
+def test_decode_workspace_grows_with_the_bound(L, bound):  # noqa: F811
+    s = _kv(L, max_pages=10000)
+    n = L.attention_decode_workspace_bytes(s, 8, bound)
+    parts = min(32, max(1, -(-bound // 128)))
+    assert n == 256 if parts == 1 else n >= 256 + 3 * 8 * parts * (8 + 4 * 64)
