@@ -656,7 +656,7 @@ typedef struct {        /* host struct */
   int64_t q_stride;     /* elements from a row of q (and dq) to the next, >= n_heads * head_dim */
   int64_t k_stride;     /* of k, dk; >= n_kv_heads * head_dim */
   int64_t v_stride;     /* of v, dv; likewise */
-  int64_t o_stride;     /* of o, dout; >= n_heads * head_dim.  Strides: multiples of 8, < 2^31 */
+  int64_t o_stride;     /* of o, dout; >= n_heads * head_dim.  Strides: multiples of 8, < 2^24 */
   int32_t n_seqs;       /* 0 .. 65536 */
   int32_t n_heads;      /* a multiple of n_kv_heads; <= 1024 */
   int32_t n_kv_heads;   /* >= 1 */

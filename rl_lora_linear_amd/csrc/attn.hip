@@ -19,6 +19,8 @@
 // dk and dv, and dq, are made by two kernels that each recompute the scores (7 products in
 // place of 5): every sum then has one owner and a fixed order, with no atomics and no
 // partial results in memory.
+#include <type_traits>
+
 #include "attn.hpp"
 
 namespace lora {
@@ -37,6 +39,7 @@ struct AttnArgs {
   int32_t* status;
   int64_t q_stride, k_stride, v_stride, o_stride, n_q, n_k;
   int32_t n_seqs, n_heads, n_kv, group, causal, tiles;
+  int32_t wpr, shift;   // forward: waves of a block in one head; log2 of its rows
   float scale, scale_log2;
 };
 
@@ -47,9 +50,10 @@ struct AttnSeq {
   int64_t q0, k0;
   int lq, lk, tile;   // tile < 0: nothing to do
 };
-__device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_t* cu, int id) {
+__device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_t* cu, int id,
+                                                 int shift = AT_SHIFT) {
   const int lane = threadIdx.x & 63;
-  const auto first = [&](int b) { return (cu[b] >> AT_SHIFT) + b; };
+  const auto first = [&](int b) { return (cu[b] >> shift) + b; };
   int lo = 0, end = a.n_seqs;
   while (end - lo > 1) {
     const int step = (end - lo + 63) / 64, j = lo + lane * step;
@@ -64,7 +68,7 @@ __device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_
   if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) return s;
   s.q0 = q0, s.k0 = k0, s.lq = q1 - q0, s.lk = k1 - k0;
   s.tile = id - first(b);
-  if (s.tile < 0 || (int64_t)s.tile * AT_ROWS >= (cu == a.cu_q ? s.lq : s.lk)) s.tile = -1;
+  if (s.tile < 0 || (int64_t)s.tile << shift >= (cu == a.cu_q ? s.lq : s.lk)) s.tile = -1;
   return s;
 }
 
@@ -118,6 +122,42 @@ __device__ __forceinline__ bf16x8 transposed_op(const char* tile, int row0, int 
   return as_bf16x8(make_uint4(a.x, a.y, b.x, b.y));
 }
 
+// The same from addresses worked out before: two rows' places in a tile.
+template <int D>
+__device__ __forceinline__ void transposed_at(uint32_t* at, int dt, int lane) {
+  const int i = lane & 15, r = 4 * (lane >> 5) + (i >> 2);
+  const int c = dt * 4 + (lane >> 4 & 1) * 2 + ((i & 3) >> 1), lo = (i & 1) * 8;
+  at[0] = at_lds<D>(r, c) + lo;
+  at[1] = at_lds<D>(r + 8, c) + lo;
+}
+__device__ __forceinline__ bf16x8 transposed_pair(const char* tile, const uint32_t* at) {
+  const uint2 a = tr_read((const uint4*)tile, at[0]), b = tr_read((const uint4*)tile, at[1]);
+  return as_bf16x8(make_uint4(a.x, a.y, b.x, b.y));
+}
+
+// LDS-DMA, 16 bytes a lane from base + voff, the lanes' one behind the other from LDS byte
+// `to` on.  Issued by hand: the compiler would wait for it before every LDS read.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ __forceinline__ void dma16(uint32_t voff, const void* base, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(voff), "s"(base) : "memory");
+}
+// Rows r0 .. r0 + AT_TILE - 1 of a [rows][D] matrix to LDS, by NW waves.  Rows past the end
+// are copies of the last one: their weights are 0.
+template <int D, int NW>
+__device__ __forceinline__ void dma_tile(const uint16_t* src, int64_t stride, int r0, int rows, uint32_t to, int wave,
+                                         int lane) {
+  constexpr int CH = D / 8, PER = 64 / CH, N = AT_TILE / PER / NW;   // rows of an instruction; instructions
+  const uint16_t* const base = src + r0 * stride;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int n = wave * N + j, r = n * PER + lane / CH;
+    const uint32_t at = (uint32_t)min(r, rows - 1 - r0) * (uint32_t)(stride * 2) + (((lane % CH) ^ at_swz<D>(r)) << 4);
+    dma16(at, base, to + n * 1024);
+  }
+}
+
 // A wave's own 32 rows as operand: lane (l, h) holds columns 16 kk + 8 h + 0..7 of row l.
 template <int D>
 __device__ __forceinline__ void load_rows(bf16x8* f, const uint16_t* row, int h) {
@@ -143,27 +183,32 @@ __device__ __forceinline__ void store_row(uint16_t* row, const f32x16* x, float 
           make_uint2(pack2bf(x[dt][r] * mul, x[dt][r + 1] * mul), pack2bf(x[dt][r + 2] * mul, x[dt][r + 3] * mul));
 }
 
+// The halves of a word that hold NaN or Inf, as a mask.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+  return ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u) | ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u);
+}
 __device__ __forceinline__ bool not_finite(bf16x8 x) {
   const uint4 u = __builtin_bit_cast(uint4, x);
-  bool bad = false;
-  for (uint32_t w : {u.x, u.y, u.z, u.w}) bad |= (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u;
-  return bad;
+  return (odd_halves(u.x) | odd_halves(u.y) | odd_halves(u.z) | odd_halves(u.w)) != 0;
 }
 
-// acc += V^T P^T over 16 keys (key0 .. in the order above) where V holds NaN or Inf: key
-// by key, kept for the queries that see the key.  A weight of 0 would not keep it out.
+// acc += V^T P^T over 16 keys (key0 .. in the order above) where V may hold NaN or Inf:
+// these are taken out and added key by key, for the queries that see the key.  (A weight
+// of 0 would not keep them out; what other queries get has the bits of the plain product.)
 __device__ __forceinline__ f32x16 product_seen(bf16x8 v, bf16x8 p, f32x16 acc, int key0, int last_key) {
   const int h = threadIdx.x >> 5 & 1;
   const uint4 u = __builtin_bit_cast(uint4, v);
+  const uint4 m = make_uint4(odd_halves(u.x), odd_halves(u.y), odd_halves(u.z), odd_halves(u.w));
+  acc = mfma32(as_bf16x8(make_uint4(u.x & ~m.x, u.y & ~m.y, u.z & ~m.z, u.w & ~m.w)), p, acc);
 #pragma unroll 1
   for (int i = 0; i < 16; ++i) {
     const int j = i & 7, hi = i >> 3;
     const uint32_t keep = h != hi ? 0u : j & 1 ? 0xFFFF0000u : 0xFFFFu;
     uint4 w;
-    w.x = (j >> 1) == 0 ? u.x & keep : 0u;
-    w.y = (j >> 1) == 1 ? u.y & keep : 0u;
-    w.z = (j >> 1) == 2 ? u.z & keep : 0u;
-    w.w = (j >> 1) == 3 ? u.w & keep : 0u;
+    w.x = (j >> 1) == 0 ? u.x & m.x & keep : 0u;
+    w.y = (j >> 1) == 1 ? u.y & m.y & keep : 0u;
+    w.z = (j >> 1) == 2 ? u.z & m.z & keep : 0u;
+    w.w = (j >> 1) == 3 ? u.w & m.w & keep : 0u;
     const f32x16 with = mfma32(as_bf16x8(w), p, acc);
     const bool seen = key0 + 8 * (j >> 2) + 4 * hi + (j & 3) <= last_key;
 #pragma unroll
@@ -173,87 +218,155 @@ __device__ __forceinline__ f32x16 product_seen(bf16x8 v, bf16x8 p, f32x16 acc, i
 }
 
 // ---------------------------------------------------------------- forward
-template <int D>
-__global__ __launch_bounds__(64 * AT_WAVES) void attention_fwd_kernel(AttnArgs a) {
+// NW waves of 32 query rows: `wpr` of them behind one another in one head, the rest in the
+// next heads of the same group, which read the same tiles.  Tiles of 64 keys pass through
+// two LDS stages by LDS-DMA, one barrier a tile.  Two waves on each SIMD take turns: while
+// one computes its weights the other's products run.
+// The weights are powers of two relative to a reference that follows the row's maximum
+// only when that has passed it by 2^6: they stay below 2^6, exact as any float, and the
+// output is hardly ever rescaled.
+constexpr float AT_SLACK = 6.f;
+
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
-  __shared__ uint4 lds[2 * AT_TILE * D / 8];
-  char *const kt = (char*)lds, *const vt = kt + AT_TILE * D * 2;
+  constexpr int TILE = AT_TILE * D * 2;            // bytes of one operand of a stage
+  __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 31, h = lane >> 5;
   if (blockIdx.x == 0) check_sequences(a);
-  const int hx = blockIdx.x % a.n_heads, kvh = hx % a.n_kv, head = kvh * a.group + hx / a.n_kv;
-  const AttnSeq s = find_sequence(a, a.cu_q, a.tiles - 1 - blockIdx.x / a.n_heads);
+  const int per_block = NW / a.wpr, columns = a.n_heads / per_block;   // heads of a block; blocks of a row tile
+  const int hx = blockIdx.x % columns, kvh = hx % a.n_kv;
+  const int head = kvh * a.group + hx / a.n_kv * per_block + wave / a.wpr;
+  const AttnSeq s = find_sequence(a, a.cu_q, a.tiles - 1 - blockIdx.x / columns, a.shift);
   if (s.tile < 0) return;
-  const int row0 = s.tile * AT_ROWS, w0 = row0 + wave * 32, i = w0 + l;   // query row
+  const int row0 = s.tile << a.shift, w0 = row0 + wave % a.wpr * 32, i = w0 + l;   // query row
   const int ahead = s.lk - s.lq;
   // the last key that this lane's query, the wave and the block see
   const int last = a.causal ? min(i + ahead, s.lk - 1) : s.lk - 1;
-  const int wave_first = a.causal ? w0 + ahead : s.lk - 1, wave_last = a.causal ? min(w0 + 31 + ahead, s.lk - 1) : s.lk - 1;
-  const int keys = a.causal ? min(row0 + AT_ROWS + ahead, s.lk) : s.lk;
+  const int wave_first = a.causal ? w0 + ahead : s.lk - 1;
+  const int wave_last = w0 >= s.lq ? -1 : a.causal ? min(w0 + 31 + ahead, s.lk - 1) : s.lk - 1;
+  const int keys = a.causal ? min(row0 + (1 << a.shift) + ahead, s.lk) : s.lk;
+  const int tiles = keys > 0 ? (keys + AT_TILE - 1) / AT_TILE : 0;
 
+  const uint16_t* const kp = a.k + s.k0 * a.k_stride + kvh * D;
+  const uint16_t* const vp = a.v + s.k0 * a.v_stride + kvh * D;
+  const uint32_t lds0 = lds_offset(lds);
+  const auto stage = [&](int t, int st) {
+    dma_tile<D, NW>(kp, a.k_stride, t * AT_TILE, s.lk, lds0 + st * 2 * TILE, wave, lane);
+    dma_tile<D, NW>(vp, a.v_stride, t * AT_TILE, s.lk, lds0 + st * 2 * TILE + TILE, wave, lane);
+  };
+
+  // a negative scale turns q's signs, a scale of 0 makes q 0: the maximum of the products
+  // is then that of the scores
   bf16x8 qf[NK];
   load_rows<D>(qf, a.q + (s.q0 + min(i, s.lq - 1)) * a.q_stride + head * D, h);
+  const float c = a.scale == 0.f ? 1.f : fabsf(a.scale_log2);
+  if (a.scale <= 0.f) {
+    const uint32_t turn = a.scale < 0.f ? 0x80008000u : 0u, keep = a.scale < 0.f ? ~0u : 0u;
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      const uint4 u = __builtin_bit_cast(uint4, qf[kk]);
+      qf[kk] = as_bf16x8(make_uint4((u.x ^ turn) & keep, (u.y ^ turn) & keep, (u.z ^ turn) & keep, (u.w ^ turn) & keep));
+    }
+  }
+  if (tiles) stage(0, 0);
   f32x16 acc[ND];
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[dt][r] = 0.f;
-  float m = -INFINITY, sum = 0.f;
-  const uint16_t* const kp = a.k + s.k0 * a.k_stride + kvh * D;
-  const uint16_t* const vp = a.v + s.k0 * a.v_stride + kvh * D;
+  float ref = -INFINITY, sum = 0.f;
 
-  for (int t0 = 0; t0 < keys; t0 += AT_TILE) {
-    __syncthreads();
-    stage_tile<D>(kt, kp, a.k_stride, t0, s.lk);
-    stage_tile<D>(vt, vp, a.v_stride, t0, s.lk);
-    __syncthreads();
-    if (t0 > wave_last || w0 >= s.lq) continue;
-    const bool masked = t0 + AT_TILE - 1 > wave_first || t0 + AT_TILE > s.lk;
+  // where this lane's operands lie in a tile
+  uint32_t ka[NK], va[ND][2];
+#pragma unroll
+  for (int kk = 0; kk < NK; ++kk) ka[kk] = at_lds<D>(l, 2 * kk + h);
+#pragma unroll
+  for (int dt = 0; dt < ND; ++dt) transposed_at<D>(va[dt], dt, lane);
+
+  const auto step = [&](int t, auto stage_c, auto masked_c) {
+    constexpr int K0 = decltype(stage_c)::value * 2 * TILE, V0 = K0 + TILE;
+    constexpr bool MASKED = decltype(masked_c)::value;
+    const int t0 = t * AT_TILE;
     f32x16 x[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) x[t][r] = 0.f;
+      for (int r = 0; r < 16; ++r) x[u][r] = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < NK; ++kk) x[t] = mfma32(direct_op<D>(kt, t * 32, kk, l, h), qf[kk], x[t]);
+      for (int kk = 0; kk < NK; ++kk)
+        x[u] = mfma32(as_bf16x8(*(const uint4*)(lds + K0 + u * 32 * D * 2 + ka[kk])), qf[kk], x[u]);
     }
-    float top = -INFINITY;
+    if (MASKED) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (t0 + u * 32 + result_row(r, h) > last) x[u][r] = -INFINITY;
+    }
+    float top = fmaxf(x[0][0], x[1][0]);
+#pragma unroll
+    for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(top, x[0][r]), x[1][r]);
+    top = fmaxf(top, __shfl_xor(top, 32, kWave)) * c;
+    if (__any(top > ref + AT_SLACK)) {
+      const float next = fmaxf(ref, top), scale = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ref - next);
+      ref = next;
+      sum *= scale;
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[dt][r] *= scale;
+    }
+    const float base = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        x[t][r] *= a.scale_log2;
-        if (masked && t0 + t * 32 + result_row(r, h) > last) x[t][r] = -INFINITY;
-        top = fmaxf(top, x[t][r]);
+        x[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][r], c, -base));
+        sum += x[u][r];
       }
-    top = fmaxf(top, __shfl_xor(top, 32, kWave));
-    const float m_new = fmaxf(m, top), ref = m_new == -INFINITY ? 0.f : m_new;
-    const float keep = __builtin_amdgcn_exp2f(m - ref);
-    m = m_new;
-    sum *= keep;
+    if (MASKED) {
+      bool odd = false;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) sum += x[t][r] = __builtin_amdgcn_exp2f(x[t][r] - ref);
+        for (int dt = 0; dt < ND; ++dt) odd |= not_finite(transposed_pair(lds + V0 + b * 16 * D * 2, va[dt]));
+      if (__any(odd)) {
 #pragma unroll
-    for (int dt = 0; dt < ND; ++dt)
+        for (int b = 0; b < 4; ++b) {
+          const bf16x8 p = pack_op(x[b >> 1], b & 1);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[dt][r] *= keep;
+          for (int dt = 0; dt < ND; ++dt)
+            acc[dt] = product_seen(transposed_pair(lds + V0 + b * 16 * D * 2, va[dt]), p, acc[dt], t0 + b * 16, last);
+        }
+        return;
+      }
+    }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const bf16x8 p = pack_op(x[b >> 1], b & 1);
 #pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        const bf16x8 v = transposed_op<D>(vt, b * 16, dt, lane);
-        if (masked && __any(not_finite(v))) acc[dt] = product_seen(v, p, acc[dt], t0 + b * 16, last);
-        else acc[dt] = mfma32(v, p, acc[dt]);
-      }
+      for (int dt = 0; dt < ND; ++dt) acc[dt] = mfma32(transposed_pair(lds + V0 + b * 16 * D * 2, va[dt]), p, acc[dt]);
     }
+  };
+  // tile t has landed for every wave, and every wave is done with the other stage
+  const auto turn = [&](int t, auto stage_c) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (t + 1 < tiles) stage(t + 1, 1 - decltype(stage_c)::value);
+    const int t0 = t * AT_TILE;
+    if (t0 > wave_last) return;
+    if (t0 + AT_TILE - 1 > wave_first || t0 + AT_TILE > s.lk) step(t, stage_c, std::true_type{});
+    else step(t, stage_c, std::false_type{});
+  };
+  for (int t = 0; t < tiles; t += 2) {
+    turn(t, std::integral_constant<int, 0>{});
+    if (t + 1 < tiles) turn(t + 1, std::integral_constant<int, 1>{});
   }
   if (i >= s.lq) return;
   sum += __shfl_xor(sum, 32, kWave);
   store_row<D>(a.out + (s.q0 + i) * a.o_stride + head * D, acc, sum == 0.f ? 0.f : 1.f / sum, h);
-  if (h == 0) a.lse[head * a.n_q + s.q0 + i] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * AT_LN2;
+  if (h == 0) a.lse[head * a.n_q + s.q0 + i] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * AT_LN2;
 }
 
 // ---------------------------------------------------------------- dq
@@ -443,10 +556,19 @@ lora_status launch_attention_fwd(const attn_shape& sh, const uint16_t* q, const 
                                  const uint16_t* v, const int32_t* cu_q, const int32_t* cu_k,
                                  uint16_t* o, float* lse, void* ws, hipStream_t s) {
   AttnArgs a = attn_args(sh, q, k, v, cu_q, cu_k, ws);
-  a.out = o, a.lse = lse, a.tiles = attn_tiles(sh.n_q, sh.n_seqs);
-  const dim3 grid((unsigned)((int64_t)a.tiles * a.n_heads)), block(64 * AT_WAVES);
-  if (sh.head_dim == 128) hipLaunchKernelGGL(attention_fwd_kernel<128>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(attention_fwd_kernel<64>, grid, block, 0, s, a);
+  a.out = o, a.lse = lse;
+  const auto tiles = [&](int shift) { return (sh.n_q >> shift) + sh.n_seqs; };
+  // eight waves where that leaves a block for each CU: two heads of a group, or 256 rows
+  int waves = 8, heads = a.group % 2 == 0 ? 2 : 1;
+  a.shift = heads == 2 ? 7 : 8;
+  if (tiles(a.shift) * (a.n_heads / heads) < device_cus()) waves = 4, heads = 1, a.shift = 7;
+  a.wpr = waves / heads;
+  a.tiles = (int)tiles(a.shift);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)a.tiles * (a.n_heads / heads))), dim3(64 * waves), 0, s, a);
+  };
+  if (sh.head_dim == 128) waves == 8 ? go(attention_fwd_kernel<128, 8>) : go(attention_fwd_kernel<128, 4>);
+  else waves == 8 ? go(attention_fwd_kernel<64, 8>) : go(attention_fwd_kernel<64, 4>);
   return launch_check("attention_forward");
 }
 

@@ -60,7 +60,7 @@ lora_status check_attn(const attn_shape* p, const char* what) {
   if (s.head_dim != 64 && s.head_dim != 128) return unsupported(what, "head_dim must be 64 or 128");
   const int64_t q = (int64_t)s.n_heads * s.head_dim, k = (int64_t)s.n_kv_heads * s.head_dim;
   for (int64_t st : {s.q_stride, s.k_stride, s.v_stride, s.o_stride})
-    LORA_ARG_CHECK(st % 8 == 0 && st < ((int64_t)1 << 31), "%s: stride %lld must be a multiple of 8 below 2^31",
+    LORA_ARG_CHECK(st % 8 == 0 && st < (1 << 24), "%s: stride %lld must be a multiple of 8 below 2^24",
                    what, (long long)st);
   LORA_ARG_CHECK(s.q_stride >= q && s.o_stride >= q && s.k_stride >= k && s.v_stride >= k,
                  "%s: a stride is shorter than its row", what);

@@ -29,7 +29,7 @@ def test_attention(L):  # noqa: F811
               (dict(n_heads=1026), E, b"1024"), (dict(head_dim=80), L.LORA_E_UNSUPPORTED, b"64 or 128"), (dict(head_dim=256), L.LORA_E_UNSUPPORTED, b"64 or 128"),
               (dict(scale=float("nan")), E, b"scale"), (dict(scale=float("inf")), E, b"scale"), (dict(causal=2), E, b"causal"),
               (dict(q_stride=255), E, b"multiple of 8"), (dict(q_stride=248), E, b"shorter"), (dict(k_stride=120), E, b"shorter"),
-              (dict(v_stride=-8), E, b"shorter"), (dict(o_stride=1 << 31), E, b"2^31"),
+              (dict(v_stride=-8), E, b"shorter"), (dict(o_stride=1 << 24), E, b"2^24"),
               (dict(n_q=(1 << 30) - 1, n_heads=1024, n_kv_heads=2), L.LORA_E_UNSUPPORTED, b"one launch")]
     for kw, kind, word in shapes:
         s = mk(**kw)
