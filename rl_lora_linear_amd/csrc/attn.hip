@@ -26,15 +26,13 @@
 namespace lora {
 
 constexpr float AT_LOG2E = 1.4426950408889634f, AT_LN2 = 0.6931471805599453f;
-constexpr int AT_WAVES = 4, AT_ROWS = 32 * AT_WAVES;   // rows of a block
-constexpr int AT_SHIFT = 7;                            // log2(AT_ROWS)
-constexpr int AT_TILE = 64;                            // rows of a tile in LDS
-static_assert(1 << AT_SHIFT == AT_ROWS);
+constexpr int AT_TILE = 64;   // rows of a tile in LDS
 
 struct AttnArgs {
   const uint16_t *q, *k, *v, *o, *dout;
   uint16_t *out, *dq, *dk, *dv;
-  float *lse, *delta;   // [heads][n_q]
+  float* lse;     // [heads][n_q]
+  float* stats;   // [heads][2][n_q]: lse in powers of two, delta; from the dq kernel for the other
   const int32_t *cu_q, *cu_k;
   int32_t* status;
   int64_t q_stride, k_stride, v_stride, o_stride, n_q, n_k;
@@ -50,8 +48,7 @@ struct AttnSeq {
   int64_t q0, k0;
   int lq, lk, tile;   // tile < 0: nothing to do
 };
-__device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_t* cu, int id,
-                                                 int shift = AT_SHIFT) {
+__device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_t* cu, int id, int shift) {
   const int lane = threadIdx.x & 63;
   const auto first = [&](int b) { return (cu[b] >> shift) + b; };
   int lo = 0, end = a.n_seqs;
@@ -94,35 +91,8 @@ __device__ __forceinline__ uint32_t at_lds(int r, int chunk) {
   return (uint32_t)(r * (D * 2) + ((chunk ^ at_swz<D>(r)) << 4));
 }
 
-// A tile of rows r0 .. r0 + AT_TILE - 1 of a [rows][D] matrix into LDS, zeros past `rows`.
-template <int D>
-__device__ __forceinline__ void stage_tile(char* dst, const uint16_t* src, int64_t stride, int r0, int rows) {
-  constexpr int CH = D / 8;
-#pragma unroll
-  for (int i = 0; i < AT_TILE * CH / (64 * AT_WAVES); ++i) {
-    const int j = i * 64 * AT_WAVES + threadIdx.x, r = j / CH, c = j % CH;
-    const uint4 x = r0 + r < rows ? *(const uint4*)(src + (int64_t)(r0 + r) * stride + c * 8) : make_uint4(0, 0, 0, 0);
-    *(uint4*)(dst + at_lds<D>(r, c)) = x;
-  }
-}
-
-// Operand of 32 rows, columns 16 kk .. 16 kk + 15.
-template <int D>
-__device__ __forceinline__ bf16x8 direct_op(const char* tile, int row0, int kk, int l, int h) {
-  return as_bf16x8(*(const uint4*)(tile + at_lds<D>(row0 + l, 2 * kk + h)));
-}
-// Transposed operand: columns 32 dt .. 32 dt + 31 as its rows, over rows row0 .. row0 + 15
-// in the order above.
-template <int D>
-__device__ __forceinline__ bf16x8 transposed_op(const char* tile, int row0, int dt, int lane) {
-  const int i = lane & 15, r = row0 + 4 * (lane >> 5) + (i >> 2);
-  const int c = dt * 4 + (lane >> 4 & 1) * 2 + ((i & 3) >> 1), lo = (i & 1) * 8;
-  const uint2 a = tr_read((const uint4*)tile, at_lds<D>(r, c) + lo);
-  const uint2 b = tr_read((const uint4*)tile, at_lds<D>(r + 8, c) + lo);
-  return as_bf16x8(make_uint4(a.x, a.y, b.x, b.y));
-}
-
-// The same from addresses worked out before: two rows' places in a tile.
+// A transposed operand: columns 32 dt .. 32 dt + 31 as its rows, over 16 rows in the order
+// above, by two transposing reads; where this lane's lie from the first row on.
 template <int D>
 __device__ __forceinline__ void transposed_at(uint32_t* at, int dt, int lane) {
   const int i = lane & 15, r = 4 * (lane >> 5) + (i >> 2);
@@ -143,16 +113,20 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 __device__ __forceinline__ void dma16(uint32_t voff, const void* base, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(voff), "s"(base) : "memory");
 }
-// Rows r0 .. r0 + AT_TILE - 1 of a [rows][D] matrix to LDS, by NW waves.  Rows past the end
+__device__ __forceinline__ void dma4_at(const void* p, uint32_t to) {   // 4 bytes a lane, each from its own address
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(p) : "memory");
+}
+// Rows r0 .. r0 + ROWS - 1 of a [rows][D] matrix to LDS, by NW waves.  Rows past the end
 // are copies of the last one: their weights are 0.
-template <int D, int NW>
+template <int D, int NW, int ROWS = AT_TILE>
 __device__ __forceinline__ void dma_tile(const uint16_t* src, int64_t stride, int r0, int rows, uint32_t to, int wave,
                                          int lane) {
-  constexpr int CH = D / 8, PER = 64 / CH, N = AT_TILE / PER / NW;   // rows of an instruction; instructions
+  constexpr int CH = D / 8, PER = 64 / CH, N = ROWS / PER;   // rows of an instruction; instructions
   const uint16_t* const base = src + r0 * stride;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int n = wave * N + j, r = n * PER + lane / CH;
+  for (int j = 0; j < (N + NW - 1) / NW; ++j) {
+    const int n = j * NW + wave, r = n * PER + lane / CH;
+    if (N % NW && n >= N) break;
     const uint32_t at = (uint32_t)min(r, rows - 1 - r0) * (uint32_t)(stride * 2) + (((lane % CH) ^ at_swz<D>(r)) << 4);
     dma16(at, base, to + n * 1024);
   }
@@ -190,6 +164,20 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
 __device__ __forceinline__ bool not_finite(bf16x8 x) {
   const uint4 u = __builtin_bit_cast(uint4, x);
   return (odd_halves(u.x) | odd_halves(u.y) | odd_halves(u.z) | odd_halves(u.w)) != 0;
+}
+
+// Whether what this lane fetched of a tile by dma_tile holds NaN or Inf.
+template <int D, int NW, int ROWS = AT_TILE>
+__device__ __forceinline__ bool dma_not_finite(const char* tile, int wave, int lane) {
+  constexpr int N = ROWS * D * 2 / 1024;
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < (N + NW - 1) / NW; ++j) {
+    const int n = j * NW + wave;
+    if (N % NW && n >= N) break;
+    odd |= not_finite(as_bf16x8(*(const uint4*)(tile + n * 1024 + lane * 16)));
+  }
+  return odd;
 }
 
 // acc += V^T P^T over 16 keys (key0 .. in the order above) where V may hold NaN or Inf:
@@ -232,6 +220,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
   constexpr int TILE = AT_TILE * D * 2;            // bytes of one operand of a stage
   __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
+  __shared__ int odd_tile[2];                      // of a stage: one more than the tile where v holds NaN or Inf
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 31, h = lane >> 5;
   if (blockIdx.x == 0) check_sequences(a);
@@ -270,6 +259,8 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
       qf[kk] = as_bf16x8(make_uint4((u.x ^ turn) & keep, (u.y ^ turn) & keep, (u.z ^ turn) & keep, (u.w ^ turn) & keep));
     }
   }
+  if (threadIdx.x < 2) odd_tile[threadIdx.x] = 0;
+  __syncthreads();
   if (tiles) stage(0, 0);
   f32x16 acc[ND];
 #pragma unroll
@@ -285,9 +276,8 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt) transposed_at<D>(va[dt], dt, lane);
 
-  const auto step = [&](int t, auto stage_c, auto masked_c) {
-    constexpr int K0 = decltype(stage_c)::value * 2 * TILE, V0 = K0 + TILE;
-    constexpr bool MASKED = decltype(masked_c)::value;
+  const auto step = [&](int t, auto st, auto masked) {   // masked: false_type, or whether to mask
+    const int K0 = st * 2 * TILE, V0 = K0 + TILE;
     const int t0 = t * AT_TILE;
     f32x16 x[2];
 #pragma unroll
@@ -298,7 +288,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
       for (int kk = 0; kk < NK; ++kk)
         x[u] = mfma32(as_bf16x8(*(const uint4*)(lds + K0 + u * 32 * D * 2 + ka[kk])), qf[kk], x[u]);
     }
-    if (MASKED) {
+    if (masked) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -326,13 +316,8 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
         x[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][r], c, -base));
         sum += x[u][r];
       }
-    if (MASKED) {
-      bool odd = false;
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) odd |= not_finite(transposed_pair(lds + V0 + b * 16 * D * 2, va[dt]));
-      if (__any(odd)) {
+    if (masked) {
+      if (__builtin_amdgcn_readfirstlane(odd_tile[st]) == t + 1) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const bf16x8 p = pack_op(x[b >> 1], b & 1);
@@ -350,18 +335,31 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
       for (int dt = 0; dt < ND; ++dt) acc[dt] = mfma32(transposed_pair(lds + V0 + b * 16 * D * 2, va[dt]), p, acc[dt]);
     }
   };
-  // tile t has landed for every wave, and every wave is done with the other stage
-  const auto turn = [&](int t, auto stage_c) {
+  // tile t has landed for every wave, and every wave is done with the other stage; where a
+  // tile is masked, each wave has looked through the part of v that it fetched
+  const auto arrive = [&](int t, int st, bool look) {
+    if (look) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (__any(dma_not_finite<D, NW>(lds + st * 2 * TILE + TILE, wave, lane))) odd_tile[st] = t + 1;
+    }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (t + 1 < tiles) stage(t + 1, 1 - decltype(stage_c)::value);
-    const int t0 = t * AT_TILE;
-    if (t0 > wave_last) return;
-    if (t0 + AT_TILE - 1 > wave_first || t0 + AT_TILE > s.lk) step(t, stage_c, std::true_type{});
-    else step(t, stage_c, std::false_type{});
+    if (t + 1 < tiles) stage(t + 1, 1 - st);
   };
-  for (int t = 0; t < tiles; t += 2) {
-    turn(t, std::integral_constant<int, 0>{});
-    if (t + 1 < tiles) turn(t + 1, std::integral_constant<int, 1>{});
+  // the tiles that no query of the block has to mask, in pairs; then the rest
+  const int whole = min(a.causal ? row0 + ahead + 1 : s.lk, s.lk);
+  const int pairs = max(whole, 0) / (2 * AT_TILE);
+  const bool on = w0 < s.lq;
+  int t = 0;
+  for (; t < 2 * pairs; t += 2) {
+    arrive(t, 0, false);
+    if (on) step(t, std::integral_constant<int, 0>{}, std::false_type{});
+    arrive(t + 1, 1, false);
+    if (on) step(t + 1, std::integral_constant<int, 1>{}, std::false_type{});
+  }
+  for (; t < tiles; ++t) {
+    arrive(t, t & 1, true);
+    const int t0 = t * AT_TILE;
+    if (t0 <= wave_last) step(t, t & 1, t0 + AT_TILE - 1 > wave_first || t0 + AT_TILE > s.lk);
   }
   if (i >= s.lq) return;
   sum += __shfl_xor(sum, 32, kWave);
@@ -370,23 +368,35 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- dq
-template <int D>
-__global__ __launch_bounds__(64 * AT_WAVES) void attention_dq_kernel(AttnArgs a) {
+// Waves, tiles and stages as in the forward.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW) void attention_dq_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
-  __shared__ uint4 lds[2 * AT_TILE * D / 8];
-  char *const kt = (char*)lds, *const vt = kt + AT_TILE * D * 2;
+  constexpr int TILE = AT_TILE * D * 2;
+  __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 31, h = lane >> 5;
   if (blockIdx.x == 0) check_sequences(a);
-  const int hx = blockIdx.x % a.n_heads, kvh = hx % a.n_kv, head = kvh * a.group + hx / a.n_kv;
-  const AttnSeq s = find_sequence(a, a.cu_q, a.tiles - 1 - blockIdx.x / a.n_heads);
+  const int per_block = NW / a.wpr, columns = a.n_heads / per_block;
+  const int hx = blockIdx.x % columns, kvh = hx % a.n_kv;
+  const int head = kvh * a.group + hx / a.n_kv * per_block + wave / a.wpr;
+  const AttnSeq s = find_sequence(a, a.cu_q, a.tiles - 1 - blockIdx.x / columns, a.shift);
   if (s.tile < 0) return;
-  const int row0 = s.tile * AT_ROWS, w0 = row0 + wave * 32, i = w0 + l;
+  const int row0 = s.tile << a.shift, w0 = row0 + wave % a.wpr * 32, i = w0 + l;
   const int ahead = s.lk - s.lq;
   const int last = a.causal ? min(i + ahead, s.lk - 1) : s.lk - 1;
-  const int wave_first = a.causal ? w0 + ahead : s.lk - 1, wave_last = a.causal ? min(w0 + 31 + ahead, s.lk - 1) : s.lk - 1;
-  const int keys = a.causal ? min(row0 + AT_ROWS + ahead, s.lk) : s.lk;
+  const int wave_first = a.causal ? w0 + ahead : s.lk - 1;
+  const int wave_last = w0 >= s.lq ? -1 : a.causal ? min(w0 + 31 + ahead, s.lk - 1) : s.lk - 1;
+  const int keys = a.causal ? min(row0 + (1 << a.shift) + ahead, s.lk) : s.lk;
+  const int tiles = keys > 0 ? (keys + AT_TILE - 1) / AT_TILE : 0;
 
+  const uint16_t* const kp = a.k + s.k0 * a.k_stride + kvh * D;
+  const uint16_t* const vp = a.v + s.k0 * a.v_stride + kvh * D;
+  const uint32_t lds0 = lds_offset(lds);
+  const auto stage = [&](int t, int st) {
+    dma_tile<D, NW>(kp, a.k_stride, t * AT_TILE, s.lk, lds0 + st * 2 * TILE, wave, lane);
+    dma_tile<D, NW>(vp, a.v_stride, t * AT_TILE, s.lk, lds0 + st * 2 * TILE + TILE, wave, lane);
+  };
   const int64_t row = s.q0 + min(i, s.lq - 1);
   bf16x8 qf[NK], df[NK];
   load_rows<D>(qf, a.q + row * a.q_stride + head * D, h);
@@ -402,130 +412,186 @@ __global__ __launch_bounds__(64 * AT_WAVES) void attention_dq_kernel(AttnArgs a)
     delta += __shfl_xor(delta, 32, kWave);
   }
   const float lse = a.lse[head * a.n_q + row] * AT_LOG2E;
-  if (i < s.lq && h == 0) a.delta[head * a.n_q + row] = delta;
+  if (i < s.lq) a.stats[((int64_t)head * 2 + h) * a.n_q + row] = h ? delta : lse;
+  if (tiles) stage(0, 0);
   f32x16 acc[ND];
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[dt][r] = 0.f;
-  const uint16_t* const kp = a.k + s.k0 * a.k_stride + kvh * D;
-  const uint16_t* const vp = a.v + s.k0 * a.v_stride + kvh * D;
 
-  for (int t0 = 0; t0 < keys; t0 += AT_TILE) {
-    __syncthreads();
-    stage_tile<D>(kt, kp, a.k_stride, t0, s.lk);
-    stage_tile<D>(vt, vp, a.v_stride, t0, s.lk);
-    __syncthreads();
-    if (t0 > wave_last || w0 >= s.lq) continue;
-    const bool masked = t0 + AT_TILE - 1 > wave_first || t0 + AT_TILE > s.lk;
+  uint32_t ka[NK], ta[ND][2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+  for (int kk = 0; kk < NK; ++kk) ka[kk] = at_lds<D>(l, 2 * kk + h);
+#pragma unroll
+  for (int dt = 0; dt < ND; ++dt) transposed_at<D>(ta[dt], dt, lane);
+
+  const auto step = [&](int t, auto st, auto masked) {   // masked: false_type, or whether to mask
+    const int K0 = st * 2 * TILE, V0 = K0 + TILE;
+    const int t0 = t * AT_TILE;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
       f32x16 x, y;
 #pragma unroll
       for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < NK; ++kk) {
-        x = mfma32(direct_op<D>(kt, t * 32, kk, l, h), qf[kk], x);
-        y = mfma32(direct_op<D>(vt, t * 32, kk, l, h), df[kk], y);
-      }
+      for (int kk = 0; kk < NK; ++kk) x = mfma32(as_bf16x8(*(const uint4*)(lds + K0 + u * 32 * D * 2 + ka[kk])), qf[kk], x);
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) y = mfma32(as_bf16x8(*(const uint4*)(lds + V0 + u * 32 * D * 2 + ka[kk])), df[kk], y);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(x[r] * a.scale_log2 - lse);
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], a.scale_log2, -lse));
         x[r] = p * (y[r] - delta);
-        if (masked && t0 + t * 32 + result_row(r, h) > last) x[r] = 0.f;
+      }
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (t0 + u * 32 + result_row(r, h) > last) x[r] = 0.f;
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const bf16x8 ds = pack_op(x, b);
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt) acc[dt] = mfma32(transposed_op<D>(kt, t * 32 + b * 16, dt, lane), ds, acc[dt]);
+        for (int dt = 0; dt < ND; ++dt)
+          acc[dt] = mfma32(transposed_pair(lds + K0 + (u * 32 + b * 16) * D * 2, ta[dt]), ds, acc[dt]);
       }
     }
+  };
+  // tile t has landed for every wave, and every wave is done with the other stage
+  const auto arrive = [&](int t, int st) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (t + 1 < tiles) stage(t + 1, 1 - st);
+  };
+  // the tiles that no query of the block has to mask, in pairs; then the rest
+  const int whole = min(a.causal ? row0 + ahead + 1 : s.lk, s.lk);
+  const int pairs = max(whole, 0) / (2 * AT_TILE);
+  const bool on = w0 < s.lq;
+  int t = 0;
+  for (; t < 2 * pairs; t += 2) {
+    arrive(t, 0);
+    if (on) step(t, std::integral_constant<int, 0>{}, std::false_type{});
+    arrive(t + 1, 1);
+    if (on) step(t + 1, std::integral_constant<int, 1>{}, std::false_type{});
+  }
+  for (; t < tiles; ++t) {
+    arrive(t, t & 1);
+    const int t0 = t * AT_TILE;
+    if (t0 <= wave_last) step(t, t & 1, t0 + AT_TILE - 1 > wave_first || t0 + AT_TILE > s.lk);
   }
   if (i < s.lq) store_row<D>(a.dq + (s.q0 + i) * a.q_stride + head * D, acc, a.scale, h);
 }
 
 // ---------------------------------------------------------------- dk, dv
-template <int D>
-__global__ __launch_bounds__(64 * AT_WAVES) void attention_dkv_kernel(AttnArgs a) {
+// A wave owns 32 keys, NW waves 32 NW of them in a row; tiles of 32 queries and of their
+// dout pass, head by head of the group, with their lse and delta.
+constexpr int DKV_TILE = 32;
+
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW) void attention_dkv_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
-  __shared__ uint4 lds[2 * AT_TILE * D / 8];
-  __shared__ __attribute__((aligned(16))) float lse_s[AT_TILE], delta_s[AT_TILE];
-  char *const qt = (char*)lds, *const dt_ = qt + AT_TILE * D * 2;
+  constexpr int TILE = DKV_TILE * D * 2;
+  __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
+  __shared__ __attribute__((aligned(16))) float stats[2][2][DKV_TILE];   // of a stage: lse in powers of two, delta
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 31, h = lane >> 5;
   const int kvh = blockIdx.x % a.n_kv;
   // the first keys are seen by the most queries
-  const AttnSeq s = find_sequence(a, a.cu_k, blockIdx.x / a.n_kv);
+  const AttnSeq s = find_sequence(a, a.cu_k, blockIdx.x / a.n_kv, a.shift);
   if (s.tile < 0) return;
-  const int row0 = s.tile * AT_ROWS, w0 = row0 + wave * 32, j = w0 + l;   // key row
+  const int row0 = s.tile << a.shift, w0 = row0 + wave * 32, j = w0 + l;   // key row
   const int ahead = s.lk - s.lq;
-  // the first query that sees this lane's key, one of the wave's, one of the block's
+  // the first query that sees this lane's key, one of the wave's, all of the wave's
   const int first = a.causal ? j - ahead : 0;
-  const int wave_first = a.causal ? w0 - ahead : 0, wave_all = a.causal ? w0 + 31 - ahead : 0;
-  const int begin = a.causal ? max(row0 - ahead, 0) / AT_TILE * AT_TILE : 0;
+  const int wave_first = w0 >= s.lk ? 1 << 30 : a.causal ? w0 - ahead : 0, wave_all = a.causal ? w0 + 31 - ahead : 0;
+  const int begin = a.causal ? max(row0 - ahead, 0) / DKV_TILE : 0;
+  const int per_head = max((s.lq + DKV_TILE - 1) / DKV_TILE - begin, 0), tiles = per_head * a.group;
 
+  const uint32_t lds0 = lds_offset(lds), stats0 = lds_offset(stats);
+  // the next tile to be asked for: its head and its place in the head
+  int ask_head = kvh * a.group, ask_t = begin;
+  const auto stage = [&](int st) {
+    const int t0 = ask_t * DKV_TILE;
+    dma_tile<D, NW, DKV_TILE>(a.q + s.q0 * a.q_stride + ask_head * D, a.q_stride, t0, s.lq, lds0 + st * 2 * TILE, wave, lane);
+    dma_tile<D, NW, DKV_TILE>(a.dout + s.q0 * a.o_stride + ask_head * D, a.o_stride, t0, s.lq, lds0 + st * 2 * TILE + TILE, wave, lane);
+    if (wave == 0)   // the lower lanes fetch the tile's lse, the upper ones its delta
+      dma4_at(a.stats + ((int64_t)ask_head * 2 + h) * a.n_q + s.q0 + min(t0 + l, s.lq - 1), stats0 + st * (int)sizeof(stats[0]));
+    if (++ask_t == begin + per_head) ask_t = begin, ++ask_head;
+  };
   bf16x8 kf[NK], vf[NK];
   const int64_t row = s.k0 + min(j, s.lk - 1);
   load_rows<D>(kf, a.k + row * a.k_stride + kvh * D, h);
   load_rows<D>(vf, a.v + row * a.v_stride + kvh * D, h);
+  if (tiles) stage(0);
   f32x16 dk[ND], dv[ND];
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dk[dt][r] = dv[dt][r] = 0.f;
+  uint32_t ka[NK], ta[ND][2];
+#pragma unroll
+  for (int kk = 0; kk < NK; ++kk) ka[kk] = at_lds<D>(l, 2 * kk + h);
+#pragma unroll
+  for (int dt = 0; dt < ND; ++dt) transposed_at<D>(ta[dt], dt, lane);
 
-  for (int gh = 0; gh < a.group; ++gh) {
-    const int head = kvh * a.group + gh;
-    const uint16_t* const qp = a.q + s.q0 * a.q_stride + head * D;
-    const uint16_t* const dp = a.dout + s.q0 * a.o_stride + head * D;
-    for (int t0 = begin; t0 < s.lq; t0 += AT_TILE) {
-      __syncthreads();
-      stage_tile<D>(qt, qp, a.q_stride, t0, s.lq);
-      stage_tile<D>(dt_, dp, a.o_stride, t0, s.lq);
-      if (threadIdx.x < AT_TILE) {
-        const bool in = t0 + (int)threadIdx.x < s.lq;
-        const int64_t at = head * a.n_q + s.q0 + t0 + threadIdx.x;
-        // rows that do not exist, and queries that see no key, weigh 0
-        const float v = in ? a.lse[at] : INFINITY;
-        lse_s[threadIdx.x] = v == -INFINITY ? INFINITY : v * AT_LOG2E;
-        delta_s[threadIdx.x] = in ? a.delta[at] : 0.f;
-      }
-      __syncthreads();
-      if (t0 + AT_TILE - 1 < wave_first || w0 >= s.lk) continue;
-      const bool masked = t0 < wave_all;
+  const auto step = [&](int t0, auto stage_c, const bool masked) {
+    constexpr int ST = decltype(stage_c)::value, Q0 = ST * 2 * TILE, G0 = Q0 + TILE;
+    f32x16 x, y;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x16 x, y;
+    for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.f;
+    for (int kk = 0; kk < NK; ++kk) x = mfma32(as_bf16x8(*(const uint4*)(lds + Q0 + ka[kk])), kf[kk], x);
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) {
-          x = mfma32(direct_op<D>(qt, t * 32, kk, l, h), kf[kk], x);
-          y = mfma32(direct_op<D>(dt_, t * 32, kk, l, h), vf[kk], y);
-        }
+    for (int kk = 0; kk < NK; ++kk) y = mfma32(as_bf16x8(*(const uint4*)(lds + G0 + ka[kk])), vf[kk], y);
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const f32x4 ls = *(const f32x4*)(lse_s + t * 32 + 8 * r4 + 4 * h), de = *(const f32x4*)(delta_s + t * 32 + 8 * r4 + 4 * h);
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const f32x4 ls = *(const f32x4*)&stats[ST][0][8 * r4 + 4 * h];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int r = r4 * 4 + c;
-            x[r] = __builtin_amdgcn_exp2f(x[r] * a.scale_log2 - ls[c]);
-            y[r] = x[r] * (y[r] - de[c]);
-            if (masked && t0 + t * 32 + result_row(r, h) < first) x[r] = y[r] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const bf16x8 p = pack_op(x, b), ds = pack_op(y, b);
-#pragma unroll
-          for (int dt = 0; dt < ND; ++dt) {
-            dv[dt] = mfma32(transposed_op<D>(dt_, t * 32 + b * 16, dt, lane), p, dv[dt]);
-            dk[dt] = mfma32(transposed_op<D>(qt, t * 32 + b * 16, dt, lane), ds, dk[dt]);
-          }
-        }
+      for (int c = 0; c < 4; ++c) {
+        const int r = r4 * 4 + c;
+        x[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], a.scale_log2, -ls[c]));
       }
     }
+    if (masked) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int q = t0 + result_row(r, h);
+        if (q < first || q >= s.lq) x[r] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const bf16x8 p = pack_op(x, b);
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) dv[dt] = mfma32(transposed_pair(lds + G0 + b * 16 * D * 2, ta[dt]), p, dv[dt]);
+    }
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const f32x4 de = *(const f32x4*)&stats[ST][1][8 * r4 + 4 * h];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int r = r4 * 4 + c;
+        y[r] = x[r] * (y[r] - de[c]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const bf16x8 ds = pack_op(y, b);
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) dk[dt] = mfma32(transposed_pair(lds + Q0 + b * 16 * D * 2, ta[dt]), ds, dk[dt]);
+    }
+  };
+  int at_t = begin;
+  const auto turn = [&](int n, auto stage_c) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (n + 1 < tiles) stage(1 - decltype(stage_c)::value);
+    const int t0 = at_t * DKV_TILE;
+    if (++at_t == begin + per_head) at_t = begin;
+    if (t0 + DKV_TILE - 1 < wave_first) return;
+    step(t0, stage_c, t0 < wave_all || t0 + DKV_TILE > s.lq);
+  };
+  for (int n = 0; n < tiles; n += 2) {
+    turn(n, std::integral_constant<int, 0>{});
+    if (n + 1 < tiles) turn(n + 1, std::integral_constant<int, 1>{});
   }
   if (j >= s.lk) return;
   store_row<D>(a.dk + (s.k0 + j) * a.k_stride + kvh * D, dk, a.scale, h);
@@ -543,32 +609,39 @@ static AttnArgs attn_args(const attn_shape& sh, const uint16_t* q, const uint16_
                           const int32_t* cu_q, const int32_t* cu_k, void* ws) {
   AttnArgs a{};
   a.q = q, a.k = k, a.v = v, a.cu_q = cu_q, a.cu_k = cu_k, a.status = (int32_t*)ws;
-  a.delta = (float*)((char*)ws + 256);
+  a.stats = (float*)((char*)ws + 256);
   a.q_stride = sh.q_stride, a.k_stride = sh.k_stride, a.v_stride = sh.v_stride, a.o_stride = sh.o_stride;
   a.n_q = sh.n_q, a.n_k = sh.n_k, a.n_seqs = sh.n_seqs, a.n_heads = sh.n_heads, a.n_kv = sh.n_kv_heads;
   a.group = sh.n_heads / sh.n_kv_heads, a.causal = sh.causal;
   a.scale = sh.scale, a.scale_log2 = sh.scale * AT_LOG2E;
   return a;
 }
-static int attn_tiles(int64_t n, int n_seqs) { return (int)(n / AT_ROWS) + n_seqs; }
+
+// The blocks of the kernels whose waves own queries: eight waves (two heads of a group by
+// 128 rows, or 256 rows) where that leaves a block for each CU, else four.
+struct QueryGrid {
+  dim3 blocks;
+  int waves;
+};
+static QueryGrid query_grid(AttnArgs& a, const attn_shape& sh) {
+  const auto tiles = [&](int shift) { return (sh.n_q >> shift) + sh.n_seqs; };
+  int waves = 8, heads = a.group % 2 == 0 ? 2 : 1;
+  a.shift = heads == 2 ? 7 : 8;
+  if (tiles(a.shift) * (a.n_heads / heads) < device_cus()) waves = 4, heads = 1, a.shift = 7;
+  a.wpr = waves / heads;
+  a.tiles = (int)tiles(a.shift);
+  return {dim3((unsigned)((int64_t)a.tiles * (a.n_heads / heads))), waves};
+}
 
 lora_status launch_attention_fwd(const attn_shape& sh, const uint16_t* q, const uint16_t* k,
                                  const uint16_t* v, const int32_t* cu_q, const int32_t* cu_k,
                                  uint16_t* o, float* lse, void* ws, hipStream_t s) {
   AttnArgs a = attn_args(sh, q, k, v, cu_q, cu_k, ws);
   a.out = o, a.lse = lse;
-  const auto tiles = [&](int shift) { return (sh.n_q >> shift) + sh.n_seqs; };
-  // eight waves where that leaves a block for each CU: two heads of a group, or 256 rows
-  int waves = 8, heads = a.group % 2 == 0 ? 2 : 1;
-  a.shift = heads == 2 ? 7 : 8;
-  if (tiles(a.shift) * (a.n_heads / heads) < device_cus()) waves = 4, heads = 1, a.shift = 7;
-  a.wpr = waves / heads;
-  a.tiles = (int)tiles(a.shift);
-  const auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)a.tiles * (a.n_heads / heads))), dim3(64 * waves), 0, s, a);
-  };
-  if (sh.head_dim == 128) waves == 8 ? go(attention_fwd_kernel<128, 8>) : go(attention_fwd_kernel<128, 4>);
-  else waves == 8 ? go(attention_fwd_kernel<64, 8>) : go(attention_fwd_kernel<64, 4>);
+  const QueryGrid g = query_grid(a, sh);
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g.blocks, dim3(64 * g.waves), 0, s, a); };
+  if (sh.head_dim == 128) g.waves == 8 ? go(attention_fwd_kernel<128, 8>) : go(attention_fwd_kernel<128, 4>);
+  else g.waves == 8 ? go(attention_fwd_kernel<64, 8>) : go(attention_fwd_kernel<64, 4>);
   return launch_check("attention_forward");
 }
 
@@ -578,17 +651,18 @@ lora_status launch_attention_bwd(const attn_shape& sh, const uint16_t* dout, con
                                  uint16_t* dq, uint16_t* dk, uint16_t* dv, void* ws, hipStream_t s) {
   AttnArgs a = attn_args(sh, q, k, v, cu_q, cu_k, ws);
   a.dout = dout, a.o = o, a.lse = const_cast<float*>(lse), a.dq = dq, a.dk = dk, a.dv = dv;
-  a.tiles = attn_tiles(sh.n_q, sh.n_seqs);
-  const dim3 block(64 * AT_WAVES), grid_q((unsigned)((int64_t)a.tiles * a.n_heads));
   // dq first: it also leaves delta for the other kernel
-  if (sh.head_dim == 128) hipLaunchKernelGGL(attention_dq_kernel<128>, grid_q, block, 0, s, a);
-  else hipLaunchKernelGGL(attention_dq_kernel<64>, grid_q, block, 0, s, a);
+  const QueryGrid g = query_grid(a, sh);
+  const auto go_q = [&](auto kernel) { hipLaunchKernelGGL(kernel, g.blocks, dim3(64 * g.waves), 0, s, a); };
+  if (sh.head_dim == 128) g.waves == 8 ? go_q(attention_dq_kernel<128, 8>) : go_q(attention_dq_kernel<128, 4>);
+  else g.waves == 8 ? go_q(attention_dq_kernel<64, 8>) : go_q(attention_dq_kernel<64, 4>);
   lora_status st = launch_check("attention_backward dq");
   if (st != LORA_OK) return st;
-  a.tiles = attn_tiles(sh.n_k, sh.n_seqs);
-  const dim3 grid_k((unsigned)((int64_t)a.tiles * a.n_kv));
-  if (sh.head_dim == 128) hipLaunchKernelGGL(attention_dkv_kernel<128>, grid_k, block, 0, s, a);
-  else hipLaunchKernelGGL(attention_dkv_kernel<64>, grid_k, block, 0, s, a);
+  a.shift = 7;
+  a.tiles = (int)((sh.n_k >> a.shift) + sh.n_seqs);
+  const dim3 grid((unsigned)((int64_t)a.tiles * a.n_kv)), block(256);
+  if (sh.head_dim == 128) hipLaunchKernelGGL((attention_dkv_kernel<128, 4>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((attention_dkv_kernel<64, 4>), grid, block, 0, s, a);
   return launch_check("attention_backward dk, dv");
 }
 

@@ -79,7 +79,7 @@ lora_status check_ws(const void* ws, size_t have, size_t need, const char* what)
   return LORA_OK;
 }
 
-size_t attn_ws(const attn_shape& s) { return 256 + (size_t)s.n_heads * s.n_q * sizeof(float); }
+size_t attn_ws(const attn_shape& s) { return 256 + (size_t)s.n_heads * s.n_q * 2 * sizeof(float); }
 
 lora_status check_kv(const kv_shape* p, const char* what) {
   LORA_ARG_CHECK(p != nullptr, "%s: shape is NULL", what);
