@@ -786,8 +786,8 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
  *   o    bf16 [n_seqs][n_heads][head_dim] out, must not overlap q
  *   lse  fp32 [n_seqs][n_heads] out, nullable
  * Products and sums are fp32, the weights exp(.) enter the second product as bf16; keys
- * and values in 8 bits enter as bf16, as the 8-bit x of w4_linear does: exactly, but for
- * scale bytes under 3 and magnitudes of 2^128 or more.  What a page holds behind a
+ * and values in 8 bits enter as bf16, as the 8-bit x of w4_linear does: exactly for scale
+ * bytes from 3 on and magnitudes under 2^128 (scale bytes 0 and 255 are not used).  What a page holds behind a
  * request's last row is never used.  The
  * length is split and joined by rules on the request's own length: its results have the
  * same bits in every batch.  n_heads a multiple of n_kv_heads, <= 1024.

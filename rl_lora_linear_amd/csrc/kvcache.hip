@@ -1,5 +1,7 @@
 // The paged key-value cache on gfx950: block tables and slot maps from request lengths,
 // new rows into the pages, and the attention of one new token of each request.
+#include <cmath>
+
 #include "attn.hpp"
 #include "q8.hpp"
 
@@ -253,11 +255,9 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
 }
 
 // ---------------------------------------------------------------- one token of each request
-// A block takes one split of a request's length for one key head (and up to 16 of its
-// query heads: the columns of a 16x16x32 matrix instruction, so a group of any size costs
-// one pass over the cache).  Its four waves take the split's tiles of 32 keys in turn,
-// each with its own running maximum, sum and output, and join at the end; the splits of
-// a request are joined by a second kernel.
+// A block takes a run of a request's keys for one key head (and up to 16 of its query
+// heads: the columns of a 16x16x32 matrix instruction, so a group of any size costs one
+// pass over the cache).  Its four waves take tiles of 32 keys in turn.
 //   S^T = K Q^T: lane (l, g) = (lane & 15, lane >> 4) holds key l's chunk as operand and
 //   ends with column (query head) l, keys 4g .. 4g+3 of the 16;
 //   O^T += V^T P^T: those are the operand of P as they lie, where the instruction's key
@@ -265,14 +265,40 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
 //   operand for the same order comes from LDS by transposing reads.
 // So nothing but the maximum and the sum crosses lanes, and each lane rescales the output
 // of its own query head.
-constexpr int DEC_WAVES = 4, DEC_TILE = 32, DEC_MIN_SPLIT = 128, DEC_MAX_SPLITS = 32;
+//
+// Where the length is cut must not show in the result, or a request's bits would change
+// with the batch.  So the sums have one shape, by the request's length alone: units of
+// DEC_UNIT keys (more where that makes more than 32 of them), in which each wave keeps a
+// running maximum, sum and output and the four are added; and the units' results
+// (maximum, sum, output) joined two by two, neighbours first, as the leaves of a binary
+// tree.  A block takes an aligned run of 2^k units, a subtree, whatever k suits the batch;
+// what is left of the tree is joined by a second kernel.
+constexpr int DEC_WAVES = 4, DEC_TILE = 32, DEC_STRIPE = DEC_WAVES * DEC_TILE, DEC_UNIT = 128, DEC_MAX_UNITS = 32;
+constexpr float DEC_SLACK = 6.f;
+constexpr int DEC_MAX_SPAN = 8;      // units of a block at most, as many as leave
+constexpr int64_t DEC_BLOCKS = 3000;  // this many blocks
 
-// The split's length for a request of `len` keys: a power of two, so that a request has
-// at most 32 splits; by its own length alone.
-__host__ __device__ __forceinline__ int decode_split(int len) {
-  int s = DEC_MIN_SPLIT;
-  while ((int64_t)s * DEC_MAX_SPLITS < len) s *= 2;
+__host__ __device__ __forceinline__ int decode_unit(int len) {
+  int s = DEC_UNIT;
+  while ((int64_t)s * DEC_MAX_UNITS < len) s *= 2;
   return s;
+}
+
+// A piece of the result: four columns of an output, with its row's maximum (in powers of
+// two) and sum, relative to which it stands.
+struct DecNode {
+  f32x4 o;
+  float m, sum;
+};
+__device__ __forceinline__ DecNode dec_join(const DecNode& x, const DecNode& y) {
+  const float m = fmaxf(x.m, y.m), ref = m == -INFINITY ? 0.f : m;
+  const float a = __builtin_amdgcn_exp2f(x.m - ref), b = __builtin_amdgcn_exp2f(y.m - ref);
+  DecNode r;
+  r.m = m;
+  r.sum = __builtin_fmaf(x.sum, a, y.sum * b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.o[i] = __builtin_fmaf(x.o[i], a, y.o[i] * b);
+  return r;
 }
 
 struct DecodeArgs {
@@ -282,13 +308,21 @@ struct DecodeArgs {
   const int32_t *table, *lens;
   uint16_t* o;
   float* lse;
-  float* part;       // [n][heads][splits][D] outputs over their sums
-  float2* stat;      // [n][heads][splits] (maximum in powers of two, sum)
+  float* part;       // [n][heads][nodes][D] outputs of the blocks' runs
+  float2* stat;      // [n][heads][nodes] their maxima and sums
   int32_t* status;
   int64_t q_stride;
-  int32_t n_heads, n_kv, group, page_shift, n_pages, max_pages, max_len, splits, col_groups;
+  int32_t n_heads, n_kv, group, page_shift, n_pages, max_pages, max_len, nodes, span, col_groups;
   float scale_log2;
+  uint32_t q_turn, q_keep;
 };
+
+// Four columns from c on of a row's output, and with the first its lse.
+__device__ __forceinline__ void dec_store(const DecodeArgs& a, int64_t row, int D, int c, const DecNode& v) {
+  const float mul = v.sum == 0.f ? 0.f : 1.f / v.sum;
+  *(uint2*)(a.o + row * D + c) = make_uint2(pack2bf(v.o[0] * mul, v.o[1] * mul), pack2bf(v.o[2] * mul, v.o[3] * mul));
+  if (a.lse && c == 0) a.lse[row] = v.sum == 0.f ? -INFINITY : (v.m + __log2f(v.sum)) * KV_LN2;
+}
 
 __device__ __forceinline__ bf16x8 kv_widen(uint32_t lo, uint32_t hi, float scale) {
   uint32_t r[4];
@@ -307,121 +341,193 @@ __device__ __forceinline__ uint32_t dec_v_at(int row, int chunk) {
   return (uint32_t)(row * (D * 2) + ((chunk ^ s) << 4));
 }
 
+// What a wave holds of a tile on its way: the lane's pieces of K as operands, and of V as
+// they go to LDS.  In 8 bits a piece is 16 codes, and its scale rides along.
 template <int D, bool X8>
-__global__ __launch_bounds__(64 * DEC_WAVES) void decode_kernel(DecodeArgs a) {
+struct DecTile {
+  static constexpr int KP = D / (X8 ? 64 : 32);                 // pieces of a key row per lane
+  static constexpr int VP = DEC_TILE * D * (X8 ? 1 : 2) / 1024; // pieces of the V rows per lane
+  uint4 k[2][KP], v[VP];
+  uint32_t ks[X8 ? 2 : 1], vs[X8 ? VP : 1];
+  int n[2];   // keys that exist among the first 16 and the second 16
+};
+
+// The pages of a tile's two halves (a page holds 16 rows at least, so a half lies in one);
+// asked for a tile ahead of its rows.
+struct DecPages {
+  int32_t p[2];
+};
+__device__ __forceinline__ DecPages dec_pages(const DecodeArgs& a, const int32_t* table, int t0, int k1) {
+  DecPages r{{0, 0}};
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    if (t0 + 16 * t < k1) r.p[t] = table[(t0 + 16 * t) >> a.page_shift];
+  return r;
+}
+
+// Asks for all rows of tile t0.  Rows behind the request's last one lie in its last page and
+// are fetched like the others; for a half that has no page, rows of page 0 are.
+template <int D, bool X8>
+__device__ __forceinline__ void dec_ask(const DecodeArgs& a, DecPages pages, int kvh, int t0, int k1, int lane,
+                                        DecTile<D, X8>& x, bool& bad) {
+  using T = DecTile<D, X8>;
+  constexpr int ROW = D * (X8 ? 1 : 2);
+  const int l = lane & 15, g = lane >> 4;
+  int64_t row[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int key = t0 + 16 * t;
+    x.n[t] = min(max(k1 - key, 0), 16);
+    uint32_t page = 0;
+    if (x.n[t]) {
+      page = (uint32_t)__builtin_amdgcn_readfirstlane(pages.p[t]);
+      if (page >= (uint32_t)a.n_pages) bad = true, x.n[t] = 0, page = 0;
+    }
+    row[t] = (((int64_t)page * a.n_kv + kvh) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const char* const at = (const char*)a.kc + row[t] * ROW;
+#pragma unroll
+    for (int i = 0; i < T::KP; ++i) x.k[t][i] = *(const uint4*)(at + (uint32_t)(l * ROW + i * 64 + g * 16));
+    if (X8) {
+      const uint8_t* const sc = a.ks + row[t] * (D / 32) + (uint32_t)(l * (D / 32));
+      x.ks[t] = D == 128 ? *(const uint32_t*)sc : *(const uint16_t*)sc;
+    }
+  }
+  constexpr int LPR = ROW / 16, PER = 64 / LPR;    // lanes of a row, rows of an instruction
+#pragma unroll
+  for (int i = 0; i < T::VP; ++i) {
+    const int r = i * PER % 16;                    // first row within its half
+    const int64_t r0 = row[i * PER / 16] + r;
+    x.v[i] = *(const uint4*)((const char*)a.vc + r0 * ROW + (uint32_t)(lane * 16));
+    if (X8) x.vs[i] = *(a.vs + r0 * (D / 32) + (uint32_t)(lane >> 1));
+  }
+}
+
+// ITEMS: pieces of the result per thread (1: up to 8 heads of 128 columns).
+template <int D, bool X8, int ITEMS>
+__global__ __launch_bounds__(64 * DEC_WAVES, X8 ? 3 : 2) void decode_kernel(DecodeArgs a) {
+  using T = DecTile<D, X8>;
   constexpr int NK = D / 32;            // steps of 32 columns
   constexpr int ND = D / 16;            // output tiles of 16 columns
   constexpr int V_BYTES = DEC_TILE * D * 2;
   __shared__ uint4 lds[DEC_WAVES * V_BYTES / 16];
+  __shared__ float2 ms[DEC_WAVES][16];
+  __shared__ f32x4 left_o[3][ITEMS][64 * DEC_WAVES];    // of a subtree that waits for its neighbour: the thread's own
+  __shared__ float2 left_ms[3][ITEMS][64 * DEC_WAVES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 15, g = lane >> 4;
   const int heads_at = blockIdx.x % (a.n_kv * a.col_groups);
   const int rest = blockIdx.x / (a.n_kv * a.col_groups);
-  const int split = rest % a.splits, b = rest / a.splits;
+  const int node = rest % a.nodes, b = rest / a.nodes;
   const int kvh = heads_at / a.col_groups, cols0 = heads_at % a.col_groups * 16;
   const int cols = min(16, a.group - cols0);
   int len = a.lens[b];
   if ((uint32_t)len > (uint32_t)a.max_len) {
-    if (split == 0 && heads_at == 0 && threadIdx.x == 0) set_flag(a.status, LORA_FLAG_BAD_LENGTH);
+    if (node == 0 && heads_at == 0 && threadIdx.x == 0) set_flag(a.status, LORA_FLAG_BAD_LENGTH);
     len = 0;
   }
-  const int per = decode_split(len);
-  const int k0 = split * per, k1 = min(k0 + per, len);
-  if (k0 >= len && split > 0) return;   // split 0 also writes a request without keys
-  const bool only = len <= per;
+  const int unit = decode_unit(len), run = unit * a.span;
+  const int k0 = node * run, k1 = min(k0 + run, len);
+  if (k0 >= len && node > 0) return;   // the first also writes a request without keys
+  const bool only = len <= run;
 
   // Q as operand: lane (l, g) holds 8 columns of query head l for each step.  In 8 bits
-  // a lane loads 16 codes at once, the columns of two steps.
+  // a lane's 16 codes are the columns of two steps.
   const auto col_of = [&](int kk) { return X8 ? (kk >> 1) * 64 + g * 16 + (kk & 1) * 8 : kk * 32 + g * 8; };
   bf16x8 qf[NK];
   const int head0 = kvh * a.group + cols0;
+  // a negative scale turns q's signs, a scale of 0 makes q 0 (scale_log2 is positive)
 #pragma unroll
-  for (int kk = 0; kk < NK; ++kk)
-    qf[kk] = as_bf16x8(l < cols ? *(const uint4*)(a.q + b * a.q_stride + (int64_t)(head0 + l) * D + col_of(kk))
-                                : make_uint4(0, 0, 0, 0));
+  for (int kk = 0; kk < NK; ++kk) {
+    const uint4 u = l < cols ? *(const uint4*)(a.q + b * a.q_stride + (int64_t)(head0 + l) * D + col_of(kk)) : make_uint4(0, 0, 0, 0);
+    qf[kk] = as_bf16x8(make_uint4((u.x ^ a.q_turn) & a.q_keep, (u.y ^ a.q_turn) & a.q_keep, (u.z ^ a.q_turn) & a.q_keep,
+                                  (u.w ^ a.q_turn) & a.q_keep));
+  }
+  const int32_t* const table = a.table + (int64_t)b * a.max_pages;
+  bool bad = false;
+  T x;
+  const int first = k0 + wave * DEC_TILE;
+  dec_ask<D, X8>(a, dec_pages(a, table, first, k1), kvh, first, k1, lane, x, bad);
+  DecPages pages = dec_pages(a, table, first + DEC_STRIPE, k1);
 
   f32x4 acc[ND];
 #pragma unroll
   for (int i = 0; i < ND; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, sum = 0.f;
   char* const vl = (char*)lds + wave * V_BYTES;
-  const int32_t* const table = a.table + (int64_t)b * a.max_pages;
-  const int page_mask = (1 << a.page_shift) - 1;
-  bool bad = false;
 
-  // a row of the cache: its index in rows, or -1 where there is none
-  const auto row_of = [&](int key) -> int64_t {
-    if (key >= k1) return -1;
-    const int32_t page = table[key >> a.page_shift];
-    if ((uint32_t)page >= (uint32_t)a.n_pages) {
-      bad = true;
-      return -1;
-    }
-    return (((int64_t)page * a.n_kv + kvh) << a.page_shift) + (key & page_mask);
-  };
-
-  for (int t0 = k0 + wave * DEC_TILE; t0 < k1; t0 += DEC_WAVES * DEC_TILE) {
+  const auto tile = [&](int t0) {
     // ---- scores of 32 keys
     f32x4 s[2];
-    bool live[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t row = row_of(t0 + t * 16 + l);
-      live[t] = row >= 0;
       s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (X8) {
-        const uint8_t* kr = (const uint8_t*)a.kc + row * D;
 #pragma unroll
-        for (int kk = 0; kk < NK; kk += 2) {
-          const uint4 c = live[t] ? *(const uint4*)(kr + col_of(kk)) : make_uint4(0, 0, 0, 0);
-          const float sc = live[t] ? e8m0(a.ks[row * (D / 32) + col_of(kk) / 32]) : 1.f;
-          s[t] = mfma16(kv_widen(c.x, c.y, sc), qf[kk], s[t]);
-          s[t] = mfma16(kv_widen(c.z, c.w, sc), qf[kk + 1], s[t]);
+      for (int i = 0; i < T::KP; ++i) {
+        if (X8) {
+          const float sc = e8m0(x.ks[t] >> (8 * (2 * i + (g >> 1))) & 255);
+          s[t] = mfma16(kv_widen(x.k[t][i].x, x.k[t][i].y, sc), qf[2 * i], s[t]);
+          s[t] = mfma16(kv_widen(x.k[t][i].z, x.k[t][i].w, sc), qf[2 * i + 1], s[t]);
+        } else {
+          s[t] = mfma16(as_bf16x8(x.k[t][i]), qf[i], s[t]);
         }
-      } else {
-        const uint16_t* kr = (const uint16_t*)a.kc + row * D;
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk)
-          s[t] = mfma16(as_bf16x8(live[t] ? *(const uint4*)(kr + col_of(kk)) : make_uint4(0, 0, 0, 0)), qf[kk], s[t]);
       }
     }
+    const int n0 = x.n[0], n1 = x.n[1];
+    const bool whole = n0 + n1 == DEC_TILE;
     // ---- V rows into LDS: rows that do not exist as zeros, whatever lies there
-    constexpr int LPR = X8 ? D / 16 : D / 8;    // lanes of a row, 16 bytes each
+    constexpr int LPR = X8 ? D / 16 : D / 8, PER = 64 / LPR;
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < DEC_TILE * LPR / 64; ++i) {
-      const int r = (i * 64 + lane) / LPR, c = (i * 64 + lane) % LPR;
-      const int64_t row = row_of(t0 + r);
-      const uint4 x = row >= 0 ? *(const uint4*)((const char*)a.vc + row * D * (X8 ? 1 : 2) + c * 16) : make_uint4(0, 0, 0, 0);
-      if (X8) {
-        const float sc = row >= 0 ? e8m0(a.vs[row * (D / 32) + c / 2]) : 1.f;
-        *(bf16x8*)(vl + dec_v_at<D>(r, 2 * c)) = kv_widen(x.x, x.y, sc);
-        *(bf16x8*)(vl + dec_v_at<D>(r, 2 * c + 1)) = kv_widen(x.z, x.w, sc);
-      } else {
-        *(uint4*)(vl + dec_v_at<D>(r, c)) = x;
+      for (int i = 0; i < T::VP; ++i) {
+        const int r = i * PER + lane / LPR;
+        const bool live = (r & 15) < (r < 16 ? n0 : n1);
+        x.v[i] = live ? x.v[i] : make_uint4(0, 0, 0, 0);
+        if (X8) x.vs[i] = live ? x.vs[i] : 127;
       }
     }
-    // ---- softmax: which of the lane's 8 keys exist is known to the lanes that loaded them
-    const uint64_t on[2] = {__ballot(live[0]), __ballot(live[1])};
-    float top = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s[t][r] = on[t] >> (4 * g + r) & 1 ? s[t][r] * a.scale_log2 : -INFINITY;
-        top = fmaxf(top, s[t][r]);
+    for (int i = 0; i < T::VP; ++i) {
+      const int r = i * PER + lane / LPR, c = lane % LPR;
+      const uint4 w = x.v[i];
+      if (X8) {
+        const float sc = e8m0(x.vs[i]);
+        *(bf16x8*)(vl + dec_v_at<D>(r, 2 * c)) = kv_widen(w.x, w.y, sc);
+        *(bf16x8*)(vl + dec_v_at<D>(r, 2 * c + 1)) = kv_widen(w.z, w.w, sc);
+      } else {
+        *(uint4*)(vl + dec_v_at<D>(r, c)) = w;
       }
+    }
+    if (t0 + DEC_STRIPE < k1) dec_ask<D, X8>(a, pages, kvh, t0 + DEC_STRIPE, k1, lane, x, bad);
+    pages = dec_pages(a, table, t0 + 2 * DEC_STRIPE, k1);
+    // ---- softmax: weights relative to a reference that follows the maximum only when that
+    // has passed it by 2^6
+    if (!whole) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (4 * g + r >= (t ? n1 : n0)) s[t][r] = -INFINITY;
+    }
+    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])), fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
     top = fmaxf(top, __shfl_xor(top, 16, kWave));
-    top = fmaxf(top, __shfl_xor(top, 32, kWave));
-    const float m_new = fmaxf(m, top), ref = m_new == -INFINITY ? 0.f : m_new;
-    const float keep = __builtin_amdgcn_exp2f(m - ref);
-    m = m_new;
-    sum *= keep;
+    top = fmaxf(top, __shfl_xor(top, 32, kWave)) * a.scale_log2;
+    if (__any(top > m + DEC_SLACK)) {
+      const float next = fmaxf(m, top), keep = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - next);
+      m = next;
+      sum *= keep;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) acc[i] *= keep;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
     uint32_t p[4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       float e[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sum += e[r] = __builtin_amdgcn_exp2f(s[t][r] - ref);
+      for (int r = 0; r < 4; ++r) sum += e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], a.scale_log2, -ref));
       p[2 * t] = pack2bf(e[0], e[1]);
       p[2 * t + 1] = pack2bf(e[2], e[3]);
     }
@@ -434,79 +540,125 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void decode_kernel(DecodeArgs a) {
       const int r = 4 * g + (l >> 2), c = 2 * i + ((l & 3) >> 1), lo = (l & 1) * 8;
       const uint2 v0 = tr_read((const uint4*)vl, dec_v_at<D>(r, c) + lo);
       const uint2 v1 = tr_read((const uint4*)vl, dec_v_at<D>(r + 16, c) + lo);
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) acc[i][r4] *= keep;
       acc[i] = mfma16(as_bf16x8(make_uint4(v0.x, v0.y, v1.x, v1.y)), pf, acc[i]);
     }
     __builtin_amdgcn_wave_barrier();
+  };
+
+  // ---- the waves' results of a unit, added in wave order (its V tiles are done with);
+  // thread t holds piece t of the 16 D / 4
+  DecNode value[ITEMS];
+  const auto join_waves = [&]() {
+    sum += __shfl_xor(sum, 16, kWave);
+    sum += __shfl_xor(sum, 32, kWave);
+    if (g == 0) ms[wave][l] = make_float2(m, sum);
+    float* const of = (float*)lds + wave * (16 * D);
+#pragma unroll
+    for (int i = 0; i < ND; ++i) *(f32x4*)(of + l * D + ((i * 16 + 4 * g) ^ ((l & 7) << 2))) = acc[i];
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < ITEMS; ++t) {
+      const int i = t * 64 * DEC_WAVES + threadIdx.x, h = i / (D / 4) & 15, c = i % (D / 4) * 4;
+      const float* const src = (const float*)lds + h * D + (c ^ ((h & 7) << 2));
+      DecNode v;
+      v.m = fmaxf(fmaxf(ms[0][h].x, ms[1][h].x), fmaxf(ms[2][h].x, ms[3][h].x));
+      v.sum = 0.f;
+      v.o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < DEC_WAVES; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ms[w][h].x - (v.m == -INFINITY ? 0.f : v.m));
+        v.sum = __builtin_fmaf(ms[w][h].y, f, v.sum);
+        const f32x4 p = *(const f32x4*)(src + w * 16 * D);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v.o[q] = __builtin_fmaf(p[q], f, v.o[q]);
+      }
+      value[t] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ND; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m = -INFINITY, sum = 0.f;
+  };
+
+  int units = 0;   // whole units so far: bit k says that left[k] waits for its neighbour
+  for (int u0 = k0; u0 < k1;) {
+    const int end = min(u0 + unit, k1);
+    for (int s0 = u0; s0 < end; s0 += DEC_STRIPE)
+      if (s0 + wave * DEC_TILE < k1) tile(s0 + wave * DEC_TILE);
+    join_waves();
+    u0 = end;
+    if (u0 == k1) break;
+    bool open = true;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (!open) continue;
+      open = units >> k & 1;
+#pragma unroll
+      for (int t = 0; t < ITEMS; ++t) {
+        if (open) value[t] = dec_join(DecNode{left_o[k][t][threadIdx.x], left_ms[k][t][threadIdx.x].x, left_ms[k][t][threadIdx.x].y}, value[t]);
+        else left_o[k][t][threadIdx.x] = value[t].o, left_ms[k][t][threadIdx.x] = make_float2(value[t].m, value[t].sum);
+      }
+    }
+    ++units;
   }
+  if (k0 >= k1) join_waves();
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (units >> k & 1) {
+#pragma unroll
+      for (int t = 0; t < ITEMS; ++t)
+        value[t] = dec_join(DecNode{left_o[k][t][threadIdx.x], left_ms[k][t][threadIdx.x].x, left_ms[k][t][threadIdx.x].y}, value[t]);
+    }
   if (bad) set_flag(a.status, LORA_FLAG_BAD_PAGE);
 
-  // ---- the waves' results, joined in wave order (the V tiles are done with)
-  sum += __shfl_xor(sum, 16, kWave);
-  sum += __shfl_xor(sum, 32, kWave);
-  __shared__ float2 ms[DEC_WAVES][16];
-  if (g == 0) ms[wave][l] = make_float2(m, sum);
-  __syncthreads();
-  float big = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < DEC_WAVES; ++w) big = fmaxf(big, ms[w][l].x);
-  const float ref = big == -INFINITY ? 0.f : big;
-  float all = 0.f;
-#pragma unroll
-  for (int w = 0; w < DEC_WAVES; ++w) all += ms[w][l].y * __builtin_amdgcn_exp2f(ms[w][l].x - ref);
-  const float mul = __builtin_amdgcn_exp2f(m - ref) * (all > 0.f || all != all ? 1.f / all : 0.f);
-  float* const of = (float*)lds + wave * (16 * D);   // [16 heads][D], a wave's V tile: 32 D bf16
-#pragma unroll
-  for (int i = 0; i < ND; ++i)
-    *(f32x4*)(of + l * D + ((i * 16 + 4 * g) ^ ((l & 7) << 2))) = acc[i] * mul;
-  __syncthreads();
   const int64_t bh = (int64_t)b * a.n_heads + head0;
-  for (int i = threadIdx.x; i < cols * (D / 4); i += 64 * DEC_WAVES) {
-    const int h = i / (D / 4), c = i % (D / 4) * 4;
-    const float* src = (const float*)lds + h * D + (c ^ ((h & 7) << 2));
-    f32x4 v = *(const f32x4*)src;
 #pragma unroll
-    for (int w = 1; w < DEC_WAVES; ++w) v += *(const f32x4*)(src + w * 16 * D);
-    if (only) *(uint2*)(a.o + (bh + h) * D + c) = make_uint2(pack2bf(v[0], v[1]), pack2bf(v[2], v[3]));
-    else *(f32x4*)(a.part + ((bh + h) * a.splits + split) * D + c) = v;
-  }
-  if (threadIdx.x < cols) {   // (lane l of wave 0: its own head's sums)
-    if (!only) a.stat[(bh + l) * a.splits + split] = make_float2(big, all);
-    else if (a.lse) a.lse[bh + l] = all == 0.f ? -INFINITY : (big + __log2f(all)) * KV_LN2;
+  for (int t = 0; t < ITEMS; ++t) {
+    const int i = t * 64 * DEC_WAVES + threadIdx.x, h = i / (D / 4), c = i % (D / 4) * 4;
+    if (h >= cols) continue;
+    if (only) dec_store(a, bh + h, D, c, value[t]);
+    else {
+      *(f32x4*)(a.part + ((bh + h) * a.nodes + node) * D + c) = value[t].o;
+      if (c == 0) a.stat[(bh + h) * a.nodes + node] = make_float2(value[t].m, value[t].sum);
+    }
   }
 }
 
-// The splits of a request and head, joined in order: a wave each.
-template <int D>
+// What is left of the trees: GROUPS groups of D / 4 threads a row (request and head), each
+// thread with four neighbouring nodes' pieces, then the groups' through LDS.
+template <int D, int GROUPS>
 __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs a, int64_t rows) {
-  const int64_t bh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (bh >= rows) return;
-  const int len = a.lens[bh / a.n_heads];
-  if ((uint32_t)len > (uint32_t)a.max_len) return;
-  const int per = decode_split(len), n = (len + per - 1) / per;
-  if (n <= 1) return;
-  const float2 st = lane < n ? a.stat[bh * a.splits + lane] : make_float2(-INFINITY, 0.f);
-  float big = st.x;
-  for (int o = 32; o; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, kWave));
-  const float ref = big == -INFINITY ? 0.f : big;
-  const float w = st.y * __builtin_amdgcn_exp2f(st.x - ref);
-  float all = w;
-  for (int o = 32; o; o >>= 1) all += __shfl_xor(all, o, kWave);
-  const float mul = w * (all > 0.f || all != all ? 1.f / all : 0.f);
-  constexpr int C = D / 64;
-  float v[C] = {};
-  const float* part = a.part + bh * a.splits * D + lane * C;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float f = __shfl(mul, i, kWave);
-#pragma unroll
-    for (int c = 0; c < C; ++c) v[c] += part[i * D + c] * f;
+  constexpr int LANES = D / 4, ROWS = 256 / LANES / GROUPS;
+  __shared__ DecNode lds[GROUPS > 1 ? 256 : 1];
+  const int grp = threadIdx.x / LANES % GROUPS, c = threadIdx.x % LANES;
+  const int64_t bh = (int64_t)blockIdx.x * ROWS + threadIdx.x / (LANES * GROUPS);
+  int n = 0;
+  if (bh < rows) {
+    const int len = a.lens[bh / a.n_heads];
+    if ((uint32_t)len <= (uint32_t)a.max_len) n = (int)cdiv(len, (int64_t)decode_unit(len) * a.span);
   }
-  if (C == 2) *(uint32_t*)(a.o + bh * D + lane * 2) = pack2bf(v[0], v[C - 1]);
-  else a.o[bh * D + lane] = f2bf(v[0]);
-  if (a.lse && lane == 0) a.lse[bh] = all == 0.f ? -INFINITY : (big + __log2f(all)) * KV_LN2;
+  if (n <= 1) n = 0;   // written before
+  DecNode v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t at = bh * a.nodes + grp * 4 + i;
+    if (grp * 4 + i >= n) continue;
+    v[i].o = ((const f32x4*)a.part)[at * LANES + c];
+    const float2 st = a.stat[at];
+    v[i].m = st.x, v[i].sum = st.y;
+  }
+  const int mine = n - grp * 4;
+  if (mine > 1) v[0] = dec_join(v[0], v[1]);
+  if (mine > 3) v[2] = dec_join(v[2], v[3]);
+  if (mine > 2) v[0] = dec_join(v[0], v[2]);
+#pragma unroll
+  for (int k = 1; k < GROUPS; k *= 2) {
+    __syncthreads();
+    if (mine > 0) lds[threadIdx.x] = v[0];
+    __syncthreads();
+    if (grp % (2 * k) == 0 && mine > 4 * k) v[0] = dec_join(v[0], lds[threadIdx.x + k * LANES]);
+  }
+  if (n && grp == 0) dec_store(a, bh, D, c * 4, v[0]);
 }
 
 }  // namespace lora
@@ -561,15 +713,23 @@ lora_status launch_kv_write(const kv_shape& sh, int64_t n, const uint16_t* k, in
   return launch_check("kv_write");
 }
 
-// Splits that a request of up to max_len keys may have.
-static int decode_splits(int64_t max_len) {
-  return (int)std::min<int64_t>(DEC_MAX_SPLITS, std::max<int64_t>(1, cdiv(max_len, DEC_MIN_SPLIT)));
+// How a batch is cut: units of a block, and nodes that a request of up to max_len keys has
+// then.
+struct DecodePlan {
+  int span, nodes;
+};
+static DecodePlan decode_plan(const kv_shape& sh, int32_t n_heads, int64_t max_len) {
+  const int64_t units = std::min<int64_t>(DEC_MAX_UNITS, std::max<int64_t>(1, cdiv(max_len, DEC_UNIT)));
+  const int64_t columns = (int64_t)sh.n_seqs * sh.n_kv_heads * cdiv(n_heads / sh.n_kv_heads, 16);
+  int span = 1;
+  while (span < DEC_MAX_SPAN && columns * cdiv(units, 2 * span) >= DEC_BLOCKS) span *= 2;
+  return {span, (int)cdiv(units, span)};
 }
 
 size_t decode_ws_bytes(const kv_shape& sh, int32_t n_heads, int64_t max_len) {
-  const int splits = decode_splits(max_len);
-  if (splits == 1) return 256;
-  const size_t parts = (size_t)sh.n_seqs * n_heads * splits;
+  const DecodePlan p = decode_plan(sh, n_heads, max_len);
+  if (p.nodes == 1) return 256;
+  const size_t parts = (size_t)sh.n_seqs * n_heads * p.nodes;
   return 256 + align_up(parts * sizeof(float2), 256) + parts * sh.head_dim * sizeof(float);
 }
 
@@ -578,27 +738,32 @@ lora_status launch_decode(const kv_shape& sh, int32_t n_heads, const uint16_t* q
                           const uint8_t* v_scales, const int32_t* table, const int32_t* seq_lens,
                           int64_t max_len, float scale, uint16_t* o, float* lse, void* ws,
                           hipStream_t s) {
+  const DecodePlan p = decode_plan(sh, n_heads, max_len);
   DecodeArgs a{};
   a.q = q, a.kc = k_cache, a.vc = v_cache, a.ks = k_scales, a.vs = v_scales;
   a.table = table, a.lens = seq_lens, a.o = o, a.lse = lse, a.status = (int32_t*)ws;
   a.q_stride = q_stride, a.n_heads = n_heads, a.n_kv = sh.n_kv_heads, a.group = n_heads / sh.n_kv_heads;
   a.page_shift = log2_of(sh.page_size), a.n_pages = sh.n_pages, a.max_pages = sh.max_pages;
-  a.max_len = (int32_t)max_len, a.splits = decode_splits(max_len), a.col_groups = (int)cdiv(a.group, 16);
-  a.scale_log2 = scale * KV_LOG2E;
+  a.max_len = (int32_t)max_len, a.nodes = p.nodes, a.span = p.span, a.col_groups = (int)cdiv(a.group, 16);
+  a.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * KV_LOG2E;
+  a.q_turn = scale < 0.f ? 0x80008000u : 0u, a.q_keep = scale == 0.f ? 0u : ~0u;
   const int64_t rows = (int64_t)sh.n_seqs * n_heads;
   a.stat = (float2*)((char*)ws + 256);
-  a.part = (float*)((char*)ws + 256 + align_up(rows * a.splits * (int64_t)sizeof(float2), 256));
-  const int64_t blocks = (int64_t)sh.n_seqs * a.splits * a.n_kv * a.col_groups;
+  a.part = (float*)((char*)ws + 256 + align_up(rows * a.nodes * (int64_t)sizeof(float2), 256));
+  const int64_t blocks = (int64_t)sh.n_seqs * a.nodes * a.n_kv * a.col_groups;
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * DEC_WAVES), 0, s, a);
   };
-  if (sh.head_dim == 128) k_scales ? go(decode_kernel<128, true>) : go(decode_kernel<128, false>);
-  else k_scales ? go(decode_kernel<64, true>) : go(decode_kernel<64, false>);
+  if (sh.head_dim == 64) k_scales ? go(decode_kernel<64, true, 1>) : go(decode_kernel<64, false, 1>);
+  else if (a.group <= 8) k_scales ? go(decode_kernel<128, true, 1>) : go(decode_kernel<128, false, 1>);
+  else k_scales ? go(decode_kernel<128, true, 2>) : go(decode_kernel<128, false, 2>);
   lora_status st = launch_check("decode");
-  if (st != LORA_OK || a.splits == 1) return st;
-  const dim3 grid((unsigned)cdiv(rows, 4));
-  if (sh.head_dim == 128) hipLaunchKernelGGL(decode_join_kernel<128>, grid, dim3(256), 0, s, a, rows);
-  else hipLaunchKernelGGL(decode_join_kernel<64>, grid, dim3(256), 0, s, a, rows);
+  if (st != LORA_OK || a.nodes == 1) return st;
+  const auto join = [&](auto kernel, int per_block) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(rows, per_block)), dim3(256), 0, s, a, rows);
+  };
+  if (sh.head_dim == 128) a.nodes <= 4 ? join(decode_join_kernel<128, 1>, 8) : join(decode_join_kernel<128, 8>, 1);
+  else a.nodes <= 4 ? join(decode_join_kernel<64, 1>, 16) : join(decode_join_kernel<64, 8>, 2);
   return launch_check("decode_join");
 }
 

@@ -34,9 +34,7 @@ __device__ __forceinline__ uint2 quantize8(const float* v, int& scale_byte) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// The scale of an E8M0 byte, 2^(b - 127): subnormal for 0, NaN for 255.
-__device__ __forceinline__ float e8m0(uint32_t b) {
-  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
-}
+// The scale of an E8M0 byte from 1 to 254, 2^(b - 127).
+__device__ __forceinline__ float e8m0(uint32_t b) { return __uint_as_float(b << 23); }
 
 }  // namespace lora

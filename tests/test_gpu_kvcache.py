@@ -362,6 +362,44 @@ def test_decode_same_bits_in_every_batch(x8):
         assert np.array_equal(o1[0], o[b]) and np.array_equal(lse1[0], lse[b]), b
 
 
+@pytest.mark.parametrize("d,kv,group,x8", [(128, 8, 2, False), (64, 8, 4, True), (128, 4, 16, True), (128, 4, 9, False)])
+def test_decode_large_batches_cut_elsewhere(d, kv, group, x8):
+    """Batches large enough that a block takes 2, 4 and 8 units: the bits of requests alone."""
+    rng = np.random.default_rng(d + group)
+    for n, longest in ((256, 400), (300, 1100), (400, 4200)):
+        lens = rng.integers(0, longest, n)
+        lens[:4] = longest, longest - 127, longest // 2 + 1, 130
+        pages = -(-lens // 16)
+        ids = torch.randperm(int(pages.sum()), device="cuda", dtype=torch.int32)
+        width = int(pages.max())
+        table = torch.zeros(n, width, dtype=torch.int32, device="cuda")
+        table[torch.arange(width, device="cuda") < torch.from_numpy(pages).cuda()[:, None]] = ids
+        shape = (len(ids), kv, 16, d)
+        if x8:
+            c = [torch.randint(0, 0x7E, shape, dtype=torch.uint8, device="cuda") for _ in range(2)] + \
+                [torch.randint(115, 122, (*shape[:3], d // 32), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        else:
+            c = [torch.randn(shape, device="cuda").bfloat16() for _ in range(2)] + [None, None]
+        q = torch.randn(n, kv * group, d, device="cuda").bfloat16()
+
+        def run(rows, bound):
+            m = len(rows)
+            s = L.make_kv_shape(m, kv, d, 16, len(ids), width)
+            o, lse = torch.full((m, kv * group, d), NAN, dtype=torch.bfloat16, device="cuda"), torch.full((m, kv * group), NAN, device="cuda")
+            ws = torch.full((L.attention_decode_workspace_bytes(s, kv * group, bound),), 0xFF, dtype=torch.uint8, device="cuda")
+            L.lora_workspace_init(ws)
+            L.attention_decode(s, q[rows].contiguous(), c[0], c[1], table[rows].contiguous(), dev_i32(lens[rows]), bound, 0.1, o, ws,
+                               k_scales=c[2], v_scales=c[3], lse=lse)
+            assert L.lora_device_status(ws) == 0
+            return o, lse
+
+        o, lse = run(np.arange(n), longest)
+        assert not torch.isnan(o).any()
+        for b in (0, 1, 2, 3, n - 1):
+            o1, lse1 = run(np.array([b]), width * 16)
+            assert torch.equal(o1[0], o[b]) and torch.equal(lse1[0], lse[b]), (n, b)
+
+
 def test_decode_q_in_a_fused_row():
     c = Decode([40, 200, 3], heads=6, kv=2, d=64, seed=5)
     wide = torch.full((3, 10, 64), NAN, dtype=torch.bfloat16, device="cuda")
