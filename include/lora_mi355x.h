@@ -647,7 +647,7 @@ lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table,
  *   o_i = bf16(sum_j exp(s_ij - lse_i) v_j).
  * A query that sees no key (Lk < Lq, Lk = 0) has o = 0 and lse = -inf.  Products and
  * sums are fp32; the weights exp(.) enter the second product as bf16.  A sequence's
- * results have the same bits whatever else the batch holds, and depend on nothing
+ * o and lse have the same bits whatever else the batch holds, and depend on nothing
  * outside its rows; with causal, o_i and lse_i depend on keys that query i sees only,
  * also where others hold NaN or Inf. */
 typedef struct {        /* host struct */
@@ -685,8 +685,9 @@ lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const 
  *   p_ij = exp(s_ij - lse_i),  ds_ij = p_ij (dout_i . v_j - dout_i . o_i)
  *   dq_i = scale sum_j ds_ij k_j
  *   dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
- * over the heads of j's group too; each sum in fp32, in a fixed order (bitwise
- * repeatable), p and ds entering the products as bf16, rounded to bf16 once at the end.
+ * over the heads of j's group too; each sum in fp32, in an order fixed by the call's
+ * sizes (bitwise repeatable; dq's by its own sequence alone), p and ds entering the
+ * products as bf16, rounded to bf16 once at the end.
  *   dout as o; dq, dk, dv bf16 out with the strides of q, k, v (so they may be slices of
  *   one buffer); none may overlap an input.  Rows that belong to no sequence are left as
  *   they were.  A NaN or Inf of a sequence may reach all gradients of that sequence, and

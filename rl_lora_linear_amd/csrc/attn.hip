@@ -91,17 +91,29 @@ __device__ __forceinline__ uint32_t at_lds(int r, int chunk) {
   return (uint32_t)(r * (D * 2) + ((chunk ^ at_swz<D>(r)) << 4));
 }
 
-// A transposed operand: columns 32 dt .. 32 dt + 31 as its rows, over 16 rows in the order
-// above, by two transposing reads; where this lane's lie from the first row on.
+// Where a lane's operands lie in a tile.  Direct: row l, columns 16 kk + 8 h on.
+// Transposed: columns 32 dt .. 32 dt + 31 as rows, over 16 rows in the order above, by two
+// transposing reads.  The swizzle is a XOR, so one base each gives all of them; OPAQUE
+// keeps the compiler from holding them all in registers.
+struct AttnPlaces {
+  uint32_t direct, transposed;
+};
 template <int D>
-__device__ __forceinline__ void transposed_at(uint32_t* at, int dt, int lane) {
-  const int i = lane & 15, r = 4 * (lane >> 5) + (i >> 2);
-  const int c = dt * 4 + (lane >> 4 & 1) * 2 + ((i & 3) >> 1), lo = (i & 1) * 8;
-  at[0] = at_lds<D>(r, c) + lo;
-  at[1] = at_lds<D>(r + 8, c) + lo;
+__device__ __forceinline__ AttnPlaces attn_places(int lane) {
+  const int i = lane & 15, r = 4 * (lane >> 5) + (i >> 2), c = (lane >> 4 & 1) * 2 + ((i & 3) >> 1);
+  return {at_lds<D>(lane & 31, lane >> 5), at_lds<D>(r, c) + (i & 1) * 8};
 }
-__device__ __forceinline__ bf16x8 transposed_pair(const char* tile, const uint32_t* at) {
-  const uint2 a = tr_read((const uint4*)tile, at[0]), b = tr_read((const uint4*)tile, at[1]);
+__device__ __forceinline__ AttnPlaces opaque(AttnPlaces p) {
+  asm volatile("" : "+v"(p.direct), "+v"(p.transposed));
+  return p;
+}
+__device__ __forceinline__ bf16x8 direct_op(const char* rows, AttnPlaces p, int kk) {
+  return as_bf16x8(*(const uint4*)(rows + (p.direct ^ (kk << 5))));
+}
+template <int D>
+__device__ __forceinline__ bf16x8 transposed_op(const char* rows, AttnPlaces p, int dt) {
+  const uint2 a = tr_read((const uint4*)rows, p.transposed ^ (dt << 6));
+  const uint2 b = tr_read((const uint4*)(rows + 8 * D * 2), p.transposed ^ (dt << 6) ^ 32);
   return as_bf16x8(make_uint4(a.x, a.y, b.x, b.y));
 }
 
@@ -137,6 +149,32 @@ template <int D>
 __device__ __forceinline__ void load_rows(bf16x8* f, const uint16_t* row, int h) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) f[kk] = as_bf16x8(*(const uint4*)(row + kk * 16 + h * 8));
+}
+
+// Waits for the rows here: else the compiler does where they are used, in the loop, each
+// time, and there the wait would be for the tiles on their way as well.
+template <int N>
+__device__ __forceinline__ void settle(bf16x8 (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint4 u = __builtin_bit_cast(uint4, f[i]);
+    asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w));
+    f[i] = as_bf16x8(u);
+  }
+}
+
+// The order of the products before this point in a block of instructions: the LDS reads of
+// four, then each product with the reads of the fourth one on.
+template <int PRODUCTS, int READS>
+__device__ __forceinline__ void feed_products() {
+  constexpr int AHEAD = 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, READS * AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < PRODUCTS - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
 __device__ __forceinline__ bf16x8 pack_op(const f32x16& x, int half) {
@@ -216,7 +254,7 @@ __device__ __forceinline__ f32x16 product_seen(bf16x8 v, bf16x8 p, f32x16 acc, i
 constexpr float AT_SLACK = 6.f;
 
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_fwd_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
   constexpr int TILE = AT_TILE * D * 2;            // bytes of one operand of a stage
   __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
@@ -259,6 +297,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
       qf[kk] = as_bf16x8(make_uint4((u.x ^ turn) & keep, (u.y ^ turn) & keep, (u.z ^ turn) & keep, (u.w ^ turn) & keep));
     }
   }
+  settle(qf);
   if (threadIdx.x < 2) odd_tile[threadIdx.x] = 0;
   __syncthreads();
   if (tiles) stage(0, 0);
@@ -269,25 +308,21 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
     for (int r = 0; r < 16; ++r) acc[dt][r] = 0.f;
   float ref = -INFINITY, sum = 0.f;
 
-  // where this lane's operands lie in a tile
-  uint32_t ka[NK], va[ND][2];
-#pragma unroll
-  for (int kk = 0; kk < NK; ++kk) ka[kk] = at_lds<D>(l, 2 * kk + h);
-#pragma unroll
-  for (int dt = 0; dt < ND; ++dt) transposed_at<D>(va[dt], dt, lane);
+  const AttnPlaces places = attn_places<D>(lane);
 
   const auto step = [&](int t, auto st, auto masked) {   // masked: false_type, or whether to mask
     const int K0 = st * 2 * TILE, V0 = K0 + TILE;
     const int t0 = t * AT_TILE;
+    const AttnPlaces at = opaque(places);
     f32x16 x[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.f;
+    // (two sums in turn: a product that adds to the one before it waits for it)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) x[u][r] = 0.f;
+    for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
-      for (int kk = 0; kk < NK; ++kk)
-        x[u] = mfma32(as_bf16x8(*(const uint4*)(lds + K0 + u * 32 * D * 2 + ka[kk])), qf[kk], x[u]);
-    }
+      for (int u = 0; u < 2; ++u) x[u] = mfma32(direct_op(lds + K0 + u * 32 * D * 2, at, kk), qf[kk], x[u]);
+    feed_products<2 * NK, 1>();
     if (masked) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -323,7 +358,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
           const bf16x8 p = pack_op(x[b >> 1], b & 1);
 #pragma unroll
           for (int dt = 0; dt < ND; ++dt)
-            acc[dt] = product_seen(transposed_pair(lds + V0 + b * 16 * D * 2, va[dt]), p, acc[dt], t0 + b * 16, last);
+            acc[dt] = product_seen(transposed_op<D>(lds + V0 + b * 16 * D * 2, at, dt), p, acc[dt], t0 + b * 16, last);
         }
         return;
       }
@@ -332,7 +367,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
     for (int b = 0; b < 4; ++b) {
       const bf16x8 p = pack_op(x[b >> 1], b & 1);
 #pragma unroll
-      for (int dt = 0; dt < ND; ++dt) acc[dt] = mfma32(transposed_pair(lds + V0 + b * 16 * D * 2, va[dt]), p, acc[dt]);
+      for (int dt = 0; dt < ND; ++dt) acc[dt] = mfma32(transposed_op<D>(lds + V0 + b * 16 * D * 2, at, dt), p, acc[dt]);
     }
   };
   // tile t has landed for every wave, and every wave is done with the other stage; where a
@@ -370,7 +405,7 @@ __global__ __launch_bounds__(64 * NW) void attention_fwd_kernel(AttnArgs a) {
 // ---------------------------------------------------------------- dq
 // Waves, tiles and stages as in the forward.
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) void attention_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_dq_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
   constexpr int TILE = AT_TILE * D * 2;
   __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
@@ -411,6 +446,8 @@ __global__ __launch_bounds__(64 * NW) void attention_dq_kernel(AttnArgs a) {
       for (int j = 0; j < 8; ++j) delta += (float)of[kk][j] * (float)df[kk][j];
     delta += __shfl_xor(delta, 32, kWave);
   }
+  settle(qf);
+  settle(df);
   const float lse = a.lse[head * a.n_q + row] * AT_LOG2E;
   if (i < s.lq) a.stats[((int64_t)head * 2 + h) * a.n_q + row] = h ? delta : lse;
   if (tiles) stage(0, 0);
@@ -420,24 +457,23 @@ __global__ __launch_bounds__(64 * NW) void attention_dq_kernel(AttnArgs a) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[dt][r] = 0.f;
 
-  uint32_t ka[NK], ta[ND][2];
-#pragma unroll
-  for (int kk = 0; kk < NK; ++kk) ka[kk] = at_lds<D>(l, 2 * kk + h);
-#pragma unroll
-  for (int dt = 0; dt < ND; ++dt) transposed_at<D>(ta[dt], dt, lane);
+  const AttnPlaces places = attn_places<D>(lane);
 
   const auto step = [&](int t, auto st, auto masked) {   // masked: false_type, or whether to mask
     const int K0 = st * 2 * TILE, V0 = K0 + TILE;
     const int t0 = t * AT_TILE;
+    const AttnPlaces at = places;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f32x16 x, y;
 #pragma unroll
       for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < NK; ++kk) x = mfma32(as_bf16x8(*(const uint4*)(lds + K0 + u * 32 * D * 2 + ka[kk])), qf[kk], x);
-#pragma unroll
-      for (int kk = 0; kk < NK; ++kk) y = mfma32(as_bf16x8(*(const uint4*)(lds + V0 + u * 32 * D * 2 + ka[kk])), df[kk], y);
+      for (int kk = 0; kk < NK; ++kk) {
+        x = mfma32(direct_op(lds + K0 + u * 32 * D * 2, at, kk), qf[kk], x);
+        y = mfma32(direct_op(lds + V0 + u * 32 * D * 2, at, kk), df[kk], y);
+      }
+      feed_products<2 * NK, 1>();
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], a.scale_log2, -lse));
@@ -453,7 +489,7 @@ __global__ __launch_bounds__(64 * NW) void attention_dq_kernel(AttnArgs a) {
         const bf16x8 ds = pack_op(x, b);
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt)
-          acc[dt] = mfma32(transposed_pair(lds + K0 + (u * 32 + b * 16) * D * 2, ta[dt]), ds, acc[dt]);
+          acc[dt] = mfma32(transposed_op<D>(lds + K0 + (u * 32 + b * 16) * D * 2, at, dt), ds, acc[dt]);
       }
     }
   };
@@ -482,69 +518,94 @@ __global__ __launch_bounds__(64 * NW) void attention_dq_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- dk, dv
-// A wave owns 32 keys, NW waves 32 NW of them in a row; tiles of 32 queries and of their
-// dout pass, head by head of the group, with their lse and delta.
+// A wave owns 32 keys, KW waves 32 KW of them in a row, and the block's NW / KW phases
+// share out what those keys have to see: tiles of 32 queries of a head, with their dout,
+// lse and delta, head after head of the group, phase p taking every (NW / KW)-th.  Each
+// phase has its own LDS stages, filled by its own waves, the DMA that many tiles ahead but
+// one.  At the end the phases' sums are added in order, through LDS.
 constexpr int DKV_TILE = 32;
 
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) void attention_dkv_kernel(AttnArgs a) {
-  constexpr int ND = D / 32, NK = D / 16;
-  constexpr int TILE = DKV_TILE * D * 2;
-  __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
-  __shared__ __attribute__((aligned(16))) float stats[2][2][DKV_TILE];   // of a stage: lse in powers of two, delta
+template <int D, int NW, int KW, int S>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_dkv_kernel(AttnArgs a) {
+  constexpr int ND = D / 32, NK = D / 16, P = NW / KW;
+  constexpr int TILE = DKV_TILE * D * 2, STAGE = 2 * TILE;   // q's rows, then dout's
+  constexpr int N = DKV_TILE * D * 2 / 1024, DMAS = 2 * ((N + KW - 1) / KW) + 1;   // of a wave and stage
+  static_assert(P * S * STAGE >= (NW - KW) * TILE * 2);      // room for the other phases' dk or dv in fp32
+  static_assert(N % KW == 0);
+  __shared__ __attribute__((aligned(16))) char lds[P * S * STAGE];
+  __shared__ __attribute__((aligned(16))) float stats[P][S][2][DKV_TILE];   // of a stage: lse in powers of two, delta
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l = lane & 31, h = lane >> 5;
+  const int l = lane & 31, h = lane >> 5, phase = wave / KW, kw = wave % KW;
   const int kvh = blockIdx.x % a.n_kv;
   // the first keys are seen by the most queries
   const AttnSeq s = find_sequence(a, a.cu_k, blockIdx.x / a.n_kv, a.shift);
   if (s.tile < 0) return;
-  const int row0 = s.tile << a.shift, w0 = row0 + wave * 32, j = w0 + l;   // key row
+  const int row0 = s.tile << a.shift, w0 = row0 + kw * 32, j = w0 + l;   // key row
   const int ahead = s.lk - s.lq;
   // the first query that sees this lane's key, one of the wave's, all of the wave's
   const int first = a.causal ? j - ahead : 0;
   const int wave_first = w0 >= s.lk ? 1 << 30 : a.causal ? w0 - ahead : 0, wave_all = a.causal ? w0 + 31 - ahead : 0;
   const int begin = a.causal ? max(row0 - ahead, 0) / DKV_TILE : 0;
-  const int per_head = max((s.lq + DKV_TILE - 1) / DKV_TILE - begin, 0), tiles = per_head * a.group;
+  const int end = (s.lq + DKV_TILE - 1) / DKV_TILE, per_head = max(end - begin, 0);
+  const int tiles = per_head * a.group, steps = (tiles + P - 1) / P;
 
-  const uint32_t lds0 = lds_offset(lds), stats0 = lds_offset(stats);
-  // the next tile to be asked for: its head and its place in the head
-  int ask_head = kvh * a.group, ask_t = begin;
+  // the phase's tile: head of the group and tile of the head
+  struct At {
+    int head, tile;
+  };
+  const auto skip = [&](At& t, int n) {
+    for (t.tile += n; t.tile >= end && t.head < a.group; t.tile -= per_head) ++t.head;
+  };
+  const uint32_t lds0 = lds_offset(lds) + phase * S * STAGE, stats0 = lds_offset(stats) + phase * (int)sizeof(stats[0]);
+  At ask{0, begin};
+  // every stage is as many DMAs, so that a count of them says which have landed: behind the
+  // last tile, a tile is fetched that nobody reads
   const auto stage = [&](int st) {
-    const int t0 = ask_t * DKV_TILE;
-    dma_tile<D, NW, DKV_TILE>(a.q + s.q0 * a.q_stride + ask_head * D, a.q_stride, t0, s.lq, lds0 + st * 2 * TILE, wave, lane);
-    dma_tile<D, NW, DKV_TILE>(a.dout + s.q0 * a.o_stride + ask_head * D, a.o_stride, t0, s.lq, lds0 + st * 2 * TILE + TILE, wave, lane);
-    if (wave == 0)   // the lower lanes fetch the tile's lse, the upper ones its delta
-      dma4_at(a.stats + ((int64_t)ask_head * 2 + h) * a.n_q + s.q0 + min(t0 + l, s.lq - 1), stats0 + st * (int)sizeof(stats[0]));
-    if (++ask_t == begin + per_head) ask_t = begin, ++ask_head;
+    const bool real = ask.head < a.group;
+    const int t0 = (real ? ask.tile : begin) * DKV_TILE, head = kvh * a.group + (real ? ask.head : 0);
+    dma_tile<D, KW, DKV_TILE>(a.q + s.q0 * a.q_stride + head * D, a.q_stride, t0, s.lq, lds0 + st * STAGE, kw, lane);
+    dma_tile<D, KW, DKV_TILE>(a.dout + s.q0 * a.o_stride + head * D, a.o_stride, t0, s.lq, lds0 + st * STAGE + TILE, kw, lane);
+    // the lower lanes fetch the tile's lse, the upper ones its delta (each wave the same)
+    dma4_at(a.stats + ((int64_t)head * 2 + h) * a.n_q + s.q0 + min(t0 + l, s.lq - 1), stats0 + st * (int)sizeof(stats[0][0]));
+    skip(ask, P);
   };
   bf16x8 kf[NK], vf[NK];
   const int64_t row = s.k0 + min(j, s.lk - 1);
   load_rows<D>(kf, a.k + row * a.k_stride + kvh * D, h);
   load_rows<D>(vf, a.v + row * a.v_stride + kvh * D, h);
-  if (tiles) stage(0);
+  settle(kf);
+  settle(vf);
+  At now{0, begin};
+  if (per_head) {
+    skip(now, phase);
+    ask = now;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) stage(i);
+  }
   f32x16 dk[ND], dv[ND];
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dk[dt][r] = dv[dt][r] = 0.f;
-  uint32_t ka[NK], ta[ND][2];
-#pragma unroll
-  for (int kk = 0; kk < NK; ++kk) ka[kk] = at_lds<D>(l, 2 * kk + h);
-#pragma unroll
-  for (int dt = 0; dt < ND; ++dt) transposed_at<D>(ta[dt], dt, lane);
+  const AttnPlaces places = attn_places<D>(lane);
 
-  const auto step = [&](int t0, auto stage_c, const bool masked) {
-    constexpr int ST = decltype(stage_c)::value, Q0 = ST * 2 * TILE, G0 = Q0 + TILE;
+  const auto step = [&](int t0, int st, const bool masked) {
+    const char *const qt = lds, *const gt = qt + TILE;
+    const float* const stat = &stats[phase][st][0][0];
+    const uint32_t off = (phase * S + st) * STAGE;   // (above the bits that the swizzle turns)
+    const AttnPlaces at = opaque({places.direct + off, places.transposed + off});
     f32x16 x, y;
 #pragma unroll
     for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.f;
 #pragma unroll
-    for (int kk = 0; kk < NK; ++kk) x = mfma32(as_bf16x8(*(const uint4*)(lds + Q0 + ka[kk])), kf[kk], x);
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) y = mfma32(as_bf16x8(*(const uint4*)(lds + G0 + ka[kk])), vf[kk], y);
+    for (int kk = 0; kk < NK; ++kk) {
+      x = mfma32(direct_op(qt, at, kk), kf[kk], x);
+      y = mfma32(direct_op(gt, at, kk), vf[kk], y);
+    }
+    feed_products<2 * NK, 1>();
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
-      const f32x4 ls = *(const f32x4*)&stats[ST][0][8 * r4 + 4 * h];
+      const f32x4 ls = *(const f32x4*)&stat[8 * r4 + 4 * h];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int r = r4 * 4 + c;
@@ -562,11 +623,11 @@ __global__ __launch_bounds__(64 * NW) void attention_dkv_kernel(AttnArgs a) {
     for (int b = 0; b < 2; ++b) {
       const bf16x8 p = pack_op(x, b);
 #pragma unroll
-      for (int dt = 0; dt < ND; ++dt) dv[dt] = mfma32(transposed_pair(lds + G0 + b * 16 * D * 2, ta[dt]), p, dv[dt]);
+      for (int dt = 0; dt < ND; ++dt) dv[dt] = mfma32(transposed_op<D>(gt + b * 16 * D * 2, at, dt), p, dv[dt]);
     }
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
-      const f32x4 de = *(const f32x4*)&stats[ST][1][8 * r4 + 4 * h];
+      const f32x4 de = *(const f32x4*)&stat[DKV_TILE + 8 * r4 + 4 * h];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int r = r4 * 4 + c;
@@ -577,23 +638,40 @@ __global__ __launch_bounds__(64 * NW) void attention_dkv_kernel(AttnArgs a) {
     for (int b = 0; b < 2; ++b) {
       const bf16x8 ds = pack_op(y, b);
 #pragma unroll
-      for (int dt = 0; dt < ND; ++dt) dk[dt] = mfma32(transposed_pair(lds + Q0 + b * 16 * D * 2, ta[dt]), ds, dk[dt]);
+      for (int dt = 0; dt < ND; ++dt) dk[dt] = mfma32(transposed_op<D>(qt + b * 16 * D * 2, at, dt), ds, dk[dt]);
     }
   };
-  int at_t = begin;
-  const auto turn = [&](int n, auto stage_c) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (n + 1 < tiles) stage(1 - decltype(stage_c)::value);
-    const int t0 = at_t * DKV_TILE;
-    if (++at_t == begin + per_head) at_t = begin;
-    if (t0 + DKV_TILE - 1 < wave_first) return;
-    step(t0, stage_c, t0 < wave_all || t0 + DKV_TILE > s.lq);
-  };
-  for (int n = 0; n < tiles; n += 2) {
-    turn(n, std::integral_constant<int, 0>{});
-    if (n + 1 < tiles) turn(n + 1, std::integral_constant<int, 1>{});
+  for (int n = 0, st = 0; n < steps; ++n) {
+    // the tile has landed, every wave is done with the stage before it
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * DMAS) : "memory");
+    stage(st == 0 ? S - 1 : st - 1);
+    const int t0 = now.tile * DKV_TILE;
+    if (now.head < a.group && t0 + DKV_TILE - 1 >= wave_first) step(t0, st, t0 < wave_all || t0 + DKV_TILE > s.lq);
+    skip(now, P);
+    st = st == S - 1 ? 0 : st + 1;
   }
-  if (j >= s.lk) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no DMA outlives the loop
+  const auto add_phases = [&](f32x16* x) {
+    if (P == 1) return;
+    f32x4* const part = (f32x4*)lds + ((phase - 1) * KW + kw) * (ND * 4 * 64);
+    __syncthreads();
+    if (phase)
+#pragma unroll
+      for (int i = 0; i < ND * 4; ++i) part[i * 64 + lane] = f32x4{x[i / 4][i % 4 * 4], x[i / 4][i % 4 * 4 + 1], x[i / 4][i % 4 * 4 + 2], x[i / 4][i % 4 * 4 + 3]};
+    __syncthreads();
+    if (phase == 0)
+#pragma unroll
+      for (int p = 1; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < ND * 4; ++i) {
+          const f32x4 v = ((const f32x4*)lds)[((p - 1) * KW + kw) * (ND * 4 * 64) + i * 64 + lane];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[i / 4][i % 4 * 4 + c] += v[c];
+        }
+  };
+  add_phases(dk);
+  add_phases(dv);
+  if (phase || j >= s.lk) return;
   store_row<D>(a.dk + (s.k0 + j) * a.k_stride + kvh * D, dk, a.scale, h);
   store_row<D>(a.dv + (s.k0 + j) * a.v_stride + kvh * D, dv, 1.f, h);
 }
@@ -658,11 +736,16 @@ lora_status launch_attention_bwd(const attn_shape& sh, const uint16_t* dout, con
   else g.waves == 8 ? go_q(attention_dq_kernel<64, 8>) : go_q(attention_dq_kernel<64, 4>);
   lora_status st = launch_check("attention_backward dq");
   if (st != LORA_OK) return st;
-  a.shift = 7;
+  // 128 keys a block where that leaves a block for each CU, else 32
+  const auto key_blocks = [&](int shift) { return ((sh.n_k >> shift) + sh.n_seqs) * sh.n_kv_heads; };
+  const bool wide = key_blocks(7) >= 2 * device_cus();
+  a.shift = wide ? 7 : 5;
   a.tiles = (int)((sh.n_k >> a.shift) + sh.n_seqs);
-  const dim3 grid((unsigned)((int64_t)a.tiles * a.n_kv)), block(256);
-  if (sh.head_dim == 128) hipLaunchKernelGGL((attention_dkv_kernel<128, 4>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((attention_dkv_kernel<64, 4>), grid, block, 0, s, a);
+  const auto go_k = [&](auto kernel, int waves) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)key_blocks(a.shift)), dim3(64 * waves), 0, s, a);
+  };
+  if (sh.head_dim == 128) wide ? go_k(attention_dkv_kernel<128, 8, 4, 2>, 8) : go_k(attention_dkv_kernel<128, 4, 1, 2>, 4);
+  else wide ? go_k(attention_dkv_kernel<64, 8, 4, 2>, 8) : go_k(attention_dkv_kernel<64, 4, 1, 2>, 4);
   return launch_check("attention_backward dk, dv");
 }
 
