@@ -675,7 +675,7 @@ size_t attention_workspace_bytes(const attn_shape* shape);
  *              one array.  A sequence that breaks this sets LORA_FLAG_BAD_LENGTH and is
  *              left out.
  *   o   bf16 [n_q] rows of [n_heads][head_dim] out, must not overlap q, k or v
- *   lse fp32 [n_heads][n_q] out
+ *   lse fp32 [n_heads][n_q] out; it and ws must not overlap another operand
  * Rows of o and lse that belong to no sequence are left as they were. */
 lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const uint16_t* k,
                               const uint16_t* v, const int32_t* cu_q, const int32_t* cu_k,
@@ -747,7 +747,8 @@ typedef struct {        /* host struct */
  *                         of range is met: its rows' slots are -1, and it is put into
  *                         the ring as it is.
  * Pages that do not fit the ring (the same page put twice) are dropped whole, with
- * LORA_FLAG_BAD_PAGE.  0 <= n_slots < 2^30.
+ * LORA_FLAG_BAD_PAGE.  0 <= n_slots < 2^30.  But for seq_lens and ring_state_out as said,
+ * no output may overlap another operand.
  * Workspace: kv_tables_workspace_bytes(shape); word 0 is the status word. */
 size_t kv_tables_workspace_bytes(const kv_shape* shape);
 lora_status kv_tables(const kv_shape* shape, const int32_t* cached_lens, const int32_t* new_lens,
@@ -784,7 +785,7 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
  *        launch: a step captured with the longest length to come serves every step.  A
  *        length outside [0, max_len] counts as 0 and sets LORA_FLAG_BAD_LENGTH; rows of
  *        a page out of range are left out, with LORA_FLAG_BAD_PAGE.
- *   o    bf16 [n_seqs][n_heads][head_dim] out, must not overlap q
+ *   o    bf16 [n_seqs][n_heads][head_dim] out; outputs must not overlap other operands
  *   lse  fp32 [n_seqs][n_heads] out, nullable
  * Products and sums are fp32, the weights exp(.) enter the second product as bf16; keys
  * and values in 8 bits enter as bf16, as the 8-bit x of w4_linear does: exactly for scale

@@ -35,6 +35,18 @@ Span span(const void* p, int64_t rows, int64_t stride, int64_t cols) {
 bool meet(Span a, Span b) {
   return a.from && b.from && a.from < a.to && b.from < b.to && a.from < b.to && b.from < a.to;
 }
+Span bytes(const void* p, int64_t n) { return {(const char*)p, (const char*)p + n}; }
+// The first of `out` that lies on another buffer, of `in` or of the other outputs; -1: none.
+template <size_t N, size_t M>
+int clash(const Span (&out)[N], const Span (&in)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (const Span& s : in)
+      if (meet(out[i], s)) return (int)i;
+    for (size_t j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return (int)i;
+  }
+  return -1;
+}
 // Whether rows of two strided matrices share bytes.  Slices of one buffer (the same stride)
 // lie between one another: they meet where their columns do.
 bool rows_meet(const void* a, int64_t a_rows, int64_t a_stride, int64_t a_cols, const void* b,
@@ -131,6 +143,11 @@ lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const 
                      !rows_meet(o, s.n_q, s.o_stride, qc, k, s.n_k, s.k_stride, kc) &&
                      !rows_meet(o, s.n_q, s.o_stride, qc, v, s.n_k, s.v_stride, kc),
                  "attention_forward: o overlaps q, k or v");
+  const int64_t cu = 4 * ((int64_t)s.n_seqs + 1);
+  const Span out[] = {bytes(lse, 4 * (int64_t)s.n_heads * s.n_q), bytes(ws, (int64_t)attn_ws(s))};
+  const Span in[] = {span(q, s.n_q, s.q_stride, qc), span(k, s.n_k, s.k_stride, kc), span(v, s.n_k, s.v_stride, kc),
+                     span(o, s.n_q, s.o_stride, qc), bytes(cu_q, cu), bytes(cu_k, cu)};
+  LORA_ARG_CHECK(clash(out, in) < 0, "attention_forward: lse or the workspace overlaps another operand");
   if (s.n_q == 0 || s.n_seqs == 0) return LORA_OK;
   return launch_attention_fwd(s, q, k, v, cu_q, cu_k, o, lse, ws, S(stream));
 }
@@ -164,6 +181,19 @@ lora_status attention_backward(const attn_shape* shape, const uint16_t* dout, co
     for (const Rows& r : in) LORA_ARG_CHECK(!meets(out[i], r), "attention_backward: dq, dk or dv overlaps an input");
     for (int j = 0; j < i; ++j) LORA_ARG_CHECK(!meets(out[i], out[j]), "attention_backward: dq, dk and dv overlap");
   }
+  const int64_t cu = 4 * ((int64_t)s.n_seqs + 1);
+  const Span work[] = {bytes(ws, (int64_t)attn_ws(s))};
+  Span rest[11];
+  int n = 0;
+  for (const Rows& r : in) rest[n++] = span(r.p, r.rows, r.stride, r.cols);
+  for (const Rows& r : out) rest[n++] = span(r.p, r.rows, r.stride, r.cols);
+  rest[n++] = bytes(lse, 4 * (int64_t)s.n_heads * s.n_q);
+  rest[n++] = bytes(cu_q, cu);
+  rest[n++] = bytes(cu_k, cu);
+  LORA_ARG_CHECK(clash(work, rest) < 0, "attention_backward: the workspace overlaps another operand");
+  for (int i = 0; i < 3; ++i)
+    LORA_ARG_CHECK(!meet(rest[5 + i], rest[8]) && !meet(rest[5 + i], rest[9]) && !meet(rest[5 + i], rest[10]),
+                   "attention_backward: dq, dk or dv overlaps lse, cu_q or cu_k");
   if (s.n_seqs == 0 || (s.n_q == 0 && s.n_k == 0)) return LORA_OK;
   return launch_attention_bwd(s, dout, q, k, v, o, lse, cu_q, cu_k, dq, dk, dv, ws, S(stream));
 }
@@ -189,8 +219,16 @@ lora_status kv_tables(const kv_shape* shape, const int32_t* cached_lens, const i
   for (const void* p : {(const void*)cached_lens, (const void*)new_lens, (const void*)seq_lens, (const void*)block_table,
                         (const void*)ring, (const void*)cu_new, (const void*)slots, (const void*)positions, (const void*)token_seqs})
     LORA_ARG_CHECK(aligned(p, 4), "kv_tables: int32 operands must be 4-byte aligned");
-  LORA_ARG_CHECK(s.n_seqs == 0 || seq_lens != new_lens, "kv_tables: seq_lens and new_lens are the same buffer");
   TRY(check_ws(ws, ws_bytes, 256, "kv_tables"));
+  const int64_t n4 = 4 * (int64_t)s.n_seqs, s4 = 4 * n_slots;
+  // in place, or apart: seq_lens and cached_lens, the two states
+  const Span lens = bytes(seq_lens != cached_lens ? cached_lens : nullptr, n4),
+             state = bytes(ring_state_out != ring_state ? ring_state : nullptr, 16);
+  const Span out[] = {bytes(seq_lens, n4), bytes(block_table, n4 * s.max_pages), bytes(ring, 4 * (int64_t)s.n_pages),
+                      bytes(ring_state_out, 16), bytes(cu_new, n4 + 4), bytes(slots, s4), bytes(positions, s4),
+                      bytes(token_seqs, s4), bytes(ws, 256)};
+  const Span in[] = {lens, bytes(new_lens, n4), state};
+  LORA_ARG_CHECK(clash(out, in) < 0, "kv_tables: an output overlaps another operand");
   return launch_kv_tables(s, cached_lens, new_lens, seq_lens, block_table, ring, ring_state, ring_state_out, cu_new,
                           n_slots, slots, positions, token_seqs, ws, S(stream));
 }
@@ -216,6 +254,12 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
                        !meet(span(c, rows, half, half), span(v, n, v_stride, cols)),
                    "kv_write: a cache overlaps k or v");
   LORA_ARG_CHECK(!meet(span(k_cache, rows, half, half), span(v_cache, rows, half, half)), "kv_write: the caches overlap");
+  const int64_t sb = rows * (s.head_dim / 32);
+  const Span out[] = {bytes(k_scales, sb), bytes(v_scales, sb), bytes(ws, 256)};
+  const Span in[] = {span(k, n, k_stride, cols), span(v, n, v_stride, cols), span(k_cache, rows, half, half),
+                     span(v_cache, rows, half, half), bytes(slots, 4 * n)};
+  LORA_ARG_CHECK(clash(out, in) < 0, "kv_write: the scales or the workspace overlap another operand");
+  LORA_ARG_CHECK(!meet(in[2], in[4]) && !meet(in[3], in[4]), "kv_write: a cache overlaps slots");
   if (n == 0) return LORA_OK;
   return launch_kv_write(s, n, k, k_stride, v, v_stride, slots, k_cache, v_cache, k_scales, v_scales, ws, S(stream));
 }
@@ -258,6 +302,13 @@ lora_status attention_decode(const kv_shape* shape, int32_t n_heads, const uint1
   TRY(check_caches(s, k_cache, v_cache, k_scales, v_scales, "attention_decode"));
   TRY(check_ws(ws, ws_bytes, decode_ws_bytes(s, n_heads, max_len), "attention_decode"));
   LORA_ARG_CHECK(!meet(span(o, s.n_seqs, cols, cols), span(q, s.n_seqs, q_stride, cols)), "attention_decode: o overlaps q");
+  const int64_t rows = cache_rows(s), half = k_scales ? s.head_dim / 2 : s.head_dim, sb = rows * (s.head_dim / 32);
+  const Span out[] = {span(o, s.n_seqs, cols, cols), bytes(lse, 4 * (int64_t)s.n_seqs * n_heads),
+                      bytes(ws, (int64_t)decode_ws_bytes(s, n_heads, max_len))};
+  const Span in[] = {span(q, s.n_seqs, q_stride, cols), span(k_cache, rows, half, half), span(v_cache, rows, half, half),
+                     bytes(k_scales, sb), bytes(v_scales, sb), bytes(block_table, 4 * (int64_t)s.n_seqs * s.max_pages),
+                     bytes(seq_lens, 4 * (int64_t)s.n_seqs)};
+  LORA_ARG_CHECK(clash(out, in) < 0, "attention_decode: an output overlaps another operand");
   if (s.n_seqs == 0) return LORA_OK;
   return launch_decode(s, n_heads, q, q_stride, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, max_len,
                        scale, o, lse, ws, S(stream));

@@ -18,10 +18,10 @@ def test_attention(L):  # noqa: F811
     need = L.attention_workspace_bytes(mk())
     assert 256 + 8 * 4 * 100 <= need
 
-    def fwd(s=None, q=at(1), k=at(2), v=at(3), cq=P, ck=P, o=at(4), lse=P, ws=P, nb=BIG):
+    def fwd(s=None, q=at(1), k=at(2), v=at(3), cq=P, ck=P, o=at(4), lse=at(10), ws=at(11), nb=BIG):
         return lib.attention_forward(ctypes.byref(s or mk()), q, k, v, cq, ck, o, lse, ws, nb, None)
 
-    def bwd(s=None, do=at(1), q=at(2), k=at(3), v=at(4), o=at(5), lse=P, cq=P, ck=P, dq=at(6), dk=at(7), dv=at(8), ws=P, nb=BIG):
+    def bwd(s=None, do=at(1), q=at(2), k=at(3), v=at(4), o=at(5), lse=at(10), cq=P, ck=P, dq=at(6), dk=at(7), dv=at(8), ws=at(11), nb=BIG):
         return lib.attention_backward(ctypes.byref(s or mk()), do, q, k, v, o, lse, cq, ck, dq, dk, dv, ws, nb, None)
 
     shapes = [(dict(n_q=-1), E, b"n_q"), (dict(n_k=1 << 30), E, b"n_k"), (dict(n_seqs=-1), E, b"n_seqs"), (dict(n_seqs=65537), E, b"n_seqs"),
@@ -54,6 +54,16 @@ def test_attention(L):  # noqa: F811
         for n in range(1, 9):
             if n != own:
                 _is(L, bwd(**{out: at(n)}), E, b"overlap")
+    for k in ("lse", "ws"):
+        for n in (1, 2, 3, 4):
+            _is(L, fwd(**{k: at(n)}), E, b"overlaps")
+        _is(L, fwd(**{k: P}), E, b"overlaps")
+    _is(L, fwd(lse=at(11)), E, b"overlaps")
+    for n in range(1, 9):
+        _is(L, bwd(ws=at(n)), E, b"overlaps")
+        if n >= 6:
+            _is(L, bwd(lse=at(n)), E, b"overlap")
+            _is(L, bwd(cq=at(n)), E, b"overlap")
     # slices of one buffer lie between one another: taken; a slice too far: refused
     row = 8 * 64
     s = mk(n_k=100, q_stride=row, k_stride=row, v_stride=row)
@@ -84,7 +94,8 @@ def _bad_kv(L):
 def test_tables(L):  # noqa: F811
     lib, E = L.LIB, L.LORA_E_INVALID_ARG
 
-    def call(s=None, c=P, n=P, sl=at(1), t=P, r=P, st=P, so=P, cu=P, ns=10, slots=P, pos=P, seq=P, ws=P, nb=BIG):
+    def call(s=None, c=at(20), n=at(21), sl=at(1), t=at(2), r=at(3), st=at(22), so=at(4), cu=at(5), ns=10, slots=at(6), pos=at(7), seq=at(8),
+             ws=at(9), nb=BIG):
         return lib.kv_tables(ctypes.byref(s or _kv(L)), c, n, sl, t, r, st, so, cu, ns, slots, pos, seq, ws, nb, None)
 
     for kw, kind in _bad_kv(L):
@@ -99,7 +110,13 @@ def test_tables(L):  # noqa: F811
         _is(L, call(**{k: ctypes.c_void_p(68)}), E, b"aligned")
     _is(L, call(ns=-1), E, b"n_slots")
     _is(L, call(ns=1 << 30), E, b"n_slots")
-    _is(L, call(sl=P), E, b"same buffer")
+    for k in ("sl", "t", "r", "so", "cu", "slots", "pos", "seq", "ws"):
+        for other in (*range(1, 10), 20, 21, 22):
+            own = {"sl": (1, 20), "t": (2,), "r": (3,), "so": (4, 22), "cu": (5,), "slots": (6,), "pos": (7,), "seq": (8,), "ws": (9,)}[k]
+            if other not in own:
+                _is(L, call(**{k: at(other)}), E, b"overlaps")
+    _is(L, call(sl=ctypes.c_void_p((20 << 20) + 4)), E, b"overlaps")       # over cached_lens, but not on it
+    _is(L, call(so=ctypes.c_void_p((22 << 20) + 8)), E, b"overlaps")
     _is(L, call(ws=None), L.LORA_E_WORKSPACE)
     _is(L, call(nb=255), L.LORA_E_WORKSPACE)
     _is(L, call(ws=ODD), E, b"aligned")
@@ -108,7 +125,7 @@ def test_tables(L):  # noqa: F811
 def test_write(L):  # noqa: F811
     lib, E = L.LIB, L.LORA_E_INVALID_ARG
 
-    def call(s=None, n=5, k=at(1), ks=128, v=at(2), vs=128, sl=P, kc=at(3), vc=at(4), sk=None, sv=None, ws=P, nb=256):
+    def call(s=None, n=5, k=at(1), ks=128, v=at(2), vs=128, sl=at(9), kc=at(3), vc=at(4), sk=None, sv=None, ws=at(10), nb=256):
         return lib.kv_write(ctypes.byref(s or _kv(L)), n, k, ks, v, vs, sl, kc, vc, sk, sv, ws, nb, None)
 
     for kw, kind in _bad_kv(L):
@@ -129,13 +146,19 @@ def test_write(L):  # noqa: F811
     for a, b in (("k", 3), ("k", 4), ("v", 3), ("v", 4)):
         _is(L, call(**{a: at(b)}), E, b"overlaps")
     _is(L, call(vc=at(3)), E, b"caches overlap")
+    for n in (1, 2, 3, 4, 9, 10):
+        _is(L, call(sk=at(n), sv=at(6)), E, b"overlap")
+        _is(L, call(sk=at(6), sv=at(n)), E, b"overlap")
+        if n != 10:
+            _is(L, call(ws=at(n)), E, b"overlap")
+    _is(L, call(sl=at(3)), E, b"overlaps slots")
     assert call(n=0, k=None, v=None, sl=None) == L.LORA_OK
 
 
 def test_decode(L):  # noqa: F811
     lib, E = L.LIB, L.LORA_E_INVALID_ARG
 
-    def call(s=None, h=4, q=at(1), qs=256, kc=at(2), vc=at(3), sk=None, sv=None, t=P, ln=P, m=50, sc=0.1, o=at(4), lse=None, ws=P, nb=BIG):
+    def call(s=None, h=4, q=at(1), qs=256, kc=at(2), vc=at(3), sk=None, sv=None, t=at(9), ln=at(10), m=50, sc=0.1, o=at(4), lse=None, ws=at(11), nb=BIG):
         return lib.attention_decode(ctypes.byref(s or _kv(L)), h, q, qs, kc, vc, sk, sv, t, ln, m, sc, o, lse, ws, nb, None)
 
     size = lambda s=None, h=4, m=50: lib.attention_decode_workspace_bytes(ctypes.byref(s or _kv(L)), h, m)  # noqa: E731
@@ -165,6 +188,10 @@ def test_decode(L):  # noqa: F811
     _is(L, call(s=long, m=6400, nb=need - 1), L.LORA_E_WORKSPACE)
     _is(L, call(ws=None), L.LORA_E_WORKSPACE)
     _is(L, call(o=at(1)), E, b"overlaps q")
+    for k in ("o", "lse", "ws"):
+        for n in (2, 3, 9, 10, 4, 11, 6, 7):
+            if (k, n) not in (("o", 4), ("ws", 11)):
+                _is(L, call(**{"sk": at(6), "sv": at(7), k: at(n)}), E, b"overlaps another")
     assert call(s=_kv(L, n_seqs=0), q=None, o=None, t=None, ln=None) == L.LORA_OK
 
 
