@@ -254,7 +254,7 @@ __device__ __forceinline__ f32x16 product_seen(bf16x8 v, bf16x8 p, f32x16 acc, i
 constexpr float AT_SLACK = 6.f;
 
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void attention_fwd_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
   constexpr int TILE = AT_TILE * D * 2;            // bytes of one operand of a stage
   __shared__ __attribute__((aligned(16))) char lds[4 * TILE];
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 // ---------------------------------------------------------------- dq
 // Waves, tiles and stages as in the forward.
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void attention_dq_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
   constexpr int TILE = AT_TILE * D * 2;
   __shared__ __attribute__((aligned(16))) char lds[4 * TILE];

@@ -14,9 +14,9 @@ constexpr float KV_LOG2E = 1.4426950408889634f, KV_LN2 = 0.6931471805599453f;
 // needed, pages put back.  Requests number at most some thousands, so every block sums
 // them itself (a few per thread) and keeps the sums in LDS; then new rows, new table
 // entries and returned pages are independent items, each found by a binary search.  One
-// launch does all where one block suffices.  Else a grid does the items, and a second
-// launch of one block writes what a caller may have passed in place (seq_lens over
-// cached_lens, the state over itself), which no block of the first may see changed.
+// launch does all: of one block, or of a grid where outputs do not lie on inputs.  Where
+// they do (seq_lens over cached_lens, the state over itself) no block of a grid may see
+// them changed, so a second launch of one block writes them.
 constexpr int TAB_THREADS = 1024;
 
 struct TableArgs {
@@ -34,7 +34,7 @@ struct TableArgs {
   int32_t* status;
   int64_t n_slots;
   int32_t n, page_shift, n_pages, max_pages;
-  int32_t items, lengths;   // which halves this launch does
+  int32_t items, lengths;   // which halves this launch does (the second by its first block)
 };
 
 // What one request asks for.
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(TAB_THREADS) void kv_tables_kernel(TableArgs a) {
     }
   }
   if (bad) set_flag(a.status, bad);
-  if (!a.lengths) return;
+  if (!a.lengths || blockIdx.x) return;
   // every thread has read what these overwrite; each rewrites its own requests
   __syncthreads();
   for (int b = b0; b < b1; ++b) {
@@ -688,10 +688,14 @@ lora_status launch_kv_tables(const kv_shape& sh, const int32_t* cached, const in
   }
   const int64_t items = std::max<int64_t>(n_slots, (int64_t)sh.n_seqs * 64);
   const unsigned grid = (unsigned)std::min<int64_t>(cdiv(items, TAB_THREADS), device_cus());
-  a.lengths = 0;
+  const auto meet = [&](const void* p, const void* q, size_t bytes) {
+    return (const char*)p < (const char*)q + bytes && (const char*)q < (const char*)p + bytes;
+  };
+  const bool in_place = meet(seq_lens, cached, 4 * (size_t)sh.n_seqs) || meet(state_out, state, 16);
+  a.lengths = !in_place;
   hipLaunchKernelGGL(kv_tables_kernel, dim3(grid), dim3(TAB_THREADS), lds, s, a);
   lora_status st = launch_check("kv_tables");
-  if (st != LORA_OK) return st;
+  if (st != LORA_OK || !in_place) return st;
   a.lengths = 1;
   a.items = 0;
   hipLaunchKernelGGL(kv_tables_kernel, dim3(1), dim3(TAB_THREADS), lds, s, a);

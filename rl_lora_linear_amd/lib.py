@@ -689,24 +689,25 @@ def attention_workspace_bytes(shape: AttnShape) -> int:
     return n
 
 
-def _rows(t, n, heads, d, stride, name: str, dev: int):
-    """The pointer of rows of [heads][d] in bf16 whose tokens lie stride elements apart."""
-    if t.dtype != torch.bfloat16 or t.shape != (n, heads, d) or \
-            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or (n > 1 and t.stride(0) != stride))):
-        raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs torch.bfloat16 {(n, heads, d)} with strides {(stride, d, 1)}, "
-                        f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+def _rows(t, shape, strides, name: str, dev: int):
+    """The pointer of rows of [heads][d] in bf16 whose tokens lie strides[0] elements apart."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.stride() != strides:
+        n, heads, d = shape
+        if t.dtype != torch.bfloat16 or t.shape != shape or \
+                (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or (n > 1 and t.stride(0) != strides[0]))):
+            raise LoraError(LORA_E_INVALID_ARG, f"{name}: needs torch.bfloat16 {shape} with strides {strides}, "
+                            f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
     if t.get_device() != dev or dev < 0:
         _on_device(t, name, dev)
     return t.data_ptr()
 
 
 def _attn_args(s, q, k, v, cu_q, cu_k, o, lse, dev):
-    return (_rows(q, s.n_q, s.n_heads, s.head_dim, s.q_stride, "q", dev),
-            _rows(k, s.n_k, s.n_kv_heads, s.head_dim, s.k_stride, "k", dev),
-            _rows(v, s.n_k, s.n_kv_heads, s.head_dim, s.v_stride, "v", dev),
-            _dense(cu_q, _I32T, (s.n_seqs + 1,), "cu_q", dev), _dense(cu_k, _I32T, (s.n_seqs + 1,), "cu_k", dev),
-            _rows(o, s.n_q, s.n_heads, s.head_dim, s.o_stride, "o", dev),
-            _dense(lse, _F32, (s.n_heads, s.n_q), "lse", dev))
+    d = s.head_dim
+    qs, ks, cu = (s.n_q, s.n_heads, d), (s.n_k, s.n_kv_heads, d), (s.n_seqs + 1,)
+    return (_rows(q, qs, (s.q_stride, d, 1), "q", dev), _rows(k, ks, (s.k_stride, d, 1), "k", dev),
+            _rows(v, ks, (s.v_stride, d, 1), "v", dev), _dense(cu_q, _I32T, cu, "cu_q", dev), _dense(cu_k, _I32T, cu, "cu_k", dev),
+            _rows(o, qs, (s.o_stride, d, 1), "o", dev), _dense(lse, _F32, (s.n_heads, s.n_q), "lse", dev))
 
 
 def attention_forward(shape: AttnShape, q, k, v, cu_q, cu_k, o, lse, ws, stream=None):
@@ -720,13 +721,13 @@ def attention_forward(shape: AttnShape, q, k, v, cu_q, cu_k, o, lse, ws, stream=
 
 def attention_backward(shape: AttnShape, dout, q, k, v, o, lse, cu_q, cu_k, dq, dk, dv, ws, stream=None):
     """dq, dk, dv with the shapes and strides of q, k, v; o and lse from the forward."""
-    s, dev = shape, q.get_device()
+    s, dev, d = shape, q.get_device(), shape.head_dim
     pq, pk, pv, cq, ck, po, pl = _attn_args(s, q, k, v, cu_q, cu_k, o, lse, dev)
-    _check(LIB.attention_backward(ctypes.byref(s), _rows(dout, s.n_q, s.n_heads, s.head_dim, s.o_stride, "dout", dev),
-                                  pq, pk, pv, po, pl, cq, ck, _rows(dq, s.n_q, s.n_heads, s.head_dim, s.q_stride, "dq", dev),
-                                  _rows(dk, s.n_k, s.n_kv_heads, s.head_dim, s.k_stride, "dk", dev),
-                                  _rows(dv, s.n_k, s.n_kv_heads, s.head_dim, s.v_stride, "dv", dev),
-                                  _device_ptr(ws, "ws", dev), ws.nbytes, _stream_for(q, stream)))
+    qs, ks = (s.n_q, s.n_heads, d), (s.n_k, s.n_kv_heads, d)
+    _check(LIB.attention_backward(ctypes.byref(s), _rows(dout, qs, (s.o_stride, d, 1), "dout", dev), pq, pk, pv, po, pl, cq, ck,
+                                  _rows(dq, qs, (s.q_stride, d, 1), "dq", dev), _rows(dk, ks, (s.k_stride, d, 1), "dk", dev),
+                                  _rows(dv, ks, (s.v_stride, d, 1), "dv", dev), _device_ptr(ws, "ws", dev), ws.nbytes,
+                                  _stream_for(q, stream)))
 
 
 def make_kv_shape(n_seqs, n_kv_heads, head_dim, page_size, n_pages, max_pages) -> KvShape:
@@ -768,12 +769,14 @@ def _cache_args(s, k_cache, v_cache, k_scales, v_scales, dev):
 def kv_write(shape: KvShape, k, v, slots, k_cache, v_cache, ws, k_scales=None, v_scales=None, stream=None):
     """Rows t of k and v [n][n_kv_heads][head_dim] to slot slots[t] of the caches
     [n_pages][n_kv_heads][page_size][head_dim]: bf16, or e4m3 codes with E8M0 scales [..][head_dim/32]."""
-    s, n, dev = shape, slots.numel(), k.get_device()
-    ks, vs = (t.stride(0) if n > 1 else s.n_kv_heads * s.head_dim for t in (k, v))
+    s, n, dev, d = shape, slots.numel(), k.get_device(), shape.head_dim
+    row = s.n_kv_heads * d
+    ks, vs = (k.stride(0), v.stride(0)) if n > 1 else (row, row)
+    rows = (n, s.n_kv_heads, d)
     kc, vc, sk, sv = _cache_args(s, k_cache, v_cache, k_scales, v_scales, dev)
-    _check(LIB.kv_write(ctypes.byref(s), n, _rows(k, n, s.n_kv_heads, s.head_dim, ks, "k", dev), ks,
-                        _rows(v, n, s.n_kv_heads, s.head_dim, vs, "v", dev), vs, _dense(slots, _I32T, (n,), "slots", dev),
-                        kc, vc, sk, sv, _device_ptr(ws, "ws", dev), ws.nbytes, _stream_for(k, stream)))
+    _check(LIB.kv_write(ctypes.byref(s), n, _rows(k, rows, (ks, d, 1), "k", dev), ks, _rows(v, rows, (vs, d, 1), "v", dev), vs,
+                        _dense(slots, _I32T, (n,), "slots", dev), kc, vc, sk, sv, _device_ptr(ws, "ws", dev), ws.nbytes,
+                        _stream_for(k, stream)))
 
 
 def attention_decode_workspace_bytes(shape: KvShape, n_heads, max_len) -> int:
@@ -792,7 +795,7 @@ def attention_decode(shape: KvShape, q, k_cache, v_cache, block_table, seq_lens,
     heads = q.shape[1]
     stride = q.stride(0) if s.n_seqs > 1 else heads * s.head_dim
     kc, vc, sk, sv = _cache_args(s, k_cache, v_cache, k_scales, v_scales, dev)
-    _check(LIB.attention_decode(ctypes.byref(s), heads, _rows(q, s.n_seqs, heads, s.head_dim, stride, "q", dev), stride, kc, vc,
+    _check(LIB.attention_decode(ctypes.byref(s), heads, _rows(q, (s.n_seqs, heads, s.head_dim), (stride, s.head_dim, 1), "q", dev), stride, kc, vc,
                                 sk, sv, _dense(block_table, _I32T, (s.n_seqs, s.max_pages), "block_table", dev),
                                 _dense(seq_lens, _I32T, (s.n_seqs,), "seq_lens", dev), max_len, scale,
                                 _dense(o, _BF16, (s.n_seqs, heads, s.head_dim), "o", dev),
