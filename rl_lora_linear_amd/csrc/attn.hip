@@ -334,8 +334,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 #pragma unroll
     for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(top, x[0][r]), x[1][r]);
     top = fmaxf(top, __shfl_xor(top, 32, kWave)) * c;
-    if (__any(top > ref + AT_SLACK)) {
-      const float next = fmaxf(ref, top), scale = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ref - next);
+    // (each row by its own scores alone: no other query's keys show in its bits)
+    const bool rise = top > ref + AT_SLACK;
+    if (__any(rise)) {
+      const float next = rise ? top : ref, scale = rise ? __builtin_amdgcn_exp2f(ref - next) : 1.f;
       ref = next;
       sum *= scale;
 #pragma unroll

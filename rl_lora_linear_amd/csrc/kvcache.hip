@@ -514,8 +514,9 @@ __global__ __launch_bounds__(64 * DEC_WAVES, X8 ? 3 : 2) void decode_kernel(Deco
     float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])), fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
     top = fmaxf(top, __shfl_xor(top, 16, kWave));
     top = fmaxf(top, __shfl_xor(top, 32, kWave)) * a.scale_log2;
-    if (__any(top > m + DEC_SLACK)) {
-      const float next = fmaxf(m, top), keep = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - next);
+    const bool rise = top > m + DEC_SLACK;
+    if (__any(rise)) {
+      const float next = rise ? top : m, keep = rise ? __builtin_amdgcn_exp2f(m - next) : 1.f;
       m = next;
       sum *= keep;
 #pragma unroll

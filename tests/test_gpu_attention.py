@@ -237,6 +237,23 @@ def test_later_keys_never_reach_a_query(value, d):
             assert np.all(got[at:200, :, 5] == value)
 
 
+@pytest.mark.parametrize("d,heads,kv", [(64, 2, 1), (128, 4, 2), (128, 3, 3)])
+def test_later_keys_never_show_in_a_query_s_bits(d, heads, kv):
+    """Finite keys of any size behind a query: they raise the running maxima of the rows next to it."""
+    c = Case([300, 130], heads=heads, kv=kv, d=d, seed=18)
+    o, lse = c.forward()
+    for at in (1, 40, 100, 131, 260):
+        k, v = c.dev[1].clone(), c.dev[2].clone()
+        k[at:300] *= 30
+        v[at:300] *= -7
+        o2, lse2 = torch.full_like(c.o, NAN), torch.full_like(c.lse, NAN)
+        L.attention_forward(c.shape, c.dev[0], k, v, c.cq, c.ck, o2, lse2, c.ws)
+        o2, lse2 = f64_of(o2), f64_of(lse2)
+        assert np.array_equal(o2[:at], o[:at]) and np.array_equal(lse2[:, :at], lse[:, :at]), at
+        assert not np.array_equal(o2[at:300], o[at:300])
+        assert np.array_equal(o2[300:], o[300:]) and np.array_equal(lse2[:, 300:], lse[:, 300:]), at
+
+
 def test_a_sequence_s_nan_stays_its_own():
     c = Case([100, 90, 130], heads=4, kv=2, d=128, seed=15)
     c.forward()
