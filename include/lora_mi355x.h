@@ -648,8 +648,8 @@ lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table,
  * A query that sees no key (Lk < Lq, Lk = 0) has o = 0 and lse = -inf.  Products and
  * sums are fp32; the weights exp(.) enter the second product as bf16.  A sequence's
  * o and lse have the same bits whatever else the batch holds, and depend on nothing
- * outside its rows; with causal, o_i and lse_i depend on keys that query i sees only,
- * also where others hold NaN or Inf. */
+ * outside its rows; with causal, the bits of o_i and lse_i depend on keys that query i
+ * sees only, also where others hold NaN or Inf. */
 typedef struct {        /* host struct */
   int64_t n_q;          /* rows of q, o; 0 .. 2^30 - 1 */
   int64_t n_k;          /* rows of k, v; 0 .. 2^30 - 1 */
@@ -662,7 +662,7 @@ typedef struct {        /* host struct */
   int32_t n_kv_heads;   /* >= 1 */
   int32_t head_dim;     /* 64 or 128 */
   int32_t causal;       /* 0 or 1 */
-  float scale;          /* finite */
+  float scale;          /* |scale| < 2^127 */
 } attn_shape;
 
 /* Workspace of the two calls below; word 0 is the status word.  0 on an invalid shape. */
@@ -673,7 +673,8 @@ size_t attention_workspace_bytes(const attn_shape* shape);
  *   projection's output are taken as they are.  All 16-byte aligned.
  *   cu_q, cu_k int32 [n_seqs+1], not decreasing, within [0, n_q] and [0, n_k]; may be
  *              one array.  A sequence that breaks this sets LORA_FLAG_BAD_LENGTH and is
- *              left out.
+ *              left out; parts of others may be then, too (the blocks find their sequence
+ *              by the order of the offsets).
  *   o   bf16 [n_q] rows of [n_heads][head_dim] out, must not overlap q, k or v
  *   lse fp32 [n_heads][n_q] out; it and ws must not overlap another operand
  * Rows of o and lse that belong to no sequence are left as they were. */
@@ -781,7 +782,7 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
  *        8, >= n_heads * head_dim, < 2^31)
  *   block_table int32 [n_seqs][max_pages], seq_lens int32 [n_seqs] as kv_tables leaves
  *        them.  seq_len 0: o = 0 and lse = -inf.
- *   max_len  an upper bound of the lengths (0 .. max_pages * page_size), which sizes the
+ *   max_len  an upper bound of the lengths (0 .. max_pages * page_size, at most 2^30), which sizes the
  *        launch: a step captured with the longest length to come serves every step.  A
  *        length outside [0, max_len] counts as 0 and sets LORA_FLAG_BAD_LENGTH; rows of
  *        a page out of range are left out, with LORA_FLAG_BAD_PAGE.

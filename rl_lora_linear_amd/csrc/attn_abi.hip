@@ -59,6 +59,9 @@ bool rows_meet(const void* a, int64_t a_rows, int64_t a_stride, int64_t a_cols, 
   return gap < a_cols * 2 || gap + b_cols * 2 > row;
 }
 
+// (the kernels multiply it by log2 e)
+bool scale_ok(float s) { return std::fabs(s) < 0x1p127f; }
+
 lora_status check_attn(const attn_shape* p, const char* what) {
   LORA_ARG_CHECK(p != nullptr, "%s: shape is NULL", what);
   const attn_shape& s = *p;
@@ -68,7 +71,7 @@ lora_status check_attn(const attn_shape* p, const char* what) {
   LORA_ARG_CHECK(s.n_kv_heads >= 1 && s.n_heads >= 1 && s.n_heads <= 1024 && s.n_heads % s.n_kv_heads == 0,
                  "%s: n_heads %d must be a multiple of n_kv_heads %d, at most 1024", what, s.n_heads, s.n_kv_heads);
   LORA_ARG_CHECK(s.causal == 0 || s.causal == 1, "%s: causal must be 0 or 1", what);
-  LORA_ARG_CHECK(std::isfinite(s.scale), "%s: scale must be finite", what);
+  LORA_ARG_CHECK(scale_ok(s.scale), "%s: scale must be below 2^127 in magnitude", what);
   if (s.head_dim != 64 && s.head_dim != 128) return unsupported(what, "head_dim must be 64 or 128");
   const int64_t q = (int64_t)s.n_heads * s.head_dim, k = (int64_t)s.n_kv_heads * s.head_dim;
   for (int64_t st : {s.q_stride, s.k_stride, s.v_stride, s.o_stride})
@@ -76,8 +79,9 @@ lora_status check_attn(const attn_shape* p, const char* what) {
                    what, (long long)st);
   LORA_ARG_CHECK(s.q_stride >= q && s.o_stride >= q && s.k_stride >= k && s.v_stride >= k,
                  "%s: a stride is shorter than its row", what);
-  // a launch takes fewer than 2^32 threads
-  if ((s.n_q / 128 + s.n_seqs + 1) * s.n_heads >= (1 << 24) - 1 || (s.n_k / 128 + s.n_seqs + 1) * s.n_kv_heads >= (1 << 24) - 1)
+  // a launch takes fewer than 2^32 threads, and a block has 512
+  const auto fits = [&](int64_t rows, int64_t heads) { return (rows / 128 + s.n_seqs + 1) * heads < (1 << 23); };
+  if (!fits(s.n_q, s.n_heads) || !fits(s.n_k, s.n_kv_heads))
     return unsupported(what, "too many rows times heads for one launch");
   return LORA_OK;
 }
@@ -137,6 +141,7 @@ lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const 
   LORA_ARG_CHECK(s.n_seqs == 0 || (cu_q && cu_k), "attention_forward: cu_q and cu_k must be non-NULL");
   LORA_ARG_CHECK(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(o),
                  "attention_forward: q, k, v and o must be 16-byte aligned");
+  LORA_ARG_CHECK(aligned(lse, 4) && aligned(cu_q, 4) && aligned(cu_k, 4), "attention_forward: lse, cu_q and cu_k must be 4-byte aligned");
   TRY(check_ws(ws, ws_bytes, attn_ws(s), "attention_forward"));
   const int64_t qc = (int64_t)s.n_heads * s.head_dim, kc = (int64_t)s.n_kv_heads * s.head_dim;
   LORA_ARG_CHECK(!rows_meet(o, s.n_q, s.o_stride, qc, q, s.n_q, s.q_stride, qc) &&
@@ -165,6 +170,7 @@ lora_status attention_backward(const attn_shape* shape, const uint16_t* dout, co
   for (const void* p : {(const void*)dout, (const void*)q, (const void*)k, (const void*)v, (const void*)o,
                         (const void*)dq, (const void*)dk, (const void*)dv})
     LORA_ARG_CHECK(aligned16(p), "attention_backward: bf16 operands must be 16-byte aligned");
+  LORA_ARG_CHECK(aligned(lse, 4) && aligned(cu_q, 4) && aligned(cu_k, 4), "attention_backward: lse, cu_q and cu_k must be 4-byte aligned");
   TRY(check_ws(ws, ws_bytes, attn_ws(s), "attention_backward"));
   const int64_t qc = (int64_t)s.n_heads * s.head_dim, kc = (int64_t)s.n_kv_heads * s.head_dim;
   struct Rows {
@@ -271,6 +277,7 @@ static lora_status check_decode(const kv_shape* shape, int32_t n_heads, int64_t 
                  "attention_decode: n_heads %d must be a multiple of n_kv_heads %d, at most 1024", n_heads, s.n_kv_heads);
   LORA_ARG_CHECK(max_len >= 0 && max_len <= (int64_t)s.max_pages * s.page_size,
                  "attention_decode: max_len %lld outside [0, max_pages * page_size]", (long long)max_len);
+  if (max_len > (1 << 30)) return unsupported("attention_decode", "max_len must not pass 2^30");
   // a launch takes fewer than 2^32 threads
   if ((int64_t)s.n_seqs * 32 * s.n_kv_heads * cdiv(n_heads / s.n_kv_heads, 16) >= 1 << 24)
     return unsupported("attention_decode", "too many requests times heads for one launch");
@@ -291,7 +298,7 @@ lora_status attention_decode(const kv_shape* shape, int32_t n_heads, const uint1
   TRY(check_decode(shape, n_heads, max_len));
   const kv_shape& s = *shape;
   const int64_t cols = (int64_t)n_heads * s.head_dim;
-  LORA_ARG_CHECK(std::isfinite(scale), "attention_decode: scale must be finite");
+  LORA_ARG_CHECK(scale_ok(scale), "attention_decode: scale must be below 2^127 in magnitude");
   LORA_ARG_CHECK(s.n_seqs == 0 || (q && o && block_table && seq_lens),
                  "attention_decode: q, o, block_table and seq_lens must be non-NULL");
   LORA_ARG_CHECK(aligned16(q) && aligned16(o), "attention_decode: q and o must be 16-byte aligned");

@@ -27,10 +27,11 @@ def test_attention(L):  # noqa: F811
     shapes = [(dict(n_q=-1), E, b"n_q"), (dict(n_k=1 << 30), E, b"n_k"), (dict(n_seqs=-1), E, b"n_seqs"), (dict(n_seqs=65537), E, b"n_seqs"),
               (dict(n_heads=3), E, b"multiple"), (dict(n_heads=0), E, b"multiple"), (dict(n_kv_heads=0), E, b"multiple"),
               (dict(n_heads=1026), E, b"1024"), (dict(head_dim=80), L.LORA_E_UNSUPPORTED, b"64 or 128"), (dict(head_dim=256), L.LORA_E_UNSUPPORTED, b"64 or 128"),
-              (dict(scale=float("nan")), E, b"scale"), (dict(scale=float("inf")), E, b"scale"), (dict(causal=2), E, b"causal"),
+              (dict(scale=float("nan")), E, b"scale"), (dict(scale=float("inf")), E, b"scale"), (dict(scale=-(2.0 ** 127)), E, b"scale"), (dict(causal=2), E, b"causal"),
               (dict(q_stride=255), E, b"multiple of 8"), (dict(q_stride=248), E, b"shorter"), (dict(k_stride=120), E, b"shorter"),
               (dict(v_stride=-8), E, b"shorter"), (dict(o_stride=1 << 24), E, b"2^24"),
-              (dict(n_q=(1 << 30) - 1, n_heads=1024, n_kv_heads=2), L.LORA_E_UNSUPPORTED, b"one launch")]
+              (dict(n_q=(1 << 30) - 1, n_heads=1024, n_kv_heads=2), L.LORA_E_UNSUPPORTED, b"one launch"),
+              (dict(n_seqs=65536, n_heads=128, n_kv_heads=128, q_stride=128 * 64, k_stride=128 * 64, v_stride=128 * 64, o_stride=128 * 64), L.LORA_E_UNSUPPORTED, b"one launch")]
     for kw, kind, word in shapes:
         s = mk(**kw)
         assert lib.attention_workspace_bytes(ctypes.byref(s)) == 0
@@ -45,7 +46,10 @@ def test_attention(L):  # noqa: F811
         _is(L, fwd(**{k: ODD}), E, b"aligned")
     for k in ("do", "q", "k", "v", "o", "dq", "dk", "dv", "ws"):
         _is(L, bwd(**{k: ODD}), E, b"aligned")
+    odd4 = ctypes.c_void_p((12 << 20) + 2)
     for f in (fwd, bwd):
+        for k in ("lse", "cq", "ck"):
+            _is(L, f(**{k: odd4}), E, b"4-byte aligned")
         _is(L, f(ws=None), L.LORA_E_WORKSPACE)
         _is(L, f(nb=need - 1), L.LORA_E_WORKSPACE)
     for k in ("q", "k", "v"):
@@ -181,6 +185,10 @@ def test_decode(L):  # noqa: F811
     for st in (248, 260, 1 << 31):
         _is(L, call(qs=st), E, b"q_stride")
     _is(L, call(sc=float("inf")), E, b"scale")
+    _is(L, call(sc=-(2.0 ** 127)), E, b"scale")
+    far = _kv(L, page_size=256, max_pages=(1 << 22) + 1)
+    assert size(far, m=1 << 30) > 0 and size(far, m=(1 << 30) + 1) == 0
+    _is(L, call(s=far, m=(1 << 30) + 1), L.LORA_E_UNSUPPORTED, b"2^30")
     _is(L, call(sk=at(6)), E, b"go together")
     long = _kv(L, max_pages=400)
     need = size(s=long, m=6400)
