@@ -41,14 +41,53 @@ struct AttnArgs {
   float scale, scale_log2;
 };
 
-// Tiles of a packed batch: sequence b owns the tile numbers from cu[b] / rows + b on
-// (rounded down), which leaves room for its last, partial tile; a number behind its last
-// tile is empty.  So a block finds its sequence from cu alone.
+// A block's sequence and tile of 2^shift rows, from its number and the offsets alone: the
+// n_rows / 2^shift + n_seqs numbers of a launch are enough for any offsets, and a number that
+// is left over has nothing to do.
 struct AttnSeq {
   int64_t q0, k0;
   int lq, lk, tile;   // tile < 0: nothing to do
 };
-__device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_t* cu, int id, int shift) {
+__device__ __forceinline__ bool read_sequence(const AttnArgs& a, int b, AttnSeq& s) {
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+  s = {q0, k0, q1 - q0, k1 - k0, -1};
+  return q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
+}
+// Up to 16 sequences, one to a lane: the one with the most rows on the other side first, and
+// its tiles with the most work first (of keys the first tiles, of queries the last), so that
+// the launch does not end on a long block.  Each lane sums the tiles of the sequences before
+// its own.  (4096 tokens of 8: forward 54 -> 49 us; with 64 sequences the sums cost more than
+// the order gives, 8192 tokens of 64: 35 -> 50 us.)
+constexpr int AT_SORTED = 16;
+template <bool KEYS>
+__device__ __forceinline__ AttnSeq find_sorted(const AttnArgs& a, int id, int shift) {
+  const int lane = threadIdx.x & 63;
+  AttnSeq s{0, 0, 0, 0, -1};
+  int tiles = 0, work = 0;
+  if (lane < a.n_seqs && read_sequence(a, lane, s))
+    tiles = ((KEYS ? s.lk : s.lq) + (1 << shift) - 1) >> shift, work = KEYS ? s.lq : s.lk;
+  int first = 0;
+  for (int j = 0; j < a.n_seqs; ++j) {
+    const int t = __builtin_amdgcn_readlane(tiles, j), w = __builtin_amdgcn_readlane(work, j);
+    if (w > work || (w == work && j < lane)) first += t;
+  }
+  const int n = id - first;
+  const uint64_t mine = __ballot(n >= 0 && n < tiles);
+  if (!mine) return {0, 0, 0, 0, -1};
+  const int b = __builtin_ctzll(mine);
+  s.tile = KEYS ? n : tiles - 1 - n;
+  s.q0 = __builtin_amdgcn_readlane((int)s.q0, b), s.k0 = __builtin_amdgcn_readlane((int)s.k0, b);
+  s.lq = __builtin_amdgcn_readlane(s.lq, b), s.lk = __builtin_amdgcn_readlane(s.lk, b);
+  s.tile = __builtin_amdgcn_readlane(s.tile, b);
+  return s;
+}
+// Any number of them: sequence b owns the numbers from cu[b] / 2^shift + b on (rounded down),
+// which leaves room for its last, partial tile; a number behind its last tile is empty.
+template <bool KEYS>
+__device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, int id, int shift) {
+  if (a.n_seqs <= AT_SORTED) return find_sorted<KEYS>(a, id, shift);
+  if (!KEYS) id = a.tiles - 1 - id;
+  const int32_t* const cu = KEYS ? a.cu_k : a.cu_q;
   const int lane = threadIdx.x & 63;
   const auto first = [&](int b) { return (cu[b] >> shift) + b; };
   int lo = 0, end = a.n_seqs;
@@ -59,13 +98,11 @@ __device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_
     lo += (63 - __clzll(m)) * step;
     end = min(end, lo + step);
   }
-  AttnSeq s{0, 0, 0, 0, -1};
+  AttnSeq s;
   const int b = __builtin_amdgcn_readfirstlane(lo);
-  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-  if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) return s;
-  s.q0 = q0, s.k0 = k0, s.lq = q1 - q0, s.lk = k1 - k0;
+  if (!read_sequence(a, b, s)) return s;
   s.tile = id - first(b);
-  if (s.tile < 0 || (int64_t)s.tile << shift >= (cu == a.cu_q ? s.lq : s.lk)) s.tile = -1;
+  if (s.tile < 0 || (int64_t)s.tile << shift >= (KEYS ? s.lk : s.lq)) s.tile = -1;
   return s;
 }
 
@@ -73,8 +110,8 @@ __device__ __forceinline__ AttnSeq find_sequence(const AttnArgs& a, const int32_
 __device__ __forceinline__ void check_sequences(const AttnArgs& a) {
   bool bad = false;
   for (int b = threadIdx.x; b < a.n_seqs; b += blockDim.x) {
-    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-    bad |= q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k;
+    AttnSeq s;
+    bad |= !read_sequence(a, b, s);
   }
   if (bad) set_flag(a.status, LORA_FLAG_BAD_LENGTH);
 }
@@ -265,7 +302,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int per_block = NW / a.wpr, columns = a.n_heads / per_block;   // heads of a block; blocks of a row tile
   const int hx = blockIdx.x % columns, kvh = hx % a.n_kv;
   const int head = kvh * a.group + hx / a.n_kv * per_block + wave / a.wpr;
-  const AttnSeq s = find_sequence(a, a.cu_q, a.tiles - 1 - blockIdx.x / columns, a.shift);
+  const AttnSeq s = find_sequence<false>(a, blockIdx.x / columns, a.shift);
   if (s.tile < 0) return;
   const int row0 = s.tile << a.shift, w0 = row0 + wave % a.wpr * 32, i = w0 + l;   // query row
   const int ahead = s.lk - s.lq;
@@ -284,6 +321,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     dma_tile<D, NW>(vp, a.v_stride, t * AT_TILE, s.lk, lds0 + st * 2 * TILE + TILE, wave, lane);
   };
 
+  if (threadIdx.x < 2) odd_tile[threadIdx.x] = 0;
+  if (tiles) stage(0, 0);   // (on its way while q's rows are)
   // a negative scale turns q's signs, a scale of 0 makes q 0: the maximum of the products
   // is then that of the scores
   bf16x8 qf[NK];
@@ -298,9 +337,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     }
   }
   settle(qf);
-  if (threadIdx.x < 2) odd_tile[threadIdx.x] = 0;
   __syncthreads();
-  if (tiles) stage(0, 0);
   f32x16 acc[ND];
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
@@ -417,7 +454,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int per_block = NW / a.wpr, columns = a.n_heads / per_block;
   const int hx = blockIdx.x % columns, kvh = hx % a.n_kv;
   const int head = kvh * a.group + hx / a.n_kv * per_block + wave / a.wpr;
-  const AttnSeq s = find_sequence(a, a.cu_q, a.tiles - 1 - blockIdx.x / columns, a.shift);
+  const AttnSeq s = find_sequence<false>(a, blockIdx.x / columns, a.shift);
   if (s.tile < 0) return;
   const int row0 = s.tile << a.shift, w0 = row0 + wave % a.wpr * 32, i = w0 + l;
   const int ahead = s.lk - s.lq;
@@ -434,6 +471,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     dma_tile<D, NW>(kp, a.k_stride, t * AT_TILE, s.lk, lds0 + st * 2 * TILE, wave, lane);
     dma_tile<D, NW>(vp, a.v_stride, t * AT_TILE, s.lk, lds0 + st * 2 * TILE + TILE, wave, lane);
   };
+  if (tiles) stage(0, 0);
   const int64_t row = s.q0 + min(i, s.lq - 1);
   bf16x8 qf[NK], df[NK];
   load_rows<D>(qf, a.q + row * a.q_stride + head * D, h);
@@ -452,7 +490,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   settle(df);
   const float lse = a.lse[head * a.n_q + row] * AT_LOG2E;
   if (i < s.lq) a.stats[((int64_t)head * 2 + h) * a.n_q + row] = h ? delta : lse;
-  if (tiles) stage(0, 0);
   f32x16 acc[ND];
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
@@ -539,8 +576,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 31, h = lane >> 5, phase = wave / KW, kw = wave % KW;
   const int kvh = blockIdx.x % a.n_kv;
-  // the first keys are seen by the most queries
-  const AttnSeq s = find_sequence(a, a.cu_k, blockIdx.x / a.n_kv, a.shift);
+  const AttnSeq s = find_sequence<true>(a, blockIdx.x / a.n_kv, a.shift);
   if (s.tile < 0) return;
   const int row0 = s.tile << a.shift, w0 = row0 + kw * 32, j = w0 + l;   // key row
   const int ahead = s.lk - s.lq;
@@ -571,12 +607,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
     dma4_at(a.stats + ((int64_t)head * 2 + h) * a.n_q + s.q0 + min(t0 + l, s.lq - 1), stats0 + st * (int)sizeof(stats[0][0]));
     skip(ask, P);
   };
-  bf16x8 kf[NK], vf[NK];
-  const int64_t row = s.k0 + min(j, s.lk - 1);
-  load_rows<D>(kf, a.k + row * a.k_stride + kvh * D, h);
-  load_rows<D>(vf, a.v + row * a.v_stride + kvh * D, h);
-  settle(kf);
-  settle(vf);
   At now{0, begin};
   if (per_head) {
     skip(now, phase);
@@ -584,6 +614,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) stage(i);
   }
+  bf16x8 kf[NK], vf[NK];
+  const int64_t row = s.k0 + min(j, s.lk - 1);
+  load_rows<D>(kf, a.k + row * a.k_stride + kvh * D, h);
+  load_rows<D>(vf, a.v + row * a.v_stride + kvh * D, h);
+  settle(kf);
+  settle(vf);
   f32x16 dk[ND], dv[ND];
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
@@ -697,8 +733,13 @@ static AttnArgs attn_args(const attn_shape& sh, const uint16_t* q, const uint16_
   return a;
 }
 
-// The blocks of the kernels whose waves own queries: eight waves (two heads of a group by
-// 128 rows, or 256 rows) where that leaves a block for each CU, else four.
+// The blocks of the kernels whose waves own queries.  Four waves, 128 rows of a head: two
+// such blocks share a CU and fill each other's waits at a block's start and end.  Eight (two
+// heads of a group by 128 rows, or 256 rows): a tile that comes through LDS serves twice the
+// queries, which pays where blocks live long.  Forward, four / eight waves, us:
+//   16384 tokens, 32 heads of 128       2057 / 1982      4096 tokens             157 / 148
+//   2048 tokens                           53 /   61      8192 tokens of 16       101 / 108
+//   8192 tokens of 6                     165 /  164      10010 of 8, heads of 64  92 /  97
 struct QueryGrid {
   dim3 blocks;
   int waves;
@@ -707,7 +748,8 @@ static QueryGrid query_grid(AttnArgs& a, const attn_shape& sh) {
   const auto tiles = [&](int shift) { return (sh.n_q >> shift) + sh.n_seqs; };
   int waves = 8, heads = a.group % 2 == 0 ? 2 : 1;
   a.shift = heads == 2 ? 7 : 8;
-  if (tiles(a.shift) * (a.n_heads / heads) < device_cus()) waves = 4, heads = 1, a.shift = 7;
+  const bool few = tiles(a.shift) * (a.n_heads / heads) < 2 * device_cus();
+  if (few || sh.n_q / 2048 < sh.n_seqs) waves = 4, heads = 1, a.shift = 7;
   a.wpr = waves / heads;
   a.tiles = (int)tiles(a.shift);
   return {dim3((unsigned)((int64_t)a.tiles * (a.n_heads / heads))), waves};
@@ -738,16 +780,29 @@ lora_status launch_attention_bwd(const attn_shape& sh, const uint16_t* dout, con
   else g.waves == 8 ? go_q(attention_dq_kernel<64, 8>) : go_q(attention_dq_kernel<64, 4>);
   lora_status st = launch_check("attention_backward dq");
   if (st != LORA_OK) return st;
-  // 128 keys a block where that leaves a block for each CU, else 32
+  // Keys of a block, by the blocks that 128 of them make.  128: each tile that comes through
+  // LDS serves most keys; 64 and 32: the longest block, which a causal batch may end up
+  // waiting for, is half and a quarter as long.  Whole backward, 128 / 64 / 32 keys, us:
+  //   16384 tokens, 8 key heads (1032 blocks)    6890 / 7028 / 8566
+  //   4096 tokens, 32 key heads (1056)            476 /  537 /  695
+  //   8192 tokens of 16, 8 key heads (640)        479 /  426 /  502
+  //   4096 tokens, 8 key heads (264)              622 /  476 /  573
+  //   4096 tokens of 8, 4 key heads (160)         390 /  256 /  205
+  //   2048 tokens, 8 key heads (136)              297 /  207 /  189
   const auto key_blocks = [&](int shift) { return ((sh.n_k >> shift) + sh.n_seqs) * sh.n_kv_heads; };
-  const bool wide = key_blocks(7) >= 2 * device_cus();
-  a.shift = wide ? 7 : 5;
+  a.shift = key_blocks(7) >= 4 * device_cus() ? 7 : key_blocks(7) >= device_cus() ? 6 : 5;
   a.tiles = (int)((sh.n_k >> a.shift) + sh.n_seqs);
   const auto go_k = [&](auto kernel, int waves) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)key_blocks(a.shift)), dim3(64 * waves), 0, s, a);
   };
-  if (sh.head_dim == 128) wide ? go_k(attention_dkv_kernel<128, 8, 4, 2>, 8) : go_k(attention_dkv_kernel<128, 4, 1, 2>, 4);
-  else wide ? go_k(attention_dkv_kernel<64, 8, 4, 2>, 8) : go_k(attention_dkv_kernel<64, 4, 1, 2>, 4);
+  const auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    a.shift == 7   ? go_k(attention_dkv_kernel<D, 8, 4, 2>, 8)
+    : a.shift == 6 ? go_k(attention_dkv_kernel<D, 8, 2, 2>, 8)
+                   : go_k(attention_dkv_kernel<D, 4, 1, 2>, 4);
+  };
+  if (sh.head_dim == 128) pick(std::integral_constant<int, 128>{});
+  else pick(std::integral_constant<int, 64>{});
   return launch_check("attention_backward dk, dv");
 }
 

@@ -283,10 +283,9 @@ def test_same_bits_in_every_batch_and_call():
         assert np.array_equal(one.backward()[0], ref[0][s])
 
 
-@pytest.mark.parametrize("d,heads,kv", [(128, 8, 4), (64, 9, 3), (128, 5, 5)])
+@pytest.mark.parametrize("d,heads,kv", [(128, 8, 4), (64, 9, 3), (128, 5, 5), (64, 8, 4), (128, 6, 1)])
 def test_large_grids(d, heads, kv):
-    """Enough tiles for the kernels of eight waves (two heads of a group by 128 rows, 256 rows,
-    128 keys): many sequences of two tiles and some of several, sampled against the oracle."""
+    """Blocks of 128 and of 64 keys, sequences found by the offsets' order: many sequences of two tiles and some of several, sampled against the oracle."""
     rng = np.random.default_rng(d + heads)
     lens = rng.integers(100, 260, 140)
     lens[5], lens[77], lens[90:95] = 700, 0, [1, 128, 256, 129, 257]
@@ -303,6 +302,39 @@ def test_large_grids(d, heads, kv):
         res, tol = one.bounds(o[s], lse[:, s])
         for x, r, t in zip((o[s], lse[:, s], *(g[s] for g in grads)), res, tol):
             assert np.all(np.abs(x - r) <= t + 1e-30), b
+
+
+@pytest.mark.parametrize("lq,lk,d,heads,kv,causal", [([2100], [2100], 128, 64, 32, True), ([2077], [2077], 64, 66, 22, True),
+                                                     ([2100], [2100], 64, 64, 64, True), ([4100, 50], [4200, 30], 128, 64, 16, True),
+                                                     ([2100], [2300], 128, 64, 32, False)], ids=str)
+def test_long_sequences_of_many_heads(lq, lk, d, heads, kv, causal):
+    """The kernels of eight waves (two heads of a group by 128 rows, or 256 rows of one): two key heads against the
+    oracle, and the bits of a call with these alone, which blocks of four waves make."""
+    c = Case(lq, lk, heads=heads, kv=kv, d=d, causal=causal, seed=27)
+    o, lse = c.forward()
+    grads = c.backward()
+    assert L.lora_device_status(c.ws) == 0
+    group = heads // kv
+    for kvh in (1, kv - 1):
+        hs, ks = slice(kvh * group, (kvh + 1) * group), slice(kvh, kvh + 1)
+        one = Case(lq, lk, heads=group, kv=1, d=d, causal=causal)
+        one.q, one.g, one.k, one.v = c.q[:, hs], c.g[:, hs], c.k[:, ks], c.v[:, ks]
+        one.upload()
+        o1, lse1 = one.forward()
+        assert np.array_equal(o1, o[:, hs]) and np.array_equal(lse1, lse[hs])
+        assert np.array_equal(one.backward()[0], grads[0][:, hs])
+        res, tol = one.bounds(o1, lse1)
+        for x, r, t in zip((o1, lse1, grads[0][:, hs], grads[1][:, ks], grads[2][:, ks]), res, tol):
+            both = np.isinf(x) & np.isinf(r)
+            assert np.all(np.abs(np.where(both, 0, x) - np.where(both, 0, r)) <= t + 1e-30), kvh
+    if causal:
+        at = lk[0] - 700
+        k, v = c.dev[1].clone(), c.dev[2].clone()
+        k[at], v[at] = NAN, NAN
+        L.attention_forward(c.shape, c.dev[0], k, v, c.cq, c.ck, c.o, c.lse, c.ws)
+        first = at - (lk[0] - lq[0])     # the first query that sees it
+        assert np.array_equal(f64_of(c.o)[:first], o[:first]) and np.array_equal(f64_of(c.lse)[:, :first], lse[:, :first])
+        assert np.isnan(f64_of(c.o)[first:lq[0]]).all()
 
 
 def test_gradients_against_differences():
