@@ -476,14 +476,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   bf16x8 qf[NK], df[NK];
   load_rows<D>(qf, a.q + row * a.q_stride + head * D, h);
   load_rows<D>(df, a.dout + row * a.o_stride + head * D, h);
+  // delta, the diagonal of dO O^T, by the instruction and in the order of dO V^T: where o is
+  // v (a single key) ds is 0, as it should be
   float delta = 0.f;
   {
     bf16x8 of[NK];
     load_rows<D>(of, a.o + row * a.o_stride + head * D, h);
+    f32x16 z;
 #pragma unroll
-    for (int kk = 0; kk < NK; ++kk)
+    for (int r = 0; r < 16; ++r) z[r] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) delta += (float)of[kk][j] * (float)df[kk][j];
+    for (int kk = 0; kk < NK; ++kk) z = mfma32(of[kk], df[kk], z);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) delta = result_row(r, h) == l ? z[r] : delta;
     delta += __shfl_xor(delta, 32, kWave);
   }
   settle(qf);

@@ -187,6 +187,17 @@ def test_rows_outside_every_sequence_stay(d):
     Case([30, 140], d=d, front=13, behind=150, seed=9).check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_key_has_no_gradient_through_its_score(d):
+    """Where a query sees one key, o is v, and dq and dk are 0, not what rounding leaves of dout.v - dout.o."""
+    c = Case([1, 1, 1, 1], heads=6, kv=2, d=d, seed=19)
+    _, _, dq, dk, dv = c.check()
+    assert not dq.any() and not dk.any() and dv.any()
+    c = Case([3, 1], [1, 1], heads=2, kv=2, d=d, causal=False, seed=20)
+    _, _, dq, dk, _ = c.check()
+    assert not dq.any() and not dk.any()
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(1)
     Case(rng.integers(0, 9, 300).tolist(), heads=2, kv=1, d=64, seed=10).check()
