@@ -22,6 +22,9 @@
  *     forward_backward_custom post).
  *   - Per-adapter AdamW with its own moments and step (Deep Dive - Tinker,
  *     "optim_step advances adapter state").
+ *   - What stands between the q/k/v and the o projections: attention over packed
+ *     prompts and its backward, a paged key-value cache in bf16 or 8 bits (its
+ *     tables made on the device), and the attention of single tokens over it.
  *
  * Conventions
  *   - bf16 tensors are passed as uint16_t bit patterns; fp32 as float.

@@ -18,7 +18,11 @@
 // without a broadcast.
 // dk and dv, and dq, are made by two kernels that each recompute the scores (7 products in
 // place of 5): every sum then has one owner and a fixed order, with no atomics and no
-// partial results in memory.
+// partial results in memory.  (Adding dq up from the key side would write and read fp32 dq
+// once for each 128 keys, and in an order that changes.)
+// Roundings: s, lse, delta and all sums are fp32; p and ds are rounded to bf16 where they
+// become operands (half a step, 2^-8 of a weight or less, signs as they come), as the
+// matrix instruction asks; outputs once at the end.
 #include <type_traits>
 
 #include "attn.hpp"
@@ -283,11 +287,20 @@ __device__ __forceinline__ f32x16 product_seen(bf16x8 v, bf16x8 p, f32x16 acc, i
 // ---------------------------------------------------------------- forward
 // NW waves of 32 query rows: `wpr` of them behind one another in one head, the rest in the
 // next heads of the same group, which read the same tiles.  Tiles of 64 keys pass through
-// two LDS stages by LDS-DMA, one barrier a tile.  Two waves on each SIMD take turns: while
-// one computes its weights the other's products run.
+// two LDS stages by LDS-DMA, one barrier a tile; the tiles that no query of the block masks
+// in a loop of their own, whose stages are compile-time offsets.  Two waves on each SIMD
+// take turns: while one computes its weights the other's products run.
 // The weights are powers of two relative to a reference that follows the row's maximum
 // only when that has passed it by 2^6: they stay below 2^6, exact as any float, and the
 // output is hardly ever rescaled.
+// Bound by the matrix units and the clock that their power leaves: 16384 tokens, 32 heads of
+// 128 over 8, causal (2.2 TFLOP): 1.93-2.08 ms, 1.06-1.14 PFLOP/s, the units busy in 59 % of
+// the cycles at 1.9 GHz (a large library matrix product: 1.37 PFLOP/s).  LDS is read
+// without conflicts and for a third of the cycles; 0.43 GB come from memory, 0.20 of
+// them the operands once.  Tried without gain: wave priorities around the products (the same), two
+// groups of waves half a tile apart (2088 against 1980 us).
+// Short prompts pay for the masked halves of their last tiles and for a block's start
+// (offsets, q, first tile: three round trips): 8192 tokens of 16, 100-108 us for 59.5 GFLOP.
 constexpr float AT_SLACK = 6.f;
 
 template <int D, int NW>
@@ -442,7 +455,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 }
 
 // ---------------------------------------------------------------- dq
-// Waves, tiles and stages as in the forward.
+// Waves, tiles and stages as in the forward, three products a tile in place of two.  8192
+// tokens of 6, 32 heads of 128 over 8 (11.3 M pairs a head): 280-288 us, 0.96-0.98 PFLOP/s;
+// the matrix units are busy in 54 % of the cycles.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void attention_dq_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
@@ -567,6 +582,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // lse and delta, head after head of the group, phase p taking every (NW / KW)-th.  Each
 // phase has its own LDS stages, filled by its own waves, the DMA that many tiles ahead but
 // one.  At the end the phases' sums are added in order, through LDS.
+// Four products a tile, two waves on a SIMD (256 registers each: the two sums alone are 128).
+// 8192 tokens of 6 as above: 420-490 us, 0.75-0.87 PFLOP/s, the matrix units busy in 40 % of
+// the cycles: the waves of a block go in step from tile to tile, and the longest block holds
+// the end up (a block's work goes from 4020 queries of four heads down to 64).  Phases of a
+// single wave need no barrier (2048 tokens 183 -> 173 us).
 constexpr int DKV_TILE = 32;
 
 template <int D, int NW, int KW, int S>
