@@ -290,15 +290,13 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
 // conversion of two codes at a time and the V tile's way through LDS take turns with the
 // loads of 12 waves.  One request of 4001: 5.6-6.1 us and 3.6-3.9, each a launch and a chain of
 // three loads (length, page, rows).
-// Units of 128 keys are the smallest that the four waves share evenly, and 32 of them the most
-// that a second kernel joins in one step; longer units would leave one long request to few CUs.
-// Larger blocks where there are 3000 of them write fewer partial results (single units:
-// 64 x 8000 286 + 8 us, 250 x 3000 in 8 bits 147 + 16).  Asking two tiles ahead, and loads
-// past the caches, were no faster.
-constexpr int DEC_WAVES = 4, DEC_TILE = 32, DEC_STRIPE = DEC_WAVES * DEC_TILE, DEC_UNIT = 128, DEC_MAX_UNITS = 32;
+// Units of 256 keys are two tiles a wave before the four waves' sums are joined (128: 250
+// requests of 1000 in bf16 152 us against 145, 16 of 1000 16 against 14; one of 4001 9.3 against
+// 10.3), and 32 of them the most that a second kernel joins in one step.
+constexpr int DEC_WAVES = 4, DEC_TILE = 32, DEC_STRIPE = DEC_WAVES * DEC_TILE, DEC_UNIT = 256, DEC_MAX_UNITS = 32;
 constexpr float DEC_SLACK = 6.f;
-constexpr int DEC_MAX_SPAN = 8;      // units of a block at most, as many as leave
-constexpr int64_t DEC_BLOCKS = 3000;  // this many blocks
+constexpr int DEC_MAX_SPAN = 8;        // units of a block at most
+constexpr int64_t DEC_BLOCKS = 3000;   // that so long a block has to leave; see decode_plan
 
 __host__ __device__ __forceinline__ int decode_unit(int len) {
   int s = DEC_UNIT;
@@ -741,7 +739,12 @@ lora_status launch_kv_write(const kv_shape& sh, int64_t n, const uint16_t* k, in
 }
 
 // How a batch is cut: units of a block, and nodes that a request of up to max_len keys has
-// then.
+// then.  Longer blocks write fewer partial results, as long as 3000 are left (64 requests of
+// 8000 as 16384, 4096 and 2048 blocks, spans of 1, 4 and 8 units: 266, 250 and 273 us; 250 of
+// 3000 in 8 bits as 12000, 3000 and 2000: 133, 117 and 148).  Where a
+// block can take its request whole and the requests fill the CUs, there are no partial
+// results and no second launch (250 of 1000: 145 -> 129 us, in 8 bits 88 -> 73; 32 of 300:
+// 12.6 -> 9.1; 100 of 1500 on 400 blocks 27.9 -> 28.9).
 struct DecodePlan {
   int span, nodes;
 };
@@ -749,7 +752,8 @@ static DecodePlan decode_plan(const kv_shape& sh, int32_t n_heads, int64_t max_l
   const int64_t units = std::min<int64_t>(DEC_MAX_UNITS, std::max<int64_t>(1, cdiv(max_len, DEC_UNIT)));
   const int64_t columns = (int64_t)sh.n_seqs * sh.n_kv_heads * cdiv(n_heads / sh.n_kv_heads, 16);
   int span = 1;
-  while (span < DEC_MAX_SPAN && columns * cdiv(units, 2 * span) >= DEC_BLOCKS) span *= 2;
+  const bool one = units <= DEC_MAX_SPAN && columns >= device_cus();
+  while (one ? span < units : span < DEC_MAX_SPAN && columns * cdiv(units, 2 * span) >= DEC_BLOCKS) span *= 2;
   return {span, (int)cdiv(units, span)};
 }
 
