@@ -284,12 +284,13 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
 //
 // Scores, weights' sums and outputs are fp32; the weights are rounded to bf16 to be an operand
 // (half a step, 2^-8 of a weight), and the output once at the end.
-// Bound by memory where the batch is large: 64 requests of 2400 to 8000 tokens, 8 key heads of
-// 128 in bf16 (1.37 GB): 250-259 us and 5 to join, 5.3 TB/s, the rate of a large copy.  In 8
-// bits, 250 requests of 900 to 3000, 4 key heads (0.51 GB): 110-114 us and 5, 4.5 TB/s: the
+// Bound by memory where the batch is large: 64 requests of 2500 to 8000 tokens, 8 key heads of
+// 128 in bf16 (1.37 GB): 246-253 us and 5 to join, 5.4 TB/s, the rate of a large copy.  In 8
+// bits, 250 requests of 900 to 3000, 4 key heads (0.51 GB): 106-110 us and 5, 4.7 TB/s: the
 // conversion of two codes at a time and the V tile's way through LDS take turns with the
-// loads of 12 waves.  One request of 4001: 5.6-6.1 us and 3.6-3.9, each a launch and a chain of
-// three loads (length, page, rows).
+// loads of 12 waves.  One request of 4001: 7.0-7.4 us and 2.6-3.5, each a launch and a chain of
+// three loads (length, page, rows).  Asking two tiles ahead, and loads past the caches, were
+// no faster.
 // Units of 256 keys are two tiles a wave before the four waves' sums are joined (128: 250
 // requests of 1000 in bf16 152 us against 145, 16 of 1000 16 against 14; one of 4001 9.3 against
 // 10.3), and 32 of them the most that a second kernel joins in one step.
