@@ -300,7 +300,7 @@ __device__ __forceinline__ f32x16 product_seen(bf16x8 v, bf16x8 p, f32x16 acc, i
 // them the operands once.  Tried without gain: wave priorities around the products (the same), two
 // groups of waves half a tile apart (2088 against 1980 us).
 // Short prompts pay for the masked halves of their last tiles and for a block's start
-// (offsets, q, first tile: three round trips): 8192 tokens of 16, 100-108 us for 59.5 GFLOP.
+// (offsets, q, first tile: three round trips): 8192 tokens of 16, 98-104 us for 59.5 GFLOP.
 constexpr float AT_SLACK = 6.f;
 
 template <int D, int NW>
@@ -760,13 +760,17 @@ static AttnArgs attn_args(const attn_shape& sh, const uint16_t* q, const uint16_
   return a;
 }
 
-// The blocks of the kernels whose waves own queries.  Four waves, 128 rows of a head: two
-// such blocks share a CU and fill each other's waits at a block's start and end.  Eight (two
-// heads of a group by 128 rows, or 256 rows): a tile that comes through LDS serves twice the
-// queries, which pays where blocks live long.  Forward, four / eight waves, us:
+// The blocks of the kernels whose waves own queries.  Four waves: two such blocks share a CU
+// and fill each other's waits at a block's start and end.  Eight (two heads of a group by 128
+// rows, or 256 rows): a tile that comes through LDS serves twice the queries, which pays where
+// blocks live long.  Forward, four / eight waves, us:
 //   16384 tokens, 32 heads of 128       2057 / 1982      4096 tokens             157 / 148
 //   2048 tokens                           53 /   61      8192 tokens of 16       101 / 108
 //   8192 tokens of 6                     165 /  164      10010 of 8, heads of 64  92 /  97
+// Four waves of up to four heads of a group where there are blocks enough: fewer rows behind
+// a sequence's last, and waves that need the same keys.  128 rows of one head / 32 of four:
+//   8192 tokens of 100                  80.5 / 64.7      4096 tokens of 8       47.9 / 46.5
+//   8192 of 64, heads of 64             30.4 / 26.9      300 tokens             11.8 / 12.6
 struct QueryGrid {
   dim3 blocks;
   int waves;
@@ -776,7 +780,10 @@ static QueryGrid query_grid(AttnArgs& a, const attn_shape& sh) {
   int waves = 8, heads = a.group % 2 == 0 ? 2 : 1;
   a.shift = heads == 2 ? 7 : 8;
   const bool few = tiles(a.shift) * (a.n_heads / heads) < 2 * device_cus();
-  if (few || sh.n_q / 2048 < sh.n_seqs) waves = 4, heads = 1, a.shift = 7;
+  if (few || sh.n_q / 2048 < sh.n_seqs) {
+    waves = 4, heads = few || a.group % 2 ? 1 : a.group % 4 ? 2 : 4;
+    a.shift = heads == 4 ? 5 : heads == 2 ? 6 : 7;
+  }
   a.wpr = waves / heads;
   a.tiles = (int)tiles(a.shift);
   return {dim3((unsigned)((int64_t)a.tiles * (a.n_heads / heads))), waves};

@@ -294,9 +294,9 @@ def test_same_bits_in_every_batch_and_call():
         assert np.array_equal(one.backward()[0], ref[0][s])
 
 
-@pytest.mark.parametrize("d,heads,kv", [(128, 8, 4), (64, 9, 3), (128, 5, 5), (64, 8, 4), (128, 6, 1)])
+@pytest.mark.parametrize("d,heads,kv", [(128, 8, 4), (64, 9, 3), (128, 5, 5), (64, 8, 4), (128, 6, 1), (128, 8, 2), (64, 4, 1)])
 def test_large_grids(d, heads, kv):
-    """Blocks of 128 and of 64 keys, sequences found by the offsets' order: many sequences of two tiles and some of several, sampled against the oracle."""
+    """Blocks of one, two and four heads of a group, of 128 and of 64 keys, sequences found by the offsets' order: many sequences of two tiles and some of several, sampled against the oracle."""
     rng = np.random.default_rng(d + heads)
     lens = rng.integers(100, 260, 140)
     lens[5], lens[77], lens[90:95] = 700, 0, [1, 128, 256, 129, 257]
