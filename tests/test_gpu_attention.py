@@ -187,6 +187,26 @@ def test_rows_outside_every_sequence_stay(d):
     Case([30, 140], d=d, front=13, behind=150, seed=9).check()
 
 
+def test_rows_far_apart():
+    """The longest strides: rows of k, v and their gradients over more than 4 GiB, the bits of dense ones."""
+    c = Case([100, 41], heads=2, kv=1, d=64, seed=21)
+    o, lse = c.forward()
+    dq, dk, dv = c.backward()
+    stride = (1 << 24) - 8
+    far = [torch.empty(c.m * stride, dtype=torch.bfloat16, device="cuda").as_strided((c.m, 2, 64), (stride, 64, 1)) for _ in range(2)]
+    (k, v), (fk, fv) = ((t[:, :1], t[:, 1:]) for t in far)
+    k.copy_(c.dev[1])
+    v.copy_(c.dev[2])
+    shape = L.make_attention_shape(c.n, c.m, 2, 2, 1, 64, c.scale, k_stride=stride, v_stride=stride)
+    o2, lse2, fq = torch.full_like(c.o, NAN), torch.full_like(c.lse, NAN), torch.full_like(c.o, NAN)
+    L.attention_forward(shape, c.dev[0], k, v, c.cq, c.ck, o2, lse2, c.ws)
+    assert np.array_equal(f64_of(o2), o) and np.array_equal(f64_of(lse2), lse)
+    L.attention_backward(shape, c.dout, c.dev[0], k, v, o2, lse2, c.cq, c.ck, fq, fk, fv, c.ws)
+    for a, b in ((fq, dq), (fk, dk), (fv, dv)):
+        assert np.array_equal(f64_of(a.contiguous()), b)
+    assert L.lora_device_status(c.ws) == 0
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_one_key_has_no_gradient_through_its_score(d):
     """Where a query sees one key, o is v, and dq and dk are 0, not what rounding leaves of dout.v - dout.o."""

@@ -310,7 +310,7 @@ class Decode:
         return o, lse
 
 
-LENS = [[1], [0, 3, 0], [15, 16, 17], [127, 128, 129, 130], [31, 32, 33, 64, 65, 96], [256, 511], [700, 5]]
+LENS = [[1], [0, 3, 0], [15, 16, 17], [127, 128, 129, 130], [31, 32, 33, 64, 65, 96], [256, 511], [255, 257, 513, 1025], [700, 5]]
 
 
 @pytest.mark.parametrize("x8", [False, True])
@@ -398,6 +398,18 @@ def test_decode_large_batches_cut_elsewhere(d, kv, group, x8):
         for b in (0, 1, 2, 3, n - 1):
             o1, lse1 = run(np.array([b]), width * 16)
             assert torch.equal(o1[0], o[b]) and torch.equal(lse1[0], lse[b]), (n, b)
+
+
+def test_decode_heads_leave_one_another_alone():
+    """A head's bits do not follow the scores of its group's other heads."""
+    c = Decode([300, 1, 777], heads=8, kv=2, d=128, seed=7)
+    o, lse = c.run()
+    keep = c.dq.clone()
+    c.dq[:, 1::2] *= 40
+    o2, lse2 = c.run()
+    c.dq.copy_(keep)
+    assert np.array_equal(o2[:, ::2], o[:, ::2]) and np.array_equal(lse2[:, ::2], lse[:, ::2])
+    assert not np.array_equal(o2[2, 1::2], o[2, 1::2])
 
 
 def test_decode_q_in_a_fused_row():
