@@ -785,9 +785,9 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
  *        8, >= n_heads * head_dim, < 2^31)
  *   block_table int32 [n_seqs][max_pages], seq_lens int32 [n_seqs] as kv_tables leaves
  *        them.  seq_len 0: o = 0 and lse = -inf.
- *   max_len  an upper bound of the lengths (0 .. max_pages * page_size, at most 2^30), which sizes the
- *        launch: a step captured with the longest length to come serves every step.  A
- *        length outside [0, max_len] counts as 0 and sets LORA_FLAG_BAD_LENGTH; rows of
+ *   max_len  an upper bound of the lengths (0 .. max_pages * page_size, at most 2^30), which
+ *        sizes the launch: a step captured with the longest length to come serves every
+ *        step.  A length outside [0, max_len] counts as 0 and sets LORA_FLAG_BAD_LENGTH; rows of
  *        a page out of range are left out, with LORA_FLAG_BAD_PAGE.
  *   o    bf16 [n_seqs][n_heads][head_dim] out; outputs must not overlap other operands
  *   lse  fp32 [n_seqs][n_heads] out, nullable
@@ -797,7 +797,8 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
  * request's last row is never used.  The
  * length is split and joined by rules on the request's own length: its results have the
  * same bits in every batch.  n_heads a multiple of n_kv_heads, <= 1024.
- * Workspace: attention_decode_workspace_bytes(shape, n_heads, max_len); word 0 is the
+ * Workspace: attention_decode_workspace_bytes(shape, n_heads, max_len) on the device of the
+ * call, for just these arguments (a smaller batch or bound may need more); word 0 is the
  * status word. */
 size_t attention_decode_workspace_bytes(const kv_shape* shape, int32_t n_heads, int64_t max_len);
 lora_status attention_decode(const kv_shape* shape, int32_t n_heads, const uint16_t* q,

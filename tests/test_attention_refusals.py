@@ -204,9 +204,9 @@ def test_decode(L):  # noqa: F811
     assert call(s=_kv(L, n_seqs=0), q=None, o=None, t=None, ln=None) == L.LORA_OK
 
 
-@pytest.mark.parametrize("bound", [0, 1, 128, 129, 1000, 4096, 4097, 100000])
+@pytest.mark.parametrize("bound", [0, 1, 128, 129, 256, 257, 1000, 4096, 4097, 8193, 100000])
 def test_decode_workspace_grows_with_the_bound(L, bound):  # noqa: F811
     s = _kv(L, max_pages=10000)
     n = L.attention_decode_workspace_bytes(s, 8, bound)
-    parts = min(32, max(1, -(-bound // 128)))
+    parts = min(32, max(1, -(-bound // 256)))     # units of 256 keys, or 32 of them
     assert n == 256 if parts == 1 else n >= 256 + 3 * 8 * parts * (8 + 4 * 64)
