@@ -797,9 +797,9 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
  * request's last row is never used.  The
  * length is split and joined by rules on the request's own length: its results have the
  * same bits in every batch.  n_heads a multiple of n_kv_heads, <= 1024.
- * Workspace: attention_decode_workspace_bytes(shape, n_heads, max_len) on the device of the
- * call, for just these arguments (a smaller batch or bound may need more); word 0 is the
- * status word. */
+ * Workspace: attention_decode_workspace_bytes(shape, n_heads, max_len), enough for smaller
+ * n_seqs and max_len too (the call itself asks for what it uses); word 0 is the status
+ * word. */
 size_t attention_decode_workspace_bytes(const kv_shape* shape, int32_t n_heads, int64_t max_len);
 lora_status attention_decode(const kv_shape* shape, int32_t n_heads, const uint16_t* q,
                              int64_t q_stride, const void* k_cache, const void* v_cache,

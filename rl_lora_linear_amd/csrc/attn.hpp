@@ -24,6 +24,7 @@ lora_status launch_kv_write(const kv_shape& sh, int64_t n, const uint16_t* k, in
                             void* v_cache, uint8_t* k_scales, uint8_t* v_scales, void* ws,
                             hipStream_t s);
 size_t decode_ws_bytes(const kv_shape& sh, int32_t n_heads, int64_t max_len);
+size_t decode_ws_bound(const kv_shape& sh, int32_t n_heads, int64_t max_len);
 lora_status launch_decode(const kv_shape& sh, int32_t n_heads, const uint16_t* q, int64_t q_stride,
                           const void* k_cache, const void* v_cache, const uint8_t* k_scales,
                           const uint8_t* v_scales, const int32_t* table, const int32_t* seq_lens,

@@ -286,7 +286,7 @@ static lora_status check_decode(const kv_shape* shape, int32_t n_heads, int64_t 
 
 size_t attention_decode_workspace_bytes(const kv_shape* shape, int32_t n_heads, int64_t max_len) {
   if (check_decode(shape, n_heads, max_len) != LORA_OK) return 0;
-  return decode_ws_bytes(*shape, n_heads, max_len);
+  return decode_ws_bound(*shape, n_heads, max_len);
 }
 
 lora_status attention_decode(const kv_shape* shape, int32_t n_heads, const uint16_t* q,

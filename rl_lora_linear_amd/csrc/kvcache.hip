@@ -749,20 +749,35 @@ lora_status launch_kv_write(const kv_shape& sh, int64_t n, const uint16_t* k, in
 struct DecodePlan {
   int span, nodes;
 };
-static DecodePlan decode_plan(const kv_shape& sh, int32_t n_heads, int64_t max_len) {
+static DecodePlan decode_plan(int64_t columns, int64_t max_len) {   // columns: requests by key heads by 16 query heads
   const int64_t units = std::min<int64_t>(DEC_MAX_UNITS, std::max<int64_t>(1, cdiv(max_len, DEC_UNIT)));
-  const int64_t columns = (int64_t)sh.n_seqs * sh.n_kv_heads * cdiv(n_heads / sh.n_kv_heads, 16);
   int span = 1;
   const bool one = units <= DEC_MAX_SPAN && columns >= device_cus();
   while (one ? span < units : span < DEC_MAX_SPAN && columns * cdiv(units, 2 * span) >= DEC_BLOCKS) span *= 2;
   return {span, (int)cdiv(units, span)};
 }
+static int64_t decode_columns(const kv_shape& sh, int32_t n_heads) {
+  return (int64_t)sh.n_kv_heads * cdiv(n_heads / sh.n_kv_heads, 16);
+}
+static size_t decode_part_bytes(size_t parts, const kv_shape& sh) {
+  return parts ? 256 + align_up(parts * sizeof(float2), 256) + parts * sh.head_dim * sizeof(float) : 256;
+}
 
 size_t decode_ws_bytes(const kv_shape& sh, int32_t n_heads, int64_t max_len) {
-  const DecodePlan p = decode_plan(sh, n_heads, max_len);
-  if (p.nodes == 1) return 256;
-  const size_t parts = (size_t)sh.n_seqs * n_heads * p.nodes;
-  return 256 + align_up(parts * sizeof(float2), 256) + parts * sh.head_dim * sizeof(float);
+  const DecodePlan p = decode_plan(sh.n_seqs * decode_columns(sh, n_heads), max_len);
+  return decode_part_bytes(p.nodes == 1 ? 0 : (size_t)sh.n_seqs * n_heads * p.nodes, sh);
+}
+
+// The most of them over smaller batches and bounds, which may be cut into more parts.
+size_t decode_ws_bound(const kv_shape& sh, int32_t n_heads, int64_t max_len) {
+  size_t most = 0;
+  const int64_t units = std::min<int64_t>(DEC_MAX_UNITS, cdiv(max_len, DEC_UNIT));
+  for (int64_t n = 1; n <= sh.n_seqs; ++n)
+    for (int64_t u = 2; u <= units; ++u) {
+      const DecodePlan p = decode_plan(n * decode_columns(sh, n_heads), u * DEC_UNIT);
+      if (p.nodes > 1) most = std::max(most, (size_t)n * n_heads * p.nodes);
+    }
+  return decode_part_bytes(most, sh);
 }
 
 lora_status launch_decode(const kv_shape& sh, int32_t n_heads, const uint16_t* q, int64_t q_stride,
@@ -770,7 +785,7 @@ lora_status launch_decode(const kv_shape& sh, int32_t n_heads, const uint16_t* q
                           const uint8_t* v_scales, const int32_t* table, const int32_t* seq_lens,
                           int64_t max_len, float scale, uint16_t* o, float* lse, void* ws,
                           hipStream_t s) {
-  const DecodePlan p = decode_plan(sh, n_heads, max_len);
+  const DecodePlan p = decode_plan(sh.n_seqs * decode_columns(sh, n_heads), max_len);
   DecodeArgs a{};
   a.q = q, a.kc = k_cache, a.vc = v_cache, a.ks = k_scales, a.vs = v_scales;
   a.table = table, a.lens = seq_lens, a.o = o, a.lse = lse, a.status = (int32_t*)ws;

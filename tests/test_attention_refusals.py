@@ -210,3 +210,14 @@ def test_decode_workspace_grows_with_the_bound(L, bound):  # noqa: F811
     n = L.attention_decode_workspace_bytes(s, 8, bound)
     parts = min(32, max(1, -(-bound // 256)))     # units of 256 keys, or 32 of them
     assert n == 256 if parts == 1 else n >= 256 + 3 * 8 * parts * (8 + 4 * 64)
+
+
+@pytest.mark.parametrize("heads,kv", [(8, 8), (32, 8), (40, 1)])
+def test_decode_workspace_of_a_large_batch_serves_smaller_ones(L, heads, kv):  # noqa: F811
+    """Large batches are cut into fewer parts than small ones; a workspace sized for them serves all."""
+    rng = __import__("random").Random(heads)
+    mk = lambda n: _kv(L, n_seqs=n, n_kv_heads=kv, max_pages=1000)  # noqa: E731
+    for _ in range(60):
+        n, m = rng.randint(1, 700), rng.randint(1, 16000)
+        have = L.attention_decode_workspace_bytes(mk(n), heads, m)
+        assert have >= L.attention_decode_workspace_bytes(mk(rng.randint(1, n)), heads, rng.randint(0, m))
