@@ -160,14 +160,16 @@ __device__ __forceinline__ bf16x8 transposed_op(const char* rows, AttnPlaces p, 
 
 // LDS-DMA, 16 bytes a lane from base + voff, the lanes' one behind the other from LDS byte
 // `to` on.  Issued by hand: the compiler would wait for it before every LDS read.
+// M0 holds the LDS address: an operand, so that the compiler writes it and knows it; the hardware
+// asks for one wait state between that write and the load.
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 __device__ __forceinline__ void dma16(uint32_t voff, const void* base, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(voff), "s"(base) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(voff), "s"(base) : "memory");
 }
 __device__ __forceinline__ void dma4_at(const void* p, uint32_t to) {   // 4 bytes a lane, each from its own address
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(p) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(to), "v"(p) : "memory");
 }
 // Rows r0 .. r0 + ROWS - 1 of a [rows][D] matrix to LDS, by NW waves.  Rows past the end
 // are copies of the last one: their weights are 0.

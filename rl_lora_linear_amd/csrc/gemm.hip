@@ -153,15 +153,17 @@ __device__ __forceinline__ uint32_t lds_addr(const uint4* p) {
 
 // One 16-byte LDS-DMA per lane: global (base + voff) -> LDS (m0v + 16 * lane).
 // base is wave-uniform (SGPR pair), voff a per-lane 32-bit byte offset.
+// M0 holds the LDS address: an operand, so that the compiler writes it and knows it; the hardware
+// asks for one wait state between that write and the load.
 __device__ __forceinline__ void dma16s(uint32_t voff, const void* base, uint32_t m0v) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0v), "v"(voff), "s"(base)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(m0v), "v"(voff), "s"(base)
                : "memory");
 }
 
 // One 16-byte LDS-DMA per lane from a per-lane 64-bit address:
 // global g -> LDS (m0v + 16 * lane).
 __device__ __forceinline__ void dma16v(const void* g, uint32_t m0v) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0v), "v"(g) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(m0v), "v"(g) : "memory");
 }
 
 // 16-byte chunks of one run's staged factor block: B_a rows n0.. (cols rows of

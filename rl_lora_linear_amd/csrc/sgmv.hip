@@ -93,8 +93,11 @@ __device__ __forceinline__ uint32_t lds_u32(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
+// One 16-byte LDS-DMA per lane, global g -> LDS (m0v + 16 * lane).
+// M0 holds the LDS address: an operand, so that the compiler writes it and knows it; the hardware
+// asks for one wait state between that write and the load.
 __device__ __forceinline__ void dma16(const void* g, uint32_t m0v) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0v), "v"(g) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(m0v), "v"(g) : "memory");
 }
 
 template <int VM>

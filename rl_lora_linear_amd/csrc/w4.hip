@@ -199,16 +199,18 @@ __device__ __forceinline__ uint32_t lds_at(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 // One LDS-DMA per lane, global (base + voff) -> LDS (m0v + lane * size).
+// M0 holds the LDS address: an operand, so that the compiler writes it and knows it; the hardware
+// asks for one wait state between that write and the load.
 __device__ __forceinline__ void dma16(uint32_t voff, const void* base, uint32_t m0v) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0v), "v"(voff), "s"(base)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(m0v), "v"(voff), "s"(base)
                : "memory");
 }
 __device__ __forceinline__ void dma16_nt(uint32_t voff, const void* base, uint32_t m0v) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(m0v), "v"(voff), "s"(base)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"{m0}"(m0v), "v"(voff), "s"(base)
                : "memory");
 }
 __device__ __forceinline__ void dma4(uint32_t voff, const void* base, uint32_t m0v) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(m0v), "v"(voff), "s"(base)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(m0v), "v"(voff), "s"(base)
                : "memory");
 }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
