@@ -678,7 +678,7 @@ size_t attention_workspace_bytes(const attn_shape* shape);
  *              one array.  A sequence that breaks this sets LORA_FLAG_BAD_LENGTH and is
  *              left out; parts of others may be then, too (the blocks find their sequence
  *              by the order of the offsets).
- *   o   bf16 [n_q] rows of [n_heads][head_dim] out, must not overlap q, k or v
+ *   o   bf16 [n_q] rows of [n_heads][head_dim] out, must not overlap an input
  *   lse fp32 [n_heads][n_q] out; it and ws must not overlap another operand
  * Rows of o and lse that belong to no sequence are left as they were. */
 lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const uint16_t* k,

@@ -153,6 +153,7 @@ lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const 
   const Span in[] = {span(q, s.n_q, s.q_stride, qc), span(k, s.n_k, s.k_stride, kc), span(v, s.n_k, s.v_stride, kc),
                      span(o, s.n_q, s.o_stride, qc), bytes(cu_q, cu), bytes(cu_k, cu)};
   LORA_ARG_CHECK(clash(out, in) < 0, "attention_forward: lse or the workspace overlaps another operand");
+  LORA_ARG_CHECK(!meet(in[3], in[4]) && !meet(in[3], in[5]), "attention_forward: o overlaps cu_q or cu_k");
   if (s.n_q == 0 || s.n_seqs == 0) return LORA_OK;
   return launch_attention_fwd(s, q, k, v, cu_q, cu_k, o, lse, ws, S(stream));
 }

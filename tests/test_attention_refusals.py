@@ -84,6 +84,13 @@ def test_attention(L):  # noqa: F811
     assert fwd(s=mk(n_seqs=0), cq=None, ck=None) == L.LORA_OK
 
 
+def test_attention_output_on_the_offsets(L):  # noqa: F811
+    """cu_q and cu_k are read by every block, so o may not be written over them."""
+    s = L.make_attention_shape(100, 120, 3, 4, 2, 64, 0.1)
+    for cq, ck in ((at(4), at(9)), (at(9), at(4)), (ctypes.c_void_p((4 << 20) + 2 * 100 * 4 * 64 - 4), at(9))):
+        _is(L, L.LIB.attention_forward(ctypes.byref(s), at(1), at(2), at(3), cq, ck, at(4), at(10), at(11), BIG, None), L.LORA_E_INVALID_ARG, b"overlaps")
+
+
 def _kv(L, **kw):
     return L.make_kv_shape(**{**dict(n_seqs=3, n_kv_heads=2, head_dim=64, page_size=16, n_pages=20, max_pages=4), **kw})
 
