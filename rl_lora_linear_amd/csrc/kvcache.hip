@@ -296,8 +296,9 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
 // 10.3), and 32 of them the most that a second kernel joins in one step.
 constexpr int DEC_WAVES = 4, DEC_TILE = 32, DEC_STRIPE = DEC_WAVES * DEC_TILE, DEC_UNIT = 256, DEC_MAX_UNITS = 32;
 constexpr float DEC_SLACK = 6.f;
-constexpr int DEC_MAX_SPAN = 8;        // units of a block at most
-constexpr int64_t DEC_BLOCKS = 3000;   // that so long a block has to leave; see decode_plan
+constexpr int DEC_MAX_SPAN = 8;      // units of a block that takes its request whole, at most
+constexpr int DEC_CUT_SPAN = 4;      // of one that takes a part; see decode_plan
+constexpr int DEC_CU_BLOCKS = 9;     // blocks of a CU that so long a block has to leave
 
 __host__ __device__ __forceinline__ int decode_unit(int len) {
   int s = DEC_UNIT;
@@ -740,20 +741,34 @@ lora_status launch_kv_write(const kv_shape& sh, int64_t n, const uint16_t* k, in
 }
 
 // How a batch is cut: units of a block, and nodes that a request of up to max_len keys has
-// then.  Longer blocks write fewer partial results, as long as 3000 are left (64 requests of
-// 8000 as 16384, 4096 and 2048 blocks, spans of 1, 4 and 8 units: 266, 250 and 273 us; 250 of
-// 3000 in 8 bits as 12000, 3000 and 2000: 133, 117 and 148).  Where a
-// block can take its request whole and the requests fill the CUs, there are no partial
-// results and no second launch (250 of 1000: 145 -> 129 us, in 8 bits 88 -> 73; 32 of 300:
-// 12.6 -> 9.1; 100 of 1500 on 400 blocks 27.9 -> 28.9).
+// then.  A block that can take its request whole (up to eight units) does where the requests
+// make a block for each CU: no partial results, no second launch.  Longer requests are cut into
+// runs of up to four units as long as nine blocks are left for each CU (three are resident).
+// Runs of eight end a launch on long blocks however many there are.  Requests of 0.3 to 1
+// times a length, 32 heads of 128; runs of 1, 2, 4 and 8 units, us (* what the rule takes):
+//   400 x 3000, 4 key heads                373   351  *318   397    (1600 blocks by 12 units)
+//   400 x 3000, 4 key heads, 8 bits        212   199  *178   224
+//   200 x 3000, 4 key heads, 8 bits        109   102  * 94   122    (2400 blocks of four)
+//   170 x 3000, 4 key heads, 8 bits         93  * 87    82   104    (2040)
+//   64 x 8000, 8 key heads                 266   254  *252   276
+//   32 x 8000, 8 key heads                 127  *124   131   142    (2048)
+//   64 x 4000, 8 key heads                 139  *133   144   141    (2048)
+//   16 x 31000, 8 key heads, 8 bits      * 150   155   160   150    (2048 of two)
+// (over 580 such batches the time is within 2.3 % of the best run's on average).  Whole requests
+// against the best cut:
+//   32 x 300, 8 key heads                 10.6 / 13.5      31 x 300 (248 blocks)   10.3 / 13.0
+//   32 x 1000                             20.6 / 20.4      250 x 1000               123 /  146
+//   32 x 2000, 8 bits (256 blocks)        30.2 / 25.0      64 x 2000, 8 bits       43.9 / 48.7
+//   100 x 1500                            89.8 / 88.5      128 x 2000, 2 key heads 44.5 / 45.8
 struct DecodePlan {
   int span, nodes;
 };
 static DecodePlan decode_plan(int64_t columns, int64_t max_len) {   // columns: requests by key heads by 16 query heads
   const int64_t units = std::min<int64_t>(DEC_MAX_UNITS, std::max<int64_t>(1, cdiv(max_len, DEC_UNIT)));
   int span = 1;
-  const bool one = units <= DEC_MAX_SPAN && columns >= device_cus();
-  while (one ? span < units : span < DEC_MAX_SPAN && columns * cdiv(units, 2 * span) >= DEC_BLOCKS) span *= 2;
+  const int64_t cus = device_cus();
+  const bool one = units <= DEC_MAX_SPAN && columns >= cus;
+  while (one ? span < units : span < DEC_CUT_SPAN && columns * cdiv(units, 2 * span) >= DEC_CU_BLOCKS * cus) span *= 2;
   return {span, (int)cdiv(units, span)};
 }
 static int64_t decode_columns(const kv_shape& sh, int32_t n_heads) {

@@ -228,3 +228,34 @@ def test_decode_workspace_of_a_large_batch_serves_smaller_ones(L, heads, kv):  #
         n, m = rng.randint(1, 700), rng.randint(1, 16000)
         have = L.attention_decode_workspace_bytes(mk(n), heads, m)
         assert have >= L.attention_decode_workspace_bytes(mk(rng.randint(1, n)), heads, rng.randint(0, m))
+
+
+def _parts(L, n, heads, kv, m):
+    """How many parts a call cuts a request of the bound's length into, from the workspace that it asks for."""
+    s = _kv(L, n_seqs=n, n_kv_heads=kv, max_pages=2000)
+    st = L.LIB.attention_decode(ctypes.byref(s), heads, at(1), heads * 64, at(2000), at(4000), None, None, at(6000), at(6500), m, 0.1, at(7000), None,
+                                at(8000), 0, None)
+    _is(L, st, L.LORA_E_WORKSPACE)
+    need = int(L.LIB.lora_last_error().split(b"< ")[1].split()[0])
+    if need <= 256:
+        return 1
+    rows = n * heads
+    parts = (need - 256) // (rows * (8 + 4 * 64))
+    assert need == 256 + -(-rows * parts * 8 // 256) * 256 + rows * parts * 4 * 64
+    return parts
+
+
+@pytest.mark.parametrize("n,kv,m", [(249, 4, 3000), (250, 4, 3000), (251, 4, 3000), (400, 4, 3000), (800, 2, 3000), (200, 8, 3000), (100, 8, 8000), (64, 8, 8000),
+                                    (300, 1, 8000), (4096, 8, 31000)])
+def test_decode_cuts_long_requests_of_large_batches_alike(L, n, kv, m):  # noqa: F811
+    """A request too long for one block is cut into runs of at most four units of its length (runs of
+    eight end a launch on long blocks), and into those wherever the batch is large."""
+    assert _parts(L, n, 4 * kv, kv, m) == -(-min(32, -(-m // 256)) // 4)
+
+
+def test_decode_cuts_follow_the_compute_units(L):  # noqa: F811
+    """Longer runs where nine blocks a compute unit (256 of them) are left: on both sides of it."""
+    for n, parts in ((191, 6), (192, 3)):      # four key heads, 12 units: 764 and 768 columns of three runs
+        assert _parts(L, n, 16, 4, 3000) == parts
+    for n, parts in ((63, 6), (64, 1)):        # whole requests of up to eight units from 256 blocks on
+        assert _parts(L, n, 16, 4, 1500) == parts
