@@ -783,15 +783,23 @@ size_t decode_ws_bytes(const kv_shape& sh, int32_t n_heads, int64_t max_len) {
   return decode_part_bytes(p.nodes == 1 ? 0 : (size_t)sh.n_seqs * n_heads * p.nodes, sh);
 }
 
-// The most of them over smaller batches and bounds, which may be cut into more parts.
+// The most of them over smaller batches and bounds, which may be cut into more parts.  For
+// requests of u units the parts grow with the batch until the cut gets coarser: the largest
+// batch before each coarser cut, and the whole one, are all there is to look at.
 size_t decode_ws_bound(const kv_shape& sh, int32_t n_heads, int64_t max_len) {
   size_t most = 0;
   const int64_t units = std::min<int64_t>(DEC_MAX_UNITS, cdiv(max_len, DEC_UNIT));
-  for (int64_t n = 1; n <= sh.n_seqs; ++n)
-    for (int64_t u = 2; u <= units; ++u) {
-      const DecodePlan p = decode_plan(n * decode_columns(sh, n_heads), u * DEC_UNIT);
+  const int64_t columns = decode_columns(sh, n_heads), cus = device_cus();
+  for (int64_t u = 2; u <= units; ++u) {
+    const auto look = [&](int64_t most_columns) {   // the largest batch with fewer columns than that
+      const int64_t n = std::min<int64_t>(sh.n_seqs, (most_columns - 1) / columns);
+      const DecodePlan p = decode_plan(n * columns, u * DEC_UNIT);
       if (p.nodes > 1) most = std::max(most, (size_t)n * n_heads * p.nodes);
-    }
+    };
+    look(sh.n_seqs * columns + 1);
+    if (u <= DEC_MAX_SPAN) look(cus);
+    for (int span = 2; span <= DEC_CUT_SPAN; span *= 2) look(cdiv(DEC_CU_BLOCKS * cus, cdiv(u, span)));
+  }
   return decode_part_bytes(most, sh);
 }
 

@@ -1,6 +1,7 @@
 """Host-side refusals of the attention and key-value cache calls (CPU only: every call here
 fails before anything is enqueued, or has nothing to do, whatever its pointers hold)."""
 import ctypes
+import time
 
 import pytest
 
@@ -259,3 +260,21 @@ def test_decode_cuts_follow_the_compute_units(L):  # noqa: F811
         assert _parts(L, n, 16, 4, 3000) == parts
     for n, parts in ((63, 6), (64, 1)):        # whole requests of up to eight units from 256 blocks on
         assert _parts(L, n, 16, 4, 1500) == parts
+
+
+@pytest.mark.parametrize("n,heads,kv,m", [(200, 16, 4, 4000), (77, 8, 8, 20000), (260, 32, 1, 1500), (40, 48, 2, 700), (3, 4, 2, 8192), (1, 4, 4, 257)])
+def test_decode_workspace_is_the_most_that_any_smaller_call_asks_for(L, n, heads, kv, m):  # noqa: F811
+    """No less than a call of fewer requests or a shorter bound uses, and no more than the largest of them."""
+    bound = L.attention_decode_workspace_bytes(_kv(L, n_seqs=n, n_kv_heads=kv, max_pages=2000), heads, m)
+    lengths = sorted({min(256 * u, m) for u in range(1, min(32, -(-m // 256)) + 1)} | {m})
+    rows = max(b * p for b in range(1, n + 1) for x in lengths if (p := _parts(L, b, heads, kv, x)) > 1) * heads
+    assert bound == 256 + -(-rows * 8 // 256) * 256 + rows * 4 * 64
+
+
+def test_decode_workspace_is_a_quick_question(L):  # noqa: F811
+    """A caller may ask at every step: microseconds, however many requests there are."""
+    s = _kv(L, n_seqs=4096, n_kv_heads=8, max_pages=2000)
+    began = time.perf_counter()
+    for i in range(500):
+        L.attention_decode_workspace_bytes(s, 32, 31000 + i)
+    assert time.perf_counter() - began < 1.0
