@@ -57,12 +57,14 @@ __device__ __forceinline__ bool read_sequence(const AttnArgs& a, int b, AttnSeq&
   s = {q0, k0, q1 - q0, k1 - k0, -1};
   return q0 >= 0 && q1 >= q0 && q1 <= a.n_q && k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
 }
-// Up to 16 sequences, one to a lane: the one with the most rows on the other side first, and
+// Up to 24 sequences, one to a lane: the one with the most rows on the other side first, and
 // its tiles with the most work first (of keys the first tiles, of queries the last), so that
 // the launch does not end on a long block.  Each lane sums the tiles of the sequences before
-// its own.  (4096 tokens of 8: forward 54 -> 49 us; with 64 sequences the sums cost more than
-// the order gives, 8192 tokens of 64: 35 -> 50 us.)
-constexpr int AT_SORTED = 16;
+// its own, which with many sequences costs more than the order gives.  Forward in order of
+// length over forward in order of the offsets, the mean of six shapes (2500 to 10010 tokens; one
+// shape's figures scatter by 5 %): 10 sequences 0.98, 16 0.95, 20 0.95, 24 0.98, 28 1.03,
+// 32 1.04; whole backward 0.96, 0.98, 0.98, 1.01, 0.99, 0.96.  8192 tokens of 64: 67 -> 82 us.
+constexpr int AT_SORTED = 24;
 template <bool KEYS>
 __device__ __forceinline__ AttnSeq find_sorted(const AttnArgs& a, int id, int shift) {
   const int lane = threadIdx.x & 63;
