@@ -584,8 +584,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // A wave owns 32 keys, KW waves 32 KW of them in a row, and the block's NW / KW phases
 // share out what those keys have to see: tiles of 32 queries of a head, with their dout,
 // lse and delta, head after head of the group, phase p taking every (NW / KW)-th.  Each
-// phase has its own LDS stages, filled by its own waves, the DMA that many tiles ahead but
-// one.  At the end the phases' sums are added in order, through LDS.
+// phase has two LDS stages of its own, filled by its own waves, the DMA a tile ahead.  At the
+// end the phases' sums are added in order, through LDS.
 // Four products a tile, two waves on a SIMD (256 registers each: the two sums alone are 128).
 // 8192 tokens of 6 as above: 420-490 us, 0.75-0.87 PFLOP/s, the matrix units busy in 40 % of
 // the cycles: the waves of a block go in step from tile to tile, and the longest block holds
@@ -593,15 +593,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // single wave need no barrier (2048 tokens 183 -> 173 us).
 constexpr int DKV_TILE = 32;
 
-template <int D, int NW, int KW, int S>
+template <int D, int NW, int KW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_dkv_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16, P = NW / KW;
   constexpr int TILE = DKV_TILE * D * 2, STAGE = 2 * TILE;   // q's rows, then dout's
-  constexpr int N = DKV_TILE * D * 2 / 1024, DMAS = 2 * ((N + KW - 1) / KW) + 1;   // of a wave and stage
-  static_assert(P * S * STAGE >= (NW - KW) * TILE * 2);      // room for the other phases' dk or dv in fp32
-  static_assert(N % KW == 0);
-  __shared__ __attribute__((aligned(16))) char lds[P * S * STAGE];
-  __shared__ __attribute__((aligned(16))) float stats[P][S][2][DKV_TILE];   // of a stage: lse in powers of two, delta
+  static_assert(P * 2 * STAGE >= (NW - KW) * TILE * 2);      // room for the other phases' dk or dv in fp32
+  __shared__ __attribute__((aligned(16))) char lds[P * 2 * STAGE];
+  __shared__ __attribute__((aligned(16))) float stats[P][2][2][DKV_TILE];   // of a stage: lse in powers of two, delta
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & 31, h = lane >> 5, phase = wave / KW, kw = wave % KW;
   const int kvh = blockIdx.x % a.n_kv;
@@ -623,13 +621,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   const auto skip = [&](At& t, int n) {
     for (t.tile += n; t.tile >= end && t.head < a.group; t.tile -= per_head) ++t.head;
   };
-  const uint32_t lds0 = lds_offset(lds) + phase * S * STAGE, stats0 = lds_offset(stats) + phase * (int)sizeof(stats[0]);
+  const uint32_t lds0 = lds_offset(lds) + phase * 2 * STAGE, stats0 = lds_offset(stats) + phase * (int)sizeof(stats[0]);
   At ask{0, begin};
-  // every stage is as many DMAs, so that a count of them says which have landed: behind the
-  // last tile, a tile is fetched that nobody reads
   const auto stage = [&](int st) {
-    const bool real = ask.head < a.group;
-    const int t0 = (real ? ask.tile : begin) * DKV_TILE, head = kvh * a.group + (real ? ask.head : 0);
+    if (ask.head >= a.group) return;
+    const int t0 = ask.tile * DKV_TILE, head = kvh * a.group + ask.head;
     dma_tile<D, KW, DKV_TILE>(a.q + s.q0 * a.q_stride + head * D, a.q_stride, t0, s.lq, lds0 + st * STAGE, kw, lane);
     dma_tile<D, KW, DKV_TILE>(a.dout + s.q0 * a.o_stride + head * D, a.o_stride, t0, s.lq, lds0 + st * STAGE + TILE, kw, lane);
     // the lower lanes fetch the tile's lse, the upper ones its delta (each wave the same)
@@ -640,8 +636,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   if (per_head) {
     skip(now, phase);
     ask = now;
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) stage(i);
+    stage(0);
   }
   bf16x8 kf[NK], vf[NK];
   const int64_t row = s.k0 + min(j, s.lk - 1);
@@ -659,7 +654,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   const auto step = [&](int t0, int st, const bool masked) {
     const char *const qt = lds, *const gt = qt + TILE;
     const float* const stat = &stats[phase][st][0][0];
-    const uint32_t off = (phase * S + st) * STAGE;   // (above the bits that the swizzle turns)
+    const uint32_t off = (phase * 2 + st) * STAGE;   // (above the bits that the swizzle turns)
     const AttnPlaces at = opaque({places.direct + off, places.transposed + off});
     f32x16 x, y;
 #pragma unroll
@@ -711,15 +706,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   for (int n = 0, st = 0; n < steps; ++n) {
     // the tile has landed, every wave of the phase is done with the stage before it (a wave
     // that is a phase by itself waits for nobody)
-    if constexpr (KW == 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * DMAS) : "memory");
-    else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * DMAS) : "memory");
-    stage(st == 0 ? S - 1 : st - 1);
+    if constexpr (KW == 1) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    stage(1 - st);
     const int t0 = now.tile * DKV_TILE;
     if (now.head < a.group && t0 + DKV_TILE - 1 >= wave_first) step(t0, st, t0 < wave_all || t0 + DKV_TILE > s.lq);
     skip(now, P);
-    st = st == S - 1 ? 0 : st + 1;
+    st = 1 - st;
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no DMA outlives the loop
   const auto add_phases = [&](f32x16* x) {
     if (P == 1) return;
     f32x4* const part = (f32x4*)lds + ((phase - 1) * KW + kw) * (ND * 4 * 64);
@@ -838,9 +832,9 @@ lora_status launch_attention_bwd(const attn_shape& sh, const uint16_t* dout, con
   };
   const auto pick = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    a.shift == 7   ? go_k(attention_dkv_kernel<D, 8, 4, 2>, 8)
-    : a.shift == 6 ? go_k(attention_dkv_kernel<D, 8, 2, 2>, 8)
-                   : go_k(attention_dkv_kernel<D, D == 64 ? 8 : 4, 1, 2>, D == 64 ? 8 : 4);
+    a.shift == 7   ? go_k(attention_dkv_kernel<D, 8, 4>, 8)
+    : a.shift == 6 ? go_k(attention_dkv_kernel<D, 8, 2>, 8)
+                   : go_k(attention_dkv_kernel<D, D == 64 ? 8 : 4, 1>, D == 64 ? 8 : 4);
   };
   if (sh.head_dim == 128) pick(std::integral_constant<int, 128>{});
   else pick(std::integral_constant<int, 64>{});
