@@ -738,7 +738,9 @@ typedef struct {        /* host struct */
  *   slots       int32 [n_slots] out  each new row's slot, in the packed order; -1 behind
  *                               the last one
  *   positions, token_seqs int32 [n_slots] out, nullable  each new row's position and
- *                               request (an adapter id's index); -1 behind the last one
+ *                               request (an adapter id's index); -1 behind the last one.
+ *                               Rows of a request whose lengths are negative or do not fit
+ *                               max_pages have position -1, too
  * A request is served, or left out whole: its seq_len then stays the cached one, its
  * slots are -1, it takes no page, and a bit of the status word says why:
  *   LORA_FLAG_NO_PAGES    it needs pages, and the pages that it and the requests before

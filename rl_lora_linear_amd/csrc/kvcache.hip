@@ -161,7 +161,7 @@ __global__ __launch_bounds__(TAB_THREADS) void kv_tables_kernel(TableArgs a) {
       if (t < n_rows) {
         seq = last_at_most(rows_at, 0, a.n - 1, (int32_t)t);
         const Request r = request_of(a, seq);
-        pos = r.cached + (int32_t)t - rows_at[seq];
+        if (!r.bad) pos = r.cached + (int32_t)t - rows_at[seq];
         if (take_at[seq] >= 0) {
           const int32_t p = pos >> a.page_shift;
           const int32_t page = p < r.owned ? a.table[(int64_t)seq * a.max_pages + p]

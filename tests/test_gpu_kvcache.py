@@ -126,6 +126,22 @@ def test_tables_refuse_bad_requests_alone(n_slots):
     assert torch.equal(t.d["table"], before["table"]) and torch.equal(t.d["ring"], before["ring"]) and torch.equal(t.d["state"], before["state"])
 
 
+@pytest.mark.parametrize("n_slots", [64, 6000])
+def test_tables_no_positions_where_lengths_break_the_rules(n_slots):
+    """Rows of a request with a negative length, or of more rows than its table holds, have no position: -1, as behind the last row."""
+    t = Tables(6, 16, 50, 2, n_slots, seed=5)
+    t.step([4, 4, 4, 4, 4, 4])
+    t.d["lens"][1], t.d["lens"][3], t.d["lens"][4] = -3, 30, 2 ** 31 - 1
+    t.call([2, 3, 1, 3, 5, 2])      # request 3 would end at row 33 of 32
+    assert L.lora_device_status(t.ws) == L.FLAG_BAD_LENGTH
+    assert t.d["positions"].tolist()[:16] == [4, 5, -1, -1, -1, 4, -1, -1, -1, -1, -1, -1, -1, -1, 4, 5]
+    assert t.d["token_seqs"].tolist()[:16] == [0, 0, 1, 1, 1, 2, 3, 3, 3, 4, 4, 4, 4, 4, 5, 5]
+    page = [t.d["table"][b, 0].item() * 16 for b in range(6)]
+    assert t.d["slots"].tolist()[:16] == [page[0] + 4, page[0] + 5, -1, -1, -1, page[2] + 4] + [-1] * 8 + [page[5] + 4, page[5] + 5]
+    for k in ("slots", "positions", "token_seqs"):
+        assert t.d[k].tolist()[16:] == [-1] * (n_slots - 16), k
+
+
 def test_tables_bad_ring():
     for state in ([5, 4], [-1, 3], [0, 51], [2 ** 62, -2 ** 62]):
         t = Tables(2, 16, 50, 4, 64)
