@@ -649,7 +649,8 @@ lora_status adam_step_clipped(const grad_shape* shape, const grad_tensor* table,
  *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),
  *   o_i = bf16(sum_j exp(s_ij - lse_i) v_j).
  * A query that sees no key (Lk < Lq, Lk = 0) has o = 0 and lse = -inf.  Products and
- * sums are fp32; the weights exp(.) enter the second product as bf16.  A sequence's
+ * sums are fp32; the weights exp(.) enter the second product as bf16.  Scores may be up to
+ * 2^30 in magnitude (past it o may be 0 or NaN).  A sequence's
  * o and lse have the same bits whatever else the batch holds, and depend on nothing
  * outside its rows; with causal, the bits of o_i and lse_i depend on keys that query i
  * sees only, also where others hold NaN or Inf. */
@@ -691,7 +692,8 @@ lora_status attention_forward(const attn_shape* shape, const uint16_t* q, const 
  *   dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
  * over the heads of j's group too; each sum in fp32, in an order fixed by the call's
  * sizes (bitwise repeatable; dq's by its own sequence alone), p and ds entering the
- * products as bf16, rounded to bf16 once at the end.
+ * products as bf16, rounded to bf16 once at the end.  lse is an fp32 number: p is off by a
+ * factor of 1 +- 2^-21 |lse| or less, which counts from scores of thousands on.
  *   dout as o; dq, dk, dv bf16 out with the strides of q, k, v (so they may be slices of
  *   one buffer); none may overlap an input.  Rows that belong to no sequence are left as
  *   they were.  A NaN or Inf of a sequence may reach all gradients of that sequence, and
@@ -795,8 +797,8 @@ lora_status kv_write(const kv_shape* shape, int64_t n, const uint16_t* k, int64_
  *   lse  fp32 [n_seqs][n_heads] out, nullable
  * Products and sums are fp32, the weights exp(.) enter the second product as bf16; keys
  * and values in 8 bits enter as bf16, as the 8-bit x of w4_linear does: exactly for scale
- * bytes from 3 on and magnitudes under 2^128 (scale bytes 0 and 255 are not used).  What a page holds behind a
- * request's last row is never used.  The
+ * bytes from 3 on and magnitudes under 2^128 (scale bytes 0 and 255 are not used).  Scores
+ * may be up to 2^30 in magnitude.  What a page holds behind a request's last row is never used.  The
  * length is split and joined by rules on the request's own length: its results have the
  * same bits in every batch.  n_heads a multiple of n_kv_heads, <= 1024.
  * Workspace: attention_decode_workspace_bytes(shape, n_heads, max_len), enough for smaller

@@ -223,6 +223,38 @@ def test_many_short_sequences():
     Case(rng.integers(0, 9, 300).tolist(), heads=2, kv=1, d=64, seed=10).check()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,heads,kv,d", [(24, 4, 1, 64), (25, 2, 2, 128), (40, 8, 2, 64), (150, 8, 2, 64), (150, 4, 1, 128)])
+def test_many_sequences_behind_earlier_keys(n, heads, kv, d, causal):
+    """More and fewer sequences than are sorted, blocks of 32 rows of four heads among them, with keys in front of the
+    queries, fewer keys than queries, none of either, and rows of neither side's sequences at both ends."""
+    rng = np.random.default_rng(n + heads)
+    lq = rng.integers(1, 20, n)
+    lk = lq + rng.integers(-6, 30, n).clip(-lq)
+    lq[3], lk[5], lq[n - 2] = 0, 0, 90
+    lq[7], lk[7] = 75, 200
+    c = Case(lq.tolist(), lk.tolist(), heads=heads, kv=kv, d=d, causal=causal, seed=n, front=9, behind=70)
+    got = c.check()
+    again = c.backward()
+    assert all(np.array_equal(a, b, equal_nan=True) for a, b in zip(got[2:], again))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 28])
+def test_scores_of_any_documented_size(size, d):
+    """Scores up to 2^28, those of a row 2^-7 of it apart and growing: the last key that a query sees has all the
+    weight, so o is its value but for the roundings of p and o (2 u), and lse its score."""
+    c = Case([120, 1], heads=2, kv=1, d=d, scale=1.0, seed=31)
+    c.q[:], c.k[:] = 0, 0
+    c.q[:, :, 3], c.k[:, 0, 3] = size, np.arange(c.m) / 128.0
+    c.upload()
+    o, lse = c.forward()
+    last = np.arange(c.m)
+    assert np.all(np.abs(o - c.v[last]) <= 2 * U * (1 + U) * np.abs(c.v[last]))
+    assert np.all(np.abs(lse - size * last / 128.0) <= 8 * E * size * last / 128.0 + 8 * E)
+    assert L.lora_device_status(c.ws) == 0
+
+
 @pytest.mark.parametrize("scale", [0.0, 4.0, -1.0])
 def test_scales(scale):
     """All weights alike; one weight of nearly 1 (scores of +-100 and more); a negative scale."""

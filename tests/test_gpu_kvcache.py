@@ -361,6 +361,26 @@ def test_decode_peaked_and_flat(x8):
     Decode([400, 90], d=128, x8=x8, scale=-0.5, seed=3).check()
 
 
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 28])
+def test_decode_scores_of_any_documented_size(size):
+    """As in attention over prompts: growing scores up to 2^28, so the last key has all the weight."""
+    lens = [1, 40, 128, 77]
+    c = Decode(lens, heads=2, kv=1, d=64, scale=1.0, seed=12)
+    q = np.zeros(c.q.shape)
+    q[:, :, 3] = size
+    c.dq = put(q)
+    k = np.zeros(c.rows[0].shape)
+    k[:, 0, 3] = np.concatenate([np.arange(n) / 128.0 for n in lens])
+    page_at, row_at = (torch.from_numpy(a).cuda() for a in (c.slots // c.page, c.slots % c.page))
+    c.c[0][page_at, :, row_at] = put(k)
+    o, lse = c.run()
+    assert L.lora_device_status(c.ws) == 0
+    for b, n in enumerate(lens):
+        v, s = c.rows[1][c.cu[b + 1] - 1, 0], size * (n - 1) / 128.0
+        assert np.all(np.abs(o[b] - v) <= 2 * U * (1 + U) * np.abs(v)), b
+        assert np.all(np.abs(lse[b] - s) <= 8 * E * s + 8 * E), b
+
+
 @pytest.mark.parametrize("x8", [False, True])
 def test_decode_same_bits_in_every_batch(x8):
     lens = [300, 1, 2000, 129, 4500]
