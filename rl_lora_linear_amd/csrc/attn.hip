@@ -298,13 +298,15 @@ __device__ __forceinline__ f32x16 product_seen(bf16x8 v, bf16x8 p, f32x16 acc, i
 // only when that has passed it by 2^6: they stay below 2^6, exact as any float, and the
 // output is hardly ever rescaled.
 // Bound by the matrix units and the clock that their power leaves: 16384 tokens, 32 heads of
-// 128 over 8, causal (2.2 TFLOP): 1.93-2.08 ms, 1.06-1.14 PFLOP/s, the units busy in 59 % of
+// 128 over 8, causal (2.2 TFLOP): 1.96-2.08 ms, 1.06-1.12 PFLOP/s, the units busy in 59 % of
 // the cycles at 1.9 GHz (a large library matrix product: 1.37 PFLOP/s).  LDS is read
 // without conflicts and for a third of the cycles; 0.43 GB come from memory, 0.20 of
 // them the operands once.  Tried without gain: wave priorities around the products (the same), two
 // groups of waves half a tile apart (2088 against 1980 us).
-// Short prompts pay for the masked halves of their last tiles and for a block's start
-// (offsets, q, first tile: three round trips): 8192 tokens of 16, 98-104 us for 59.5 GFLOP.
+// Short prompts pay for a block's start (offsets, q, first tile: three round trips, in about
+// four rounds of blocks) and for the tiles behind the last pair of whole ones, whose v is looked
+// through before it is used (a fifth of the tiles; the masked halves are a tenth of the work):
+// 8192 tokens of 16, 98-101 us for 59.5 GFLOP.
 constexpr float AT_SLACK = 6.f;
 
 template <int D, int NW>
@@ -460,8 +462,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 
 // ---------------------------------------------------------------- dq
 // Waves, tiles and stages as in the forward, three products a tile in place of two.  8192
-// tokens of 6, 32 heads of 128 over 8 (11.3 M pairs a head): 280-288 us, 0.96-0.98 PFLOP/s;
-// the matrix units are busy in 54 % of the cycles.
+// tokens of 6, 32 heads of 128 over 8 (11.3 M pairs a head), in blocks of four heads by 32
+// rows: 287-294 us, 0.94-0.96 PFLOP/s; the matrix units are busy in 55 % of the cycles.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void attention_dq_kernel(AttnArgs a) {
   constexpr int ND = D / 32, NK = D / 16;
@@ -587,7 +589,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // phase has two LDS stages of its own, filled by its own waves, the DMA a tile ahead.  At the
 // end the phases' sums are added in order, through LDS.
 // Four products a tile, two waves on a SIMD (256 registers each: the two sums alone are 128).
-// 8192 tokens of 6 as above: 420-490 us, 0.75-0.87 PFLOP/s, the matrix units busy in 40 % of
+// 8192 tokens of 6 as above: 420-490 us, 0.75-0.87 PFLOP/s, the matrix units busy in 41 % of
 // the cycles: the waves of a block go in step from tile to tile, and the longest block holds
 // the end up (a block's work goes from 4020 queries of four heads down to 64).  Phases of a
 // single wave need no barrier (2048 tokens 183 -> 173 us).

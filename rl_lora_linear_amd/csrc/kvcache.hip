@@ -18,8 +18,8 @@ constexpr float KV_LOG2E = 1.4426950408889634f, KV_LN2 = 0.6931471805599453f;
 // they do (seq_lens over cached_lens, the state over itself) no block of a grid may see
 // them changed, so a second launch of one block writes them.
 // Bound by the chain of a launch, the lengths' loads, the scan's barriers and the dependent
-// loads of an item (its request, its page): 64 requests 6.9 us, 1000 requests with 104 000
-// new rows 9.9 us (1.3 MB; 15.7 as two launches).  Scans kept in memory between launches, or
+// loads of an item (its request, its page): 64 requests 6.7-7.0 us, 1000 requests with 104 000
+// new rows 9.5-9.8 us (1.3 MB; 15.7 as two launches).  Scans kept in memory between launches, or
 // one block that hands them to others, would wait for a launch or a flag instead.
 constexpr int TAB_THREADS = 1024;
 
@@ -285,8 +285,8 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
 // Scores, weights' sums and outputs are fp32; the weights are rounded to bf16 to be an operand
 // (half a step, 2^-8 of a weight), and the output once at the end.
 // Bound by memory where the batch is large: 64 requests of 2500 to 8000 tokens, 8 key heads of
-// 128 in bf16 (1.37 GB): 246-253 us and 5 to join, 5.4 TB/s, the rate of a large copy.  In 8
-// bits, 250 requests of 900 to 3000, 4 key heads (0.51 GB): 106-110 us and 5, 4.7 TB/s: the
+// 128 in bf16 (1.37 GB): 237-250 us and 5 to join, 5.5-5.8 TB/s, the rate of a large copy.  In 8
+// bits, 250 requests of 900 to 3000, 4 key heads (0.51 GB): 101-107 us and 5, 4.8-5 TB/s: the
 // conversion of two codes at a time and the V tile's way through LDS take turns with the
 // loads of 12 waves.  One request of 4001: 7.0-7.4 us and 2.6-3.5, each a launch and a chain of
 // three loads (length, page, rows).  Asking two tiles ahead, and loads past the caches, were
