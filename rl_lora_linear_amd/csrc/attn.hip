@@ -823,6 +823,8 @@ lora_status launch_attention_bwd(const attn_shape& sh, const uint16_t* dout, con
   //   4096 tokens, 8 key heads (264)              622 /  476 /  573
   //   4096 tokens of 8, 4 key heads (160)         390 /  256 /  189
   //   2048 tokens, 8 key heads (136)              297 /  207 /  173
+  // (Each sequence counts for a block, so batches of many short ones take 128 keys, of which their
+  // last blocks own few: 8192 tokens of 100, 227 us, and the other sizes are not measured there.)
   // With 32 keys a wave is a phase by itself; eight of them, where LDS has room for their
   // stages (heads of 64), make the block half as long as four (5000 tokens, 4 key heads:
   // 294 -> 246 us; 200 tokens: 16.4 -> 17.8).
